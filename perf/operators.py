@@ -249,9 +249,8 @@ def _run_own(s):
         xcodes, xscales = nf4.mx_pack(s["x"], check=False)
         return nf4.mx_gemm_packed(s["codes"], s["scales"], xcodes, xscales)
     if kind == "route":
-        k = s["k"]
         offsets, order, place = nf4.moe_sort(s["experts"], s["e"])
-        rows = nf4.moe_gather(s["x"], order, k)
+        rows = nf4.moe_gather(s["x"], place)
         out = nf4.moe_combine(s["y"], place, s["weights"])
         if not s["train"]:
             return offsets, order, place, rows, out
