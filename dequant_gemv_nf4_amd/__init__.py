@@ -41,4 +41,27 @@ from ._lib import (  # noqa: F401
     smallm_workspace_bytes,
     unpack,
     workspace_for,
+    MOE_BAD_ID,
+    MOE_MAX_E,
+    MX_BLOCK,
+    moe_combine,
+    moe_combine_grad,
+    moe_gather,
+    moe_sort,
+    mx_gemm,
+    mx_gemm_grouped,
+    mx_gemm_grouped_grad,
+    mx_gemm_packed,
+    mx_pack,
+    mx_unpack,
+    nf4_moe_combine,
+    nf4_moe_combine_grad,
+    nf4_moe_gather,
+    nf4_moe_sort,
+    nf4_mx_gemm,
+    nf4_mx_gemm_grouped,
+    nf4_mx_gemm_grouped_grad,
+    nf4_mx_gemm_packed,
+    nf4_mx_pack,
+    nf4_mx_unpack,
 )

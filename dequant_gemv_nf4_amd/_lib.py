@@ -15,6 +15,9 @@ MAX_K = 32768
 PACK_NONFINITE = 1
 PACK_SCALE_OVERFLOW = 2
 EMBED_BAD_ID = 1
+MX_BLOCK = 32
+MOE_MAX_E = 512
+MOE_BAD_ID = 1
 
 _STATUS = {0: "NF4_OK", -1: "NF4_EINVAL", -2: "NF4_EALIGN", -3: "NF4_ERANGE",
            -4: "NF4_EDEVICE", -5: "NF4_ELAUNCH"}
@@ -62,6 +65,21 @@ def _load():
     L.nf4_ring_destroy.argtypes = [vp]
     L.nf4_ring_slot_bytes.argtypes = [i64, i64]
     L.nf4_ring_slot_bytes.restype = ctypes.c_int64
+    ci = ctypes.c_int
+    L.nf4_mx_pack.argtypes = [vp, ci, i64, i64, vp, vp, vp, vp]
+    L.nf4_mx_unpack.argtypes = [vp, vp, i64, i64, vp, ci, vp]
+    L.nf4_mx_gemm.argtypes = [vp, vp, i64, i64, vp, i64, vp, ci, vp]
+    L.nf4_mx_gemm_packed.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, ci, vp]
+    L.nf4_mx_gemm_grouped.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, vp, ci, vp]
+    L.nf4_mx_gemm_grouped_grad.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, vp, ci, vp]
+    L.nf4_moe_sort.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp]
+    L.nf4_moe_gather.argtypes = [vp, ci, vp, i64, i64, i64, vp, vp]
+    L.nf4_moe_combine.argtypes = [vp, ci, vp, vp, i64, i64, i64, vp, vp]
+    L.nf4_moe_combine_grad.argtypes = [vp, vp, ci, vp, vp, i64, i64, i64, vp, vp, vp]
+    for f in (L.nf4_mx_pack, L.nf4_mx_unpack, L.nf4_mx_gemm, L.nf4_mx_gemm_packed,
+              L.nf4_mx_gemm_grouped, L.nf4_mx_gemm_grouped_grad, L.nf4_moe_sort,
+              L.nf4_moe_gather, L.nf4_moe_combine, L.nf4_moe_combine_grad):
+        f.restype = ci
     for f in (L.nf4_ring_create, L.nf4_ring_gemm, L.nf4_ring_destroy):
         f.restype = ctypes.c_int
     for f in (L.nf4_pack, L.nf4_unpack, L.nf4_gemv, L.nf4_gemm_smallm, L.nf4_gemm_smallm_ws,
@@ -442,3 +460,289 @@ def gemm(codes, scales, X, stream=None):
         else:
             nf4_gemm_prefill(codes, scales, X, Y, stream)
     return Y
+
+
+# ---- MXFP4 and experts ----
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+_FLOATS = tuple(_DTYPE)
+
+
+def _same_device(*named):
+    """The tensors (name, tensor or None) of one call live on one device."""
+    first = None
+    for name, t in named:
+        if t is None:
+            continue
+        if first is None:
+            first = (name, t.device)
+        elif t.device != first[1]:
+            raise ValueError(f"{name} is on {t.device}, {first[0]} on {first[1]}")
+
+
+def _mx_matrix(codes, scales, what="codes", lead=0):
+    """(lead sizes..., N, K) of a packed MXFP4 matrix (stack of matrices: lead = 1)."""
+    _need(codes, what, (torch.uint8,), (2 + lead,))
+    _need(scales, what.replace("codes", "scales"), (torch.uint8,), (2 + lead,))
+    K = 2 * codes.shape[-1]
+    if tuple(scales.shape) != tuple(codes.shape[:-1]) + (K // MX_BLOCK,) or K % MX_BLOCK:
+        raise ValueError(f"{what} {tuple(codes.shape)} needs scales of shape "
+                         f"[..., K/{MX_BLOCK}] with K = 2 * {codes.shape[-1]}, "
+                         f"got {tuple(scales.shape)}")
+    return tuple(codes.shape[:-1]) + (K,)
+
+
+def nf4_mx_pack(W, codes, scales, dev_status=None, stream=None):
+    """Quantise W [N][K] (fp32 or bf16) into MXFP4 codes uint8 [N][K/2] and scales
+    uint8 [N][K/32]."""
+    _need(W, "W", _FLOATS, (2,))
+    if _mx_matrix(codes, scales) != tuple(W.shape):
+        raise ValueError(f"codes must be [N][K/2] for W {tuple(W.shape)}")
+    if dev_status is not None:
+        _need(dev_status, "dev_status", (torch.int32,))
+    _same_device(("W", W), ("codes", codes), ("scales", scales), ("dev_status", dev_status))
+    with torch.cuda.device(W.device):
+        _check("nf4_mx_pack", _load().nf4_mx_pack(
+            _ptr(W), _DTYPE[W.dtype], W.shape[0], W.shape[1], _ptr(codes), _ptr(scales),
+            _ptr(dev_status), _stream(W.device, stream)))
+
+
+def nf4_mx_unpack(codes, scales, W_out, stream=None):
+    """W_out [N][K] (fp32 or bf16) = the values of a packed MXFP4 matrix."""
+    _need(W_out, "W_out", _FLOATS, (2,))
+    if _mx_matrix(codes, scales) != tuple(W_out.shape):
+        raise ValueError(f"W_out must be [N][K], has {tuple(W_out.shape)}")
+    _same_device(("codes", codes), ("scales", scales), ("W_out", W_out))
+    with torch.cuda.device(W_out.device):
+        _check("nf4_mx_unpack", _load().nf4_mx_unpack(
+            _ptr(codes), _ptr(scales), W_out.shape[0], W_out.shape[1], _ptr(W_out),
+            _DTYPE[W_out.dtype], _stream(W_out.device, stream)))
+
+
+def nf4_mx_gemm(codes, scales, X, Y, stream=None):
+    """Y [M][N] (fp32 or bf16) = X . dequant(codes, scales)^T, X bf16 [M][K], any M >= 1."""
+    N, K = _mx_matrix(codes, scales)
+    _need(X, "X", _BF16, (1, 2))
+    _need(Y, "Y", _FLOATS)
+    M = 1 if X.dim() == 1 else X.shape[0]
+    if X.shape[-1] != K:
+        raise ValueError(f"X has {X.shape[-1]} columns, the matrix K = {K}")
+    if Y.numel() != M * N:
+        raise ValueError("Y must have M*N elements")
+    _same_device(("X", X), ("codes", codes), ("scales", scales), ("Y", Y))
+    with torch.cuda.device(X.device):
+        _check("nf4_mx_gemm", _load().nf4_mx_gemm(
+            _ptr(codes), _ptr(scales), N, K, _ptr(X), M, _ptr(Y), _DTYPE[Y.dtype],
+            _stream(X.device, stream)))
+
+
+def nf4_mx_gemm_packed(codes, scales, xcodes, xscales, Y, stream=None):
+    """Y [M][N] (fp32 or bf16) = dequant(xcodes, xscales) . dequant(codes, scales)^T."""
+    N, K = _mx_matrix(codes, scales)
+    M, KX = _mx_matrix(xcodes, xscales, "xcodes")
+    _need(Y, "Y", _FLOATS)
+    if KX != K:
+        raise ValueError(f"xcodes has K = {KX}, codes K = {K}")
+    if Y.numel() != M * N:
+        raise ValueError("Y must have M*N elements")
+    _same_device(("codes", codes), ("scales", scales), ("xcodes", xcodes), ("xscales", xscales),
+                 ("Y", Y))
+    with torch.cuda.device(codes.device):
+        _check("nf4_mx_gemm_packed", _load().nf4_mx_gemm_packed(
+            _ptr(codes), _ptr(scales), N, K, _ptr(xcodes), _ptr(xscales), M, _ptr(Y),
+            _DTYPE[Y.dtype], _stream(codes.device, stream)))
+
+
+def _grouped(func, codes, scales, rows, name, width, offsets, out, out_name, out_width, stream):
+    E, N, K = _mx_matrix(codes, scales, lead=1)
+    sizes = {"N": N, "K": K}
+    _need(rows, name, _BF16, (2,))
+    _need(offsets, "offsets", (torch.int32,), (1,))
+    _need(out, out_name, _FLOATS, (2,))
+    R = rows.shape[0]
+    if rows.shape[1] != sizes[width]:
+        raise ValueError(f"{name} must be [R][{width}={sizes[width]}]")
+    if tuple(out.shape) != (R, sizes[out_width]):
+        raise ValueError(f"{out_name} must be [R={R}][{out_width}={sizes[out_width]}]")
+    if offsets.numel() != E + 1:
+        raise ValueError(f"offsets must have E + 1 = {E + 1} entries")
+    _same_device((name, rows), ("codes", codes), ("scales", scales), ("offsets", offsets),
+                 (out_name, out))
+    with torch.cuda.device(rows.device):
+        _check(func, getattr(_load(), func)(
+            _ptr(codes), _ptr(scales), E, N, K, _ptr(rows), _ptr(offsets), R, _ptr(out),
+            _DTYPE[out.dtype], _stream(rows.device, stream)))
+
+
+def nf4_mx_gemm_grouped(codes, scales, X, offsets, Y, stream=None):
+    """Y [R][N] (fp32 or bf16): rows offsets[e] .. offsets[e+1]-1 of X bf16 [R][K]
+    times expert e's packed matrix, codes [E][N][K/2], scales [E][N][K/32]; rows from
+    offsets[E] on are zero.  offsets: int32 [E+1] on the device."""
+    _grouped("nf4_mx_gemm_grouped", codes, scales, X, "X", "K", offsets, Y, "Y", "N", stream)
+
+
+def nf4_mx_gemm_grouped_grad(codes, scales, dY, offsets, dX, stream=None):
+    """dX [R][K] (fp32 or bf16): the gradient of nf4_mx_gemm_grouped in its rows,
+    from dY bf16 [R][N], N % 8 == 0."""
+    _grouped("nf4_mx_gemm_grouped_grad", codes, scales, dY, "dY", "N", offsets, dX, "dX", "K",
+             stream)
+
+
+def nf4_moe_sort(experts, num_experts, offsets, order, place, dev_status=None, stream=None):
+    """Sort the slots of experts (int64 [T][topk], -1: none) by expert: offsets int32
+    [E+1], order int32 [T*topk] (slot of each row), place int32 [T][topk] (row of
+    each slot; ~ marks slots without an expert, which come last)."""
+    _need(experts, "experts", (torch.int64,), (2,))
+    _need(offsets, "offsets", (torch.int32,), (1,))
+    _need(order, "order", (torch.int32,), (1,))
+    _need(place, "place", (torch.int32,), (2,))
+    T, topk = experts.shape
+    if offsets.numel() != num_experts + 1:
+        raise ValueError(f"offsets must have E + 1 = {num_experts + 1} entries")
+    if order.numel() != T * topk or tuple(place.shape) != (T, topk):
+        raise ValueError(f"order must have {T * topk} entries and place the shape of experts")
+    if dev_status is not None:
+        _need(dev_status, "dev_status", (torch.int32,))
+    _same_device(("experts", experts), ("offsets", offsets), ("order", order), ("place", place),
+                 ("dev_status", dev_status))
+    with torch.cuda.device(experts.device):
+        _check("nf4_moe_sort", _load().nf4_moe_sort(
+            _ptr(experts), T, topk, int(num_experts), _ptr(offsets), _ptr(order), _ptr(place),
+            _ptr(dev_status), _stream(experts.device, stream)))
+
+
+def _rows(place, tokens, rows, weights=None):
+    """(T, topk, H) of a row operator; tokens and rows are (name, tensor) pairs of
+    one dtype, [T][H] and [T*topk][H]."""
+    _need(place, "place", (torch.int32,), (2,))
+    T, topk = place.shape
+    H = tokens[0][1].shape[-1]
+    for n, (name, t) in [(T, x) for x in tokens] + [(T * topk, x) for x in rows]:
+        _need(t, name, _FLOATS, (2,))
+        if tuple(t.shape) != (n, H):
+            raise ValueError(f"{name} must be [{n}][{H}], has {tuple(t.shape)}")
+        if t.dtype != tokens[0][1].dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, {tokens[0][0]} {tokens[0][1].dtype}")
+    for name, t in weights or ():
+        if t is not None:
+            _need(t, name, (torch.float32,), (2,))
+            if t.shape != place.shape:
+                raise ValueError(f"{name} must have the shape of place")
+    _same_device(("place", place), *tokens, *rows, *(weights or ()))
+    return T, topk, H
+
+
+def nf4_moe_gather(X, place, out, stream=None):
+    """out [T*topk][H]: row place[t][j] = X[t], zeros for slots without an expert."""
+    T, topk, H = _rows(place, [("X", X)], [("out", out)])
+    with torch.cuda.device(X.device):
+        _check("nf4_moe_gather", _load().nf4_moe_gather(
+            _ptr(X), _DTYPE[X.dtype], _ptr(place), T, topk, H, _ptr(out),
+            _stream(X.device, stream)))
+
+
+def nf4_moe_combine(Y, place, weights, out, stream=None):
+    """out [T][H] = sum_j weights[t][j] * Y[place[t][j]] (weights None: plain sum)."""
+    T, topk, H = _rows(place, [("out", out)], [("Y", Y)], [("weights", weights)])
+    with torch.cuda.device(Y.device):
+        _check("nf4_moe_combine", _load().nf4_moe_combine(
+            _ptr(Y), _DTYPE[Y.dtype], _ptr(place), _ptr(weights), T, topk, H, _ptr(out),
+            _stream(Y.device, stream)))
+
+
+def nf4_moe_combine_grad(dOut, Y, place, weights, dY, dweights, stream=None):
+    """dY [T*topk][H] and dweights fp32 [T][topk] of nf4_moe_combine from dOut [T][H]."""
+    T, topk, H = _rows(place, [("dOut", dOut)], [("Y", Y), ("dY", dY)],
+                       [("weights", weights), ("dweights", dweights)])
+    if weights is None or dweights is None:
+        raise TypeError("weights and dweights must be torch.Tensors")
+    with torch.cuda.device(Y.device):
+        _check("nf4_moe_combine_grad", _load().nf4_moe_combine_grad(
+            _ptr(dOut), _ptr(Y), _DTYPE[Y.dtype], _ptr(place), _ptr(weights), T, topk, H,
+            _ptr(dY), _ptr(dweights), _stream(Y.device, stream)))
+
+
+def mx_pack(W, stream=None, check=True):
+    """Allocate and fill MXFP4 (codes, scales) for W; with check=True raise on blocks
+    that hold NaN or infinity (a host synchronisation)."""
+    _need(W, "W", _FLOATS, (2,))
+    N, K = W.shape
+    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+    scales = torch.empty((N, K // MX_BLOCK), dtype=torch.uint8, device=W.device)
+    status = torch.empty(1, dtype=torch.int32, device=W.device) if check else None
+    nf4_mx_pack(W, codes, scales, status, stream)
+    if check and _status_on(status, stream):
+        raise ValueError(f"nf4_mx_pack flagged blocks: status bits {int(status.item()):#x}")
+    return codes, scales
+
+
+def _status_on(status, stream):
+    """The status word's value, read after the call on `stream`."""
+    if stream is None:
+        return int(status.item())
+    handle = _stream(status.device, stream).value
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=status.device)):
+        return int(status.item())
+
+
+def mx_unpack(codes, scales, dtype=torch.float32, stream=None):
+    N, K = _mx_matrix(codes, scales)
+    W = torch.empty((N, K), dtype=dtype, device=codes.device)
+    nf4_mx_unpack(codes, scales, W, stream)
+    return W
+
+
+def mx_gemm(codes, scales, X, out_dtype=torch.float32, stream=None):
+    """Y [M][N] = X . dequant(codes, scales)^T for any M (a vector X: Y [N])."""
+    M = (X.shape[0],) if X.dim() == 2 else ()
+    Y = torch.empty(M + (codes.shape[0],), dtype=out_dtype, device=X.device)
+    nf4_mx_gemm(codes, scales, X, Y, stream)
+    return Y
+
+
+def mx_gemm_packed(codes, scales, xcodes, xscales, out_dtype=torch.float32, stream=None):
+    Y = torch.empty((xcodes.shape[0], codes.shape[0]), dtype=out_dtype, device=codes.device)
+    nf4_mx_gemm_packed(codes, scales, xcodes, xscales, Y, stream)
+    return Y
+
+
+def mx_gemm_grouped(codes, scales, X, offsets, out_dtype=torch.float32, stream=None):
+    Y = torch.empty((X.shape[0], codes.shape[1]), dtype=out_dtype, device=X.device)
+    nf4_mx_gemm_grouped(codes, scales, X, offsets, Y, stream)
+    return Y
+
+
+def mx_gemm_grouped_grad(codes, scales, dY, offsets, out_dtype=torch.float32, stream=None):
+    dX = torch.empty((dY.shape[0], 2 * codes.shape[2]), dtype=out_dtype, device=dY.device)
+    nf4_mx_gemm_grouped_grad(codes, scales, dY, offsets, dX, stream)
+    return dX
+
+
+def moe_sort(experts, num_experts, stream=None):
+    """(offsets, order, place) of experts int64 [T][topk]; see nf4_moe_sort."""
+    _need(experts, "experts", (torch.int64,), (2,))
+    dev = experts.device
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+    order = torch.empty(experts.numel(), dtype=torch.int32, device=dev)
+    place = torch.empty(experts.shape, dtype=torch.int32, device=dev)
+    nf4_moe_sort(experts, num_experts, offsets, order, place, None, stream)
+    return offsets, order, place
+
+
+def moe_gather(X, place, stream=None):
+    out = torch.empty((place.numel(), X.shape[-1]), dtype=X.dtype, device=X.device)
+    nf4_moe_gather(X, place, out, stream)
+    return out
+
+
+def moe_combine(Y, place, weights=None, stream=None):
+    out = torch.empty((place.shape[0], Y.shape[-1]), dtype=Y.dtype, device=Y.device)
+    nf4_moe_combine(Y, place, weights, out, stream)
+    return out
+
+
+def moe_combine_grad(dOut, Y, place, weights, stream=None):
+    """(dY, dweights) of moe_combine."""
+    dY = torch.empty_like(Y)
+    dw = torch.empty(place.shape, dtype=torch.float32, device=Y.device)
+    nf4_moe_combine_grad(dOut, Y, place, weights, dY, dw, stream)
+    return dY, dw

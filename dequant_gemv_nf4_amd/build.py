@@ -20,13 +20,15 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnf4.so")
 SOURCES = ["api.hip", "pack.hip", "gemv.hip", "gemm_mfma.hip", "gemm_prefill.hip", "embed.hip",
-           "ring.hip"]
+           "ring.hip", "mx_pack.hip", "mx_gemm.hip", "mx_packed.hip", "mx_grad.hip", "moe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # what the library is built from (the hash the benchmark line reports)
 HASHED = ["include/nf4.h"] + ["dequant_gemv_nf4_amd/csrc/" + f for f in
                               ("api.hip", "nf4_device.h", "nf4_launch.h", "nf4_split.h",
                                "pack.hip", "gemv.hip", "gemm_mfma.hip", "gemm_prefill.hip",
-                               "embed.hip", "ring.hip")]
+                               "embed.hip", "ring.hip", "nf4_check.h", "mx_device.h",
+                               "mx_pack.hip", "mx_gemm.hip", "mx_packed.hip", "mx_grad.hip",
+                               "moe.hip")]
 BUILD_INFO = os.path.join(HERE, "build_info.json")
 
 

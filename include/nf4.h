@@ -275,6 +275,145 @@ int nf4_ring_gemm(nf4_ring *ring, const uint8_t *host_codes, const uint16_t *hos
 int64_t nf4_ring_slot_bytes(int64_t N, int64_t K);
 int nf4_ring_destroy(nf4_ring *ring);
 
+/* ------------------------------------------------------------------------
+ * MXFP4: a second 4-bit format, the one the matrix cores read as it is stored.
+ * OCP Microscaling Formats specification 1.0: blocks of 32 values along K share
+ * one scale byte s, the power of two 2^(s - 127); a value is an e2m1 code (sign,
+ * magnitude one of 0, .5, 1, 1.5, 2, 3, 4, 6) times it.  s = 255 is NaN: every value
+ * of the block is NaN, in unpacking and in the products.
+ *  - codes  uint8 [N][K/2]   byte j of row n = code(n,2j) | code(n,2j+1) << 4.
+ *  - scales uint8 [N][K/32].
+ *  K is a multiple of 32, at most NF4_MAX_K; N * K / 2 < 2^31 (one matrix).
+ *  dtype arguments: NF4_F32 or NF4_BF16.
+ * The products sum in fp32; the packed values are exact in bf16, so per output
+ *   |Y - Y_exact| <= 2^-24 * (K + 8) * sum_k |X[m][k] v(n,k)|,
+ * plus half a unit of bf16 where the output is bf16, for finite sums.  NaN and
+ * infinities in X or a NaN scale reach the outputs of their row or column only.
+ * Rules of ownership, streams, errors and determinism are those above.
+ */
+#define NF4_MX_BLOCK 32 /* values per scale byte, along K */
+
+enum nf4_dtype { NF4_F32 = 0, NF4_BF16 = 1 };
+
+/*
+ * nf4_mx_pack -- quantise W [N][K] (fp32 or bf16; weights once, or activations in
+ * front of nf4_mx_gemm_packed).  Per block of 32:
+ *   s = max(floor(log2(max |w|)) - 2, -127) + 127   (0 for a block of zeros);
+ *   code = w / 2^(s - 127) rounded to the nearest magnitude, ties to the even
+ *   code, beyond 6 to 6; the sign of w is kept.
+ * A block holding NaN or infinity gets s = 255 and codes 0, and NF4_PACK_NONFINITE
+ * is OR-ed into *dev_status (device int32, may be NULL; if given, the call first
+ * clears it to 0 on the stream).
+ * Alignment: W 16 bytes, codes 4.
+ */
+int nf4_mx_pack(const void *W, int dtype, int64_t N, int64_t K, uint8_t *codes, uint8_t *scales,
+                int32_t *dev_status, void *stream);
+
+/*
+ * nf4_mx_unpack -- the values of a packed matrix, W_out [N][K] in fp32 (exact, up
+ * to overflow to infinity at s > 252) or bf16 (the same values: they fit it).
+ * Alignment: codes 4 bytes, W_out 16.
+ */
+int nf4_mx_unpack(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, void *W_out,
+                  int dtype, void *stream);
+
+/*
+ * nf4_mx_gemm -- Y[m][n] = sum_k X[m][k] * v(n,k), X bf16 [M][K], any M >= 1
+ * (M = 1 is the decode product), Y [M][N] fp32 or bf16 (rounded once).
+ * Alignment: codes, X and Y 16 bytes.  Errors: NF4_ERANGE for M < 1 or M >= 2^26.
+ */
+int nf4_mx_gemm(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K,
+                const uint16_t *X, int64_t M, void *Y, int out_dtype, void *stream);
+
+/*
+ * nf4_mx_gemm_packed -- the product of two packed matrices, Y[m][n] =
+ * sum_k u(m,k) * v(n,k), with u the values of (xcodes, xscales) [M][K], on the
+ * block-scaled matrix instructions.
+ * Alignment: codes, xcodes and Y 16 bytes.  Errors as nf4_mx_gemm.
+ */
+int nf4_mx_gemm_packed(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K,
+                       const uint8_t *xcodes, const uint8_t *xscales, int64_t M, void *Y,
+                       int out_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Experts: tokens sorted by expert, their rows through each expert's packed
+ * matrix, and back.  A slot f = t * topk + j is token t's j-th expert; R = T * topk
+ * slots.  T = 0 is valid everywhere.  T < 2^24, R <= 2^30, topk <= NF4_MOE_MAX_E.
+ */
+#define NF4_MOE_MAX_E 512 /* most experts */
+
+/* bit OR-ed into *dev_status by nf4_moe_sort */
+#define NF4_MOE_BAD_ID 1 /* an expert id that is neither -1 nor in [0, E) */
+
+/*
+ * nf4_moe_sort -- rows in order of expert, slots of one expert in slot order.
+ * experts int64 [T][topk]; an id of -1 (a padded token, a slot over capacity) is a
+ * slot without an expert; any other id outside [0, E) is treated so too and
+ * flagged in *dev_status (may be NULL; if given, cleared first).
+ *  - offsets int32 [E + 1]: expert e has the rows offsets[e] .. offsets[e+1] - 1.
+ *  - order   int32 [R]: the slot of each row; rows offsets[E] .. R - 1 are the slots
+ *            without an expert, in slot order, written as ~slot.
+ *  - place   int32 [T][topk]: the row of each slot, ~row for one without expert.
+ * Slots without an expert have zero rows in nf4_moe_gather and no part in
+ * nf4_moe_combine.
+ */
+int nf4_moe_sort(const int64_t *experts, int64_t T, int64_t topk, int64_t E, int32_t *offsets,
+                 int32_t *order, int32_t *place, int32_t *dev_status, void *stream);
+
+/*
+ * nf4_moe_gather -- out [R][H]: row place[t][j] = X[t], zeros in the rows of slots
+ * without an expert.  X [T][H] and out of one dtype.  Its gradient in X is
+ * nf4_moe_combine of the rows' gradients without weights.
+ * The row operators take any H >= 1 up to 2^20, and are fastest where a row is a
+ * multiple of 16 bytes and the arrays are 16-byte aligned (else the alignment of
+ * an element).  Entries of place beyond [~(R-1), R-1] are skipped.
+ */
+int nf4_moe_gather(const void *X, int dtype, const int32_t *place, int64_t T, int64_t topk,
+                   int64_t H, void *out, void *stream);
+
+/*
+ * nf4_moe_combine -- out[t] = sum_j weights[t][j] * Y[place[t][j]], summed in fp32
+ * in order of j and rounded once; slots without an expert are left out.  weights
+ * fp32 [T][topk], or NULL for a plain sum.  Y [R][H] and out [T][H] of one dtype.
+ */
+int nf4_moe_combine(const void *Y, int dtype, const int32_t *place, const float *weights,
+                    int64_t T, int64_t topk, int64_t H, void *out, void *stream);
+
+/*
+ * nf4_moe_combine_grad -- from dOut [T][H]: dY[place[t][j]] = weights[t][j] *
+ * dOut[t] (zeros in rows without an expert) and dweights[t][j] =
+ * sum_h dOut[t][h] * Y[place[t][j]][h] in fp32 (0 without an expert).
+ * dOut, Y and dY [R][H] of one dtype.
+ */
+int nf4_moe_combine_grad(const void *dOut, const void *Y, int dtype, const int32_t *place,
+                         const float *weights, int64_t T, int64_t topk, int64_t H, void *dY,
+                         float *dweights, void *stream);
+
+/*
+ * nf4_mx_gemm_grouped -- Y[i][n] = sum_k X[i][k] * v_e(n,k) for the rows i =
+ * offsets[e] .. offsets[e+1] - 1 of each expert e: codes [E][N][K/2], scales
+ * [E][N][K/32], X bf16 [R][K] in sorted order, offsets int32 [E + 1] in device
+ * memory (ascending from 0, as nf4_moe_sort writes them; the kernel holds them to
+ * [0, R]), Y [R][N] fp32 or bf16.  Rows from offsets[E] on are written as zero.
+ * Experts without rows cost nothing.  R = 0 is valid.
+ * Alignment: codes, X and Y 16 bytes, offsets 4.  Errors: NF4_ERANGE for
+ * E > NF4_MOE_MAX_E or R >= 2^26, otherwise as nf4_mx_gemm.
+ */
+int nf4_mx_gemm_grouped(const uint8_t *codes, const uint8_t *scales, int64_t E, int64_t N,
+                        int64_t K, const uint16_t *X, const int32_t *offsets, int64_t R, void *Y,
+                        int out_dtype, void *stream);
+
+/*
+ * nf4_mx_gemm_grouped_grad -- the gradient of nf4_mx_gemm_grouped in its rows
+ * (the packed matrices are frozen): dX[i][k] = sum_n dY[i][n] * v_e(n,k), dY bf16
+ * [R][N], dX [R][K] fp32 or bf16, summed in fp32; rows from offsets[E] on are
+ * zero.  N is a multiple of 8 (NF4_EINVAL) and at most 2^23; otherwise as
+ * nf4_mx_gemm_grouped.  Dense: E = 1 and offsets {0, R}.
+ */
+int nf4_mx_gemm_grouped_grad(const uint8_t *codes, const uint8_t *scales, int64_t E, int64_t N,
+                             int64_t K, const uint16_t *dY, const int32_t *offsets, int64_t R,
+                             void *dX, int out_dtype, void *stream);
+
 /* The 16 NF4 levels L[0..15] (fp32) this library decodes with.  Host only. */
 void nf4_codebook(float out[16]);
 

@@ -1,0 +1,397 @@
+"""MXFP4 on the GPU against 64-bit definitions: quantising and unpacking bit for
+bit, the products (bf16 rows, packed rows, grouped by expert and the gradient)
+within the bound of fp32 sums of exact products, over sizes at which tiles, steps
+and blocks end inside; NaN, infinities, extreme scales, streams, graphs."""
+import pytest
+import torch
+
+import gpu_guard
+import mx_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def nf4():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    import dequant_gemv_nf4_amd as m
+    m._lib._load()
+    return m
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def normal(shape, seed, dtype=F32, sigma=1.0):
+    return (sigma * torch.randn(shape, generator=gen(seed), device=DEV)).to(dtype)
+
+
+def packed(shape, seed, lo=118, hi=132):
+    """Random codes and scale bytes of a matrix or a stack of matrices [.., N, K]."""
+    *lead, K = shape
+    codes = torch.randint(0, 256, (*lead, K // 2), generator=gen(seed), device=DEV,
+                          dtype=torch.uint8)
+    scales = torch.randint(lo, hi, (*lead, K // 32), generator=gen(seed + 1), device=DEV,
+                           dtype=torch.uint8)
+    return codes, scales
+
+
+# ------------------------------------------------------ quantise, unpack ----
+def check_pack(nf4, W):
+    N, K = W.shape
+    cb, codes = gpu_guard.alloc((N, K // 2), torch.uint8, DEV)
+    sb, scales = gpu_guard.alloc((N, K // 32), torch.uint8, DEV)
+    status = torch.full((1,), 77, dtype=torch.int32, device=DEV)
+    nf4.nf4_mx_pack(W, codes, scales, status)
+    torch.cuda.synchronize()
+    rc, rs, bad = ref.quantise(W.cpu())
+    assert torch.equal(scales.cpu(), rs)
+    assert torch.equal(codes.cpu(), rc)
+    assert int(status) == (nf4.PACK_NONFINITE if bad else 0)
+    gpu_guard.check(cb, "codes")
+    gpu_guard.check(sb, "scales")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N,K", [(1, 32), (3, 96), (17, 4096), (129, 160), (2, 32768), (700, 2080)])
+def test_pack_bit_exact(nf4, N, K, dtype):
+    check_pack(nf4, normal((N, K), N * 7 + K, dtype, 0.02))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_pack_extremes_and_ties(nf4, dtype):
+    """Blocks of zeros and of -0, subnormals, the largest finite values, the
+    smallest power of two that still scales, and every rounding tie at 12 scales."""
+    rows = [torch.zeros(32), torch.full((32,), -0.0), torch.full((32,), 2.0 ** -133),
+            torch.full((32,), 2.0 ** -126), torch.full((32,), 2.0 ** -125),
+            torch.full((32,), torch.finfo(dtype).max), torch.linspace(-1, 1, 32) * 2.0 ** -130]
+    ties = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0])
+    step = 2.0 ** -7 if dtype == BF else 2.0 ** -23
+    around = torch.cat([ties, ties * (1 + step), ties * (1 - step), -ties])
+    for e in (-126, -125, -100, -20, -3, -1, 0, 1, 7, 60, 100, 124):
+        rows.append(around.double().mul(2.0 ** e).float())
+    check_pack(nf4, torch.stack(rows).to(dtype).to(DEV))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_pack_flags_nonfinite_blocks_only(nf4, dtype, value):
+    W = normal((5, 192), 3, dtype)
+    W[2, 70] = value
+    W[4, 191] = value
+    check_pack(nf4, W)
+    with pytest.raises(ValueError, match="flagged"):
+        nf4.mx_pack(W)
+    codes, scales = nf4.mx_pack(W, check=False)
+    out = nf4.mx_unpack(codes, scales)
+    bad = torch.isnan(out)
+    assert int(bad.sum()) == 64 and bool(bad[2, 64:96].all()) and bool(bad[4, 160:].all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_unpack_every_code_at_every_scale(nf4, dtype):
+    codes = torch.arange(256, dtype=torch.uint8, device=DEV).repeat(256, 1)
+    scales = torch.arange(256, dtype=torch.uint8, device=DEV).reshape(256, 1).repeat(1, 16)
+    buf, out = gpu_guard.alloc((256, 512), dtype, DEV)
+    nf4.nf4_mx_unpack(codes, scales, out)
+    torch.cuda.synchronize()
+    want = ref.values(codes, scales)
+    got = out.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    # beyond the type's range: infinity
+    top = torch.finfo(F32).max
+    want = torch.where(want.abs() > top, torch.sign(want) * float("inf"), want)
+    assert torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+    gpu_guard.check(buf)
+
+
+# ------------------------------------------------------------- products ----
+MS = [1, 2, 15, 16, 17, 33, 64, 65, 129, 300]
+SHAPES = [(1, 32), (15, 64), (17, 96), (100, 1056), (257, 512), (512, 4128), (2048, 384), (36, 14336)]
+
+
+@pytest.mark.parametrize("N,K", SHAPES)
+@pytest.mark.parametrize("M", MS)
+def test_gemm(nf4, M, N, K):
+    codes, scales = packed((N, K), 11 * M + N + K)
+    X = normal((M, K), M + K, BF)
+    want, mag = ref.product(X, ref.values(codes, scales))
+    for dtype in (F32, BF):
+        buf, Y = gpu_guard.alloc((M, N), dtype, DEV)
+        nf4.nf4_mx_gemm(codes, scales, X, Y)
+        torch.cuda.synchronize()
+        gpu_guard.check(buf)
+        ref.close(Y, want, mag, K, f"M={M} N={N} K={K} {dtype}")
+
+
+@pytest.mark.parametrize("N,K", SHAPES)
+@pytest.mark.parametrize("M", MS)
+def test_gemm_packed(nf4, M, N, K):
+    codes, scales = packed((N, K), 13 * M + N + K)
+    xcodes, xscales = packed((M, K), 17 * M + N + K)
+    want, mag = ref.product(ref.values(xcodes, xscales), ref.values(codes, scales))
+    for dtype in (F32, BF):
+        buf, Y = gpu_guard.alloc((M, N), dtype, DEV)
+        nf4.nf4_mx_gemm_packed(codes, scales, xcodes, xscales, Y)
+        torch.cuda.synchronize()
+        gpu_guard.check(buf)
+        ref.close(Y, want, mag, K, f"M={M} N={N} K={K} {dtype}")
+
+
+def test_gemm_of_a_vector_and_of_an_unaligned_scale_view(nf4):
+    codes, scales = packed((100, 256), 5)
+    x = normal((256,), 6, BF)
+    assert nf4.mx_gemm(codes, scales, x).shape == (100,)
+    flat = torch.empty(scales.numel() + 1, dtype=torch.uint8, device=DEV)
+    view = flat[1:].view_as(scales)
+    view.copy_(scales)
+    for M in (1, 40, 200):
+        X = normal((M, 256), M, BF)
+        assert torch.equal(nf4.mx_gemm(codes, view, X), nf4.mx_gemm(codes, scales, X))
+        xc, xs = nf4.mx_pack(X)
+        assert torch.equal(nf4.mx_gemm_packed(codes, view, xc, xs),
+                           nf4.mx_gemm_packed(codes, scales, xc, xs))
+
+
+@pytest.mark.parametrize("M", [3, 40, 150])
+def test_nan_and_infinity_stay_in_their_row_and_column(nf4, M):
+    N, K = 70, 224
+    codes, scales = packed((N, K), 21)
+    scales[33, 2] = 255
+    X = normal((M, K), 22, BF)
+    X[1, 5] = float("nan")
+    X[2, 223] = float("inf")
+    Y = nf4.mx_gemm(codes, scales, X)
+    nan = torch.isnan(Y)
+    assert bool(nan[1].all()) and bool(nan[:, 33].all())
+    rest = torch.ones(M, dtype=torch.bool, device=DEV)
+    rest[1:3] = False
+    clean = Y[rest][:, torch.arange(N, device=DEV) != 33]
+    assert bool(torch.isfinite(clean).all())
+    # an infinite input: +-inf by the weight's sign, NaN at a weight of zero
+    v = ref.values(codes, scales)[:, 223]
+    row = Y[2].double()
+    pos = (v > 0) & ~torch.isnan(ref.values(codes, scales)).any(1)
+    assert bool((row[pos] == float("inf")).all())
+    xc, xs = nf4.mx_pack(X, check=False)
+    P = nf4.mx_gemm_packed(codes, scales, xc, xs)
+    assert bool(torch.isnan(P[1:3]).all()) and bool(torch.isnan(P[:, 33]).all())
+    assert bool(torch.isfinite(P[rest][:, torch.arange(N, device=DEV) != 33]).all())
+
+
+@pytest.mark.parametrize("M", [2, 40, 150])
+def test_extreme_scales(nf4, M):
+    """Weights near the smallest scale times large activations, and the reverse:
+    no product is flushed."""
+    N, K = 40, 128
+    for lo, hi, sx in ((0, 3, 2.0 ** 100), (245, 248, 2.0 ** -100)):
+        codes, scales = packed((N, K), lo + 1, lo, hi)
+        X = normal((M, K), 9, F32).mul(sx).to(BF)
+        want, mag = ref.product(X, ref.values(codes, scales))
+        ref.close(nf4.mx_gemm(codes, scales, X), want, mag, K)
+        off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+        dY = normal((M, N), 10, F32).mul(sx).to(BF)
+        v = ref.values(codes, scales)
+        want, mag = ref.product(dY, v.t())
+        ref.close(nf4.mx_gemm_grouped_grad(codes[None], scales[None], dY, off), want, mag, N)
+
+
+# -------------------------------------------------------------- grouped ----
+def offsets_of(counts):
+    out = [0]
+    for c in counts:
+        out.append(out[-1] + c)
+    return torch.tensor(out, dtype=torch.int32, device=DEV)
+
+
+COUNTS = [([1], 0), ([0, 0, 0], 5), ([3, 0, 1, 0], 0), ([17, 64, 0, 1, 130], 3),
+          ([0] * 70 + [5, 9], 2), ([2] * 130, 0), ([300, 1, 0, 33], 0), ([0, 1000], 17),
+          ([128, 256, 64], 0)]
+
+
+@pytest.mark.parametrize("counts,tail", COUNTS, ids=lambda v: str(v) if isinstance(v, int) else
+                         f"{len(v)}x{sum(v)}")
+@pytest.mark.parametrize("N,K", [(24, 64), (264, 288), (520, 1120)])
+def test_grouped_and_gradient(nf4, counts, tail, N, K):
+    E, R = len(counts), sum(counts) + tail
+    codes, scales = packed((E, N, K), E + R + N)
+    off = offsets_of(counts)
+    X, dY = normal((R, K), 31, BF), normal((R, N), 32, BF)
+    for dtype in (F32, BF):
+        buf, Y = gpu_guard.alloc((R, N), dtype, DEV)
+        nf4.nf4_mx_gemm_grouped(codes, scales, X, off, Y)
+        buf2, dX = gpu_guard.alloc((R, K), dtype, DEV)
+        nf4.nf4_mx_gemm_grouped_grad(codes, scales, dY, off, dX)
+        torch.cuda.synchronize()
+        gpu_guard.check(buf)
+        gpu_guard.check(buf2)
+        a = 0
+        for e, c in enumerate(counts):
+            v = ref.values(codes[e], scales[e])
+            want, mag = ref.product(X[a:a + c], v)
+            ref.close(Y[a:a + c], want, mag, K, f"expert {e}")
+            want, mag = ref.product(dY[a:a + c], v.t())
+            ref.close(dX[a:a + c], want, mag, N, f"gradient of expert {e}")
+            a += c
+        assert not bool(Y[a:].any()) and not bool(dX[a:].any())
+
+
+def test_grouped_without_rows(nf4):
+    codes, scales = packed((3, 32, 64), 1)
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    assert nf4.mx_gemm_grouped(codes, scales, torch.empty((0, 64), dtype=BF, device=DEV),
+                               off).shape == (0, 32)
+    assert nf4.mx_gemm_grouped_grad(codes, scales, torch.empty((0, 32), dtype=BF, device=DEV),
+                                    off).shape == (0, 64)
+
+
+@pytest.mark.parametrize("R", [9, 100])
+def test_grouped_holds_bad_offsets_inside_the_arrays(nf4, R):
+    """Offsets below 0, past R and descending: nothing outside the outputs is
+    written (what is inside is unspecified)."""
+    codes, scales = packed((4, 48, 96), 2)
+    off = torch.tensor([-7, 3, 1 << 30, 2, R + 50], dtype=torch.int32, device=DEV)
+    buf, Y = gpu_guard.alloc((R, 48), F32, DEV)
+    nf4.nf4_mx_gemm_grouped(codes, scales, normal((R, 96), 1, BF), off, Y)
+    buf2, dX = gpu_guard.alloc((R, 96), F32, DEV)
+    nf4.nf4_mx_gemm_grouped_grad(codes, scales, normal((R, 48), 1, BF), off, dX)
+    torch.cuda.synchronize()
+    gpu_guard.check(buf)
+    gpu_guard.check(buf2)
+
+
+@pytest.mark.parametrize("R", [12, 90, 400])
+def test_gradient_is_the_difference_quotient(nf4, R):
+    """Small whole numbers: every sum is exact, so the difference of the forward
+    product along a direction equals the gradient's inner product exactly."""
+    E, N, K = 3, 40, 96
+    g = gen(R)
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=g, device=DEV, dtype=torch.uint8)
+    scales = torch.full((E, N, K // 32), 128, dtype=torch.uint8, device=DEV)  # whole values
+    whole = lambda *s: torch.randint(-3, 4, s, generator=g, device=DEV).to(BF)  # noqa: E731
+    X, V, dY = whole(R, K), whole(R, K), whole(R, N)
+    off = offsets_of([R // 2, 0, R - R // 2])
+    dX = nf4.mx_gemm_grouped_grad(codes, scales, dY, off)
+    up = nf4.mx_gemm_grouped(codes, scales, X + V, off)
+    down = nf4.mx_gemm_grouped(codes, scales, X - V, off)
+    lhs = (dY.double() * (up.double() - down.double())).sum() / 2
+    rhs = (dX.double() * V.double()).sum()
+    assert float(lhs) == float(rhs)
+
+
+def test_stack_beyond_32_bit_offsets(nf4):
+    """The last expert of a stack of more than 4 GiB of codes."""
+    E, N, K = 45, 14336, 14336
+    codes = torch.zeros((E, N, K // 2), dtype=torch.uint8, device=DEV)
+    scales = torch.full((E, N, K // 32), 127, dtype=torch.uint8, device=DEV)
+    assert codes.numel() > 1 << 32
+    c, s = packed((N, K), 77)
+    codes[-1], scales[-1] = c, s
+    v = ref.values(c, s)
+    for R in (5, 70):
+        off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+        off[-1] = R
+        X, dY = normal((R, K), R, BF), normal((R, N), R + 1, BF)
+        want, mag = ref.product(X, v)
+        ref.close(nf4.mx_gemm_grouped(codes, scales, X, off), want, mag, K)
+        want, mag = ref.product(dY, v.t())
+        ref.close(nf4.mx_gemm_grouped_grad(codes, scales, dY, off), want, mag, N)
+
+
+# ------------------------------------------------------ streams, graphs ----
+def test_results_repeat_bit_for_bit(nf4):
+    codes, scales = packed((1000, 2048), 3)
+    for M in (1, 20, 300):
+        X = normal((M, 2048), M, BF)
+        xc, xs = nf4.mx_pack(X)
+        a, b = nf4.mx_gemm(codes, scales, X), nf4.mx_gemm_packed(codes, scales, xc, xs)
+        for _ in range(3):
+            assert torch.equal(nf4.mx_gemm(codes, scales, X), a)
+            assert torch.equal(nf4.mx_gemm_packed(codes, scales, xc, xs), b)
+
+
+def test_on_another_stream(nf4):
+    codes, scales = packed((500, 1024), 3)
+    X = normal((70, 1024), 4, BF)
+    want = nf4.mx_gemm(codes, scales, X)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    W = normal((64, 1024), 8)
+    got = nf4.mx_gemm(codes, scales, X, stream=side)
+    c, s = nf4.mx_pack(W, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+    rc, rs, _ = ref.quantise(W.cpu())
+    assert torch.equal(c.cpu(), rc) and torch.equal(s.cpu(), rs)
+
+
+@pytest.mark.parametrize("M", [1, 30, 200])
+def test_captured_and_replayed_with_new_inputs(nf4, M):
+    N, K = 300, 512
+    codes, scales = packed((N, K), 3)
+    X = normal((M, K), 4, BF)
+    xc = torch.empty((M, K // 2), dtype=torch.uint8, device=DEV)
+    xs = torch.empty((M, K // 32), dtype=torch.uint8, device=DEV)
+    Y, P = torch.empty((M, N), device=DEV), torch.empty((M, N), device=DEV)
+    off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    G = torch.empty((M, N), device=DEV)
+
+    def step():
+        nf4.nf4_mx_gemm(codes, scales, X, Y)
+        nf4.nf4_mx_pack(X, xc, xs)
+        nf4.nf4_mx_gemm_packed(codes, scales, xc, xs, P)
+        nf4.nf4_mx_gemm_grouped(codes[None], scales[None], X, off, G)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(3):
+        X.copy_(normal((M, K), 50 + i, BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = Y.clone(), P.clone(), G.clone()
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (Y, P, G)))
+
+
+def test_arguments_are_refused_by_name(nf4):
+    codes, scales = packed((64, 128), 1)
+    X = normal((4, 128), 1, BF)
+    with pytest.raises(TypeError, match="X has dtype"):
+        nf4.mx_gemm(codes, scales, X.float())
+    with pytest.raises(ValueError, match="contiguous"):
+        nf4.mx_gemm(codes, scales, normal((4, 256), 1, BF)[:, ::2])
+    with pytest.raises(ValueError, match="columns"):
+        nf4.mx_gemm(codes, scales, normal((4, 96), 1, BF))
+    with pytest.raises(ValueError, match="scales"):
+        nf4.mx_gemm(codes, scales[:, :3].contiguous(), X)
+    with pytest.raises(ValueError, match="GPU"):
+        nf4.mx_gemm(codes.cpu(), scales, X)
+    with pytest.raises(TypeError):
+        nf4.mx_gemm(codes, scales, X, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="K ="):
+        xc, xs = nf4.mx_pack(normal((4, 96), 1))
+        nf4.mx_gemm_packed(codes, scales, xc, xs)
+    with pytest.raises(ValueError, match="needs scales"):
+        nf4.mx_pack(normal((4, 80), 1))
+    with pytest.raises(ValueError, match="offsets"):
+        nf4.mx_gemm_grouped(codes[None], scales[None], X,
+                            torch.zeros(3, dtype=torch.int32, device=DEV))
+    with pytest.raises(TypeError, match="offsets"):
+        nf4.mx_gemm_grouped(codes[None], scales[None], X, torch.zeros(2, device=DEV).long())
+    with pytest.raises(nf4.NF4Error):  # N not a multiple of 8
+        c, s = packed((1, 60, 64), 1)
+        nf4.mx_gemm_grouped_grad(c, s, normal((4, 60), 1, BF),
+                                 torch.zeros(2, dtype=torch.int32, device=DEV))
+    with pytest.raises(nf4.NF4Error):  # X not 16-byte aligned
+        flat = torch.zeros(4 * 128 + 1, dtype=BF, device=DEV)
+        nf4.mx_gemm(codes, scales, flat[1:].view(4, 128))
