@@ -108,7 +108,34 @@ def _stream(device, stream):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _run(func, tensors, args, stream):
+    """Call func(*args, stream) of the library on the tensors' device: `stream`, or that
+    device's current one.  Small calls take less time than their marshalling, so
+    the device is switched only where it is another one, and pointers and the
+    stream go over as plain integers."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{func}: tensors on different devices: " + ", ".join(
+                str(t.device) for t in tensors if t is not None))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    f = getattr(_lib or _load(), func)
+    if torch.cuda.current_device() == index:
+        status = f(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = f(*args, stream)
+    if status:
+        _check(func, status)
+
+
 def _need(t, name, dtypes, ndim=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and (ndim is None or t.dim() in ndim)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -465,57 +492,48 @@ def gemm(codes, scales, X, stream=None):
 # ---- MXFP4 and experts ----
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 _FLOATS = tuple(_DTYPE)
+_U8 = (torch.uint8,)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
 
 
-def _same_device(*named):
-    """The tensors (name, tensor or None) of one call live on one device."""
-    first = None
-    for name, t in named:
-        if t is None:
-            continue
-        if first is None:
-            first = (name, t.device)
-        elif t.device != first[1]:
-            raise ValueError(f"{name} is on {t.device}, {first[0]} on {first[1]}")
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
-def _mx_matrix(codes, scales, what="codes", lead=0):
-    """(lead sizes..., N, K) of a packed MXFP4 matrix (stack of matrices: lead = 1)."""
-    _need(codes, what, (torch.uint8,), (2 + lead,))
-    _need(scales, what.replace("codes", "scales"), (torch.uint8,), (2 + lead,))
-    K = 2 * codes.shape[-1]
-    if tuple(scales.shape) != tuple(codes.shape[:-1]) + (K // MX_BLOCK,) or K % MX_BLOCK:
-        raise ValueError(f"{what} {tuple(codes.shape)} needs scales of shape "
-                         f"[..., K/{MX_BLOCK}] with K = 2 * {codes.shape[-1]}, "
-                         f"got {tuple(scales.shape)}")
-    return tuple(codes.shape[:-1]) + (K,)
+def _mx_matrix(codes, scales, what="codes", ndim=2):
+    """The sizes (.., N, K) of a packed MXFP4 matrix (a stack of them: ndim 3)."""
+    _need(codes, what, _U8, (ndim,))
+    _need(scales, "scales" if what == "codes" else "xscales", _U8, (ndim,))
+    *lead, half = codes.shape
+    if half % (MX_BLOCK // 2) or list(scales.shape) != lead + [half // (MX_BLOCK // 2)]:
+        raise ValueError(f"{what} {tuple(codes.shape)} needs scales [..., K/{MX_BLOCK}] with "
+                         f"K = {2 * half}, got {tuple(scales.shape)}")
+    return lead + [2 * half]
 
 
 def nf4_mx_pack(W, codes, scales, dev_status=None, stream=None):
     """Quantise W [N][K] (fp32 or bf16) into MXFP4 codes uint8 [N][K/2] and scales
     uint8 [N][K/32]."""
     _need(W, "W", _FLOATS, (2,))
-    if _mx_matrix(codes, scales) != tuple(W.shape):
+    N, K = W.shape
+    if _mx_matrix(codes, scales) != [N, K]:
         raise ValueError(f"codes must be [N][K/2] for W {tuple(W.shape)}")
     if dev_status is not None:
-        _need(dev_status, "dev_status", (torch.int32,))
-    _same_device(("W", W), ("codes", codes), ("scales", scales), ("dev_status", dev_status))
-    with torch.cuda.device(W.device):
-        _check("nf4_mx_pack", _load().nf4_mx_pack(
-            _ptr(W), _DTYPE[W.dtype], W.shape[0], W.shape[1], _ptr(codes), _ptr(scales),
-            _ptr(dev_status), _stream(W.device, stream)))
+        _need(dev_status, "dev_status", _I32)
+    _run("nf4_mx_pack", (W, codes, scales, dev_status),
+         (W.data_ptr(), _DTYPE[W.dtype], N, K, codes.data_ptr(), scales.data_ptr(),
+          _addr(dev_status)), stream)
 
 
 def nf4_mx_unpack(codes, scales, W_out, stream=None):
     """W_out [N][K] (fp32 or bf16) = the values of a packed MXFP4 matrix."""
     _need(W_out, "W_out", _FLOATS, (2,))
-    if _mx_matrix(codes, scales) != tuple(W_out.shape):
+    N, K = W_out.shape
+    if _mx_matrix(codes, scales) != [N, K]:
         raise ValueError(f"W_out must be [N][K], has {tuple(W_out.shape)}")
-    _same_device(("codes", codes), ("scales", scales), ("W_out", W_out))
-    with torch.cuda.device(W_out.device):
-        _check("nf4_mx_unpack", _load().nf4_mx_unpack(
-            _ptr(codes), _ptr(scales), W_out.shape[0], W_out.shape[1], _ptr(W_out),
-            _DTYPE[W_out.dtype], _stream(W_out.device, stream)))
+    _run("nf4_mx_unpack", (codes, scales, W_out),
+         (codes.data_ptr(), scales.data_ptr(), N, K, W_out.data_ptr(), _DTYPE[W_out.dtype]), stream)
 
 
 def nf4_mx_gemm(codes, scales, X, Y, stream=None):
@@ -528,11 +546,9 @@ def nf4_mx_gemm(codes, scales, X, Y, stream=None):
         raise ValueError(f"X has {X.shape[-1]} columns, the matrix K = {K}")
     if Y.numel() != M * N:
         raise ValueError("Y must have M*N elements")
-    _same_device(("X", X), ("codes", codes), ("scales", scales), ("Y", Y))
-    with torch.cuda.device(X.device):
-        _check("nf4_mx_gemm", _load().nf4_mx_gemm(
-            _ptr(codes), _ptr(scales), N, K, _ptr(X), M, _ptr(Y), _DTYPE[Y.dtype],
-            _stream(X.device, stream)))
+    _run("nf4_mx_gemm", (X, codes, scales, Y),
+         (codes.data_ptr(), scales.data_ptr(), N, K, X.data_ptr(), M, Y.data_ptr(),
+          _DTYPE[Y.dtype]), stream)
 
 
 def nf4_mx_gemm_packed(codes, scales, xcodes, xscales, Y, stream=None):
@@ -544,47 +560,40 @@ def nf4_mx_gemm_packed(codes, scales, xcodes, xscales, Y, stream=None):
         raise ValueError(f"xcodes has K = {KX}, codes K = {K}")
     if Y.numel() != M * N:
         raise ValueError("Y must have M*N elements")
-    _same_device(("codes", codes), ("scales", scales), ("xcodes", xcodes), ("xscales", xscales),
-                 ("Y", Y))
-    with torch.cuda.device(codes.device):
-        _check("nf4_mx_gemm_packed", _load().nf4_mx_gemm_packed(
-            _ptr(codes), _ptr(scales), N, K, _ptr(xcodes), _ptr(xscales), M, _ptr(Y),
-            _DTYPE[Y.dtype], _stream(codes.device, stream)))
+    _run("nf4_mx_gemm_packed", (codes, scales, xcodes, xscales, Y),
+         (codes.data_ptr(), scales.data_ptr(), N, K, xcodes.data_ptr(), xscales.data_ptr(), M,
+          Y.data_ptr(), _DTYPE[Y.dtype]), stream)
 
 
-def _grouped(func, codes, scales, rows, name, width, offsets, out, out_name, out_width, stream):
-    E, N, K = _mx_matrix(codes, scales, lead=1)
-    sizes = {"N": N, "K": K}
+def _grouped(func, codes, scales, rows, name, grad, offsets, out, out_name, stream):
+    E, N, K = _mx_matrix(codes, scales, ndim=3)
+    width, out_width = (N, K) if grad else (K, N)
     _need(rows, name, _BF16, (2,))
-    _need(offsets, "offsets", (torch.int32,), (1,))
+    _need(offsets, "offsets", _I32, (1,))
     _need(out, out_name, _FLOATS, (2,))
     R = rows.shape[0]
-    if rows.shape[1] != sizes[width]:
-        raise ValueError(f"{name} must be [R][{width}={sizes[width]}]")
-    if tuple(out.shape) != (R, sizes[out_width]):
-        raise ValueError(f"{out_name} must be [R={R}][{out_width}={sizes[out_width]}]")
+    if rows.shape[1] != width:
+        raise ValueError(f"{name} must be [R][{width}], has {tuple(rows.shape)}")
+    if tuple(out.shape) != (R, out_width):
+        raise ValueError(f"{out_name} must be [{R}][{out_width}], has {tuple(out.shape)}")
     if offsets.numel() != E + 1:
         raise ValueError(f"offsets must have E + 1 = {E + 1} entries")
-    _same_device((name, rows), ("codes", codes), ("scales", scales), ("offsets", offsets),
-                 (out_name, out))
-    with torch.cuda.device(rows.device):
-        _check(func, getattr(_load(), func)(
-            _ptr(codes), _ptr(scales), E, N, K, _ptr(rows), _ptr(offsets), R, _ptr(out),
-            _DTYPE[out.dtype], _stream(rows.device, stream)))
+    _run(func, (rows, codes, scales, offsets, out),
+         (codes.data_ptr(), scales.data_ptr(), E, N, K, rows.data_ptr(), offsets.data_ptr(), R,
+          out.data_ptr(), _DTYPE[out.dtype]), stream)
 
 
 def nf4_mx_gemm_grouped(codes, scales, X, offsets, Y, stream=None):
     """Y [R][N] (fp32 or bf16): rows offsets[e] .. offsets[e+1]-1 of X bf16 [R][K]
     times expert e's packed matrix, codes [E][N][K/2], scales [E][N][K/32]; rows from
     offsets[E] on are zero.  offsets: int32 [E+1] on the device."""
-    _grouped("nf4_mx_gemm_grouped", codes, scales, X, "X", "K", offsets, Y, "Y", "N", stream)
+    _grouped("nf4_mx_gemm_grouped", codes, scales, X, "X", False, offsets, Y, "Y", stream)
 
 
 def nf4_mx_gemm_grouped_grad(codes, scales, dY, offsets, dX, stream=None):
     """dX [R][K] (fp32 or bf16): the gradient of nf4_mx_gemm_grouped in its rows,
     from dY bf16 [R][N], N % 8 == 0."""
-    _grouped("nf4_mx_gemm_grouped_grad", codes, scales, dY, "dY", "N", offsets, dX, "dX", "K",
-             stream)
+    _grouped("nf4_mx_gemm_grouped_grad", codes, scales, dY, "dY", True, offsets, dX, "dX", stream)
 
 
 def nf4_moe_sort(experts, num_experts, offsets, order, place, dev_status=None, stream=None):
@@ -592,73 +601,64 @@ def nf4_moe_sort(experts, num_experts, offsets, order, place, dev_status=None, s
     [E+1], order int32 [T*topk] (slot of each row), place int32 [T][topk] (row of
     each slot; ~ marks slots without an expert, which come last)."""
     _need(experts, "experts", (torch.int64,), (2,))
-    _need(offsets, "offsets", (torch.int32,), (1,))
-    _need(order, "order", (torch.int32,), (1,))
-    _need(place, "place", (torch.int32,), (2,))
+    _need(offsets, "offsets", _I32, (1,))
+    _need(order, "order", _I32, (1,))
+    _need(place, "place", _I32, (2,))
     T, topk = experts.shape
     if offsets.numel() != num_experts + 1:
         raise ValueError(f"offsets must have E + 1 = {num_experts + 1} entries")
-    if order.numel() != T * topk or tuple(place.shape) != (T, topk):
+    if order.numel() != T * topk or place.shape != experts.shape:
         raise ValueError(f"order must have {T * topk} entries and place the shape of experts")
     if dev_status is not None:
-        _need(dev_status, "dev_status", (torch.int32,))
-    _same_device(("experts", experts), ("offsets", offsets), ("order", order), ("place", place),
-                 ("dev_status", dev_status))
-    with torch.cuda.device(experts.device):
-        _check("nf4_moe_sort", _load().nf4_moe_sort(
-            _ptr(experts), T, topk, int(num_experts), _ptr(offsets), _ptr(order), _ptr(place),
-            _ptr(dev_status), _stream(experts.device, stream)))
+        _need(dev_status, "dev_status", _I32)
+    _run("nf4_moe_sort", (experts, offsets, order, place, dev_status),
+         (experts.data_ptr(), T, topk, int(num_experts), offsets.data_ptr(), order.data_ptr(),
+          place.data_ptr(), _addr(dev_status)), stream)
 
 
-def _rows(place, tokens, rows, weights=None):
-    """(T, topk, H) of a row operator; tokens and rows are (name, tensor) pairs of
-    one dtype, [T][H] and [T*topk][H]."""
-    _need(place, "place", (torch.int32,), (2,))
+def _rows(place, per_token, per_row, weights=()):
+    """(T, topk, H, dtype) of a row operator.  per_token and per_row: (name, tensor)
+    pairs of one dtype, [T][H] and [T*topk][H]; weights: pairs of fp32 [T][topk]."""
+    _need(place, "place", _I32, (2,))
     T, topk = place.shape
-    H = tokens[0][1].shape[-1]
-    for n, (name, t) in [(T, x) for x in tokens] + [(T * topk, x) for x in rows]:
-        _need(t, name, _FLOATS, (2,))
-        if tuple(t.shape) != (n, H):
-            raise ValueError(f"{name} must be [{n}][{H}], has {tuple(t.shape)}")
-        if t.dtype != tokens[0][1].dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, {tokens[0][0]} {tokens[0][1].dtype}")
-    for name, t in weights or ():
-        if t is not None:
-            _need(t, name, (torch.float32,), (2,))
-            if t.shape != place.shape:
-                raise ValueError(f"{name} must have the shape of place")
-    _same_device(("place", place), *tokens, *rows, *(weights or ()))
-    return T, topk, H
+    first, ref = per_token[0]
+    for pairs, n in ((per_token, T), (per_row, T * topk)):
+        for name, t in pairs:
+            _need(t, name, _FLOATS, (2,))
+            rows, H = t.shape
+            if rows != n or H != ref.shape[1]:
+                raise ValueError(f"{name} must be [{n}][{ref.shape[1]}], has {tuple(t.shape)}")
+            if t.dtype != ref.dtype:
+                raise TypeError(f"{name} has dtype {t.dtype}, {first} {ref.dtype}")
+    for name, t in weights:
+        _need(t, name, _F32, (2,))
+        if t.shape != place.shape:
+            raise ValueError(f"{name} must have the shape of place, {tuple(place.shape)}")
+    return T, topk, ref.shape[1], _DTYPE[ref.dtype]
 
 
 def nf4_moe_gather(X, place, out, stream=None):
     """out [T*topk][H]: row place[t][j] = X[t], zeros for slots without an expert."""
-    T, topk, H = _rows(place, [("X", X)], [("out", out)])
-    with torch.cuda.device(X.device):
-        _check("nf4_moe_gather", _load().nf4_moe_gather(
-            _ptr(X), _DTYPE[X.dtype], _ptr(place), T, topk, H, _ptr(out),
-            _stream(X.device, stream)))
+    T, topk, H, dtype = _rows(place, (("X", X),), (("out", out),))
+    _run("nf4_moe_gather", (X, place, out),
+         (X.data_ptr(), dtype, place.data_ptr(), T, topk, H, out.data_ptr()), stream)
 
 
 def nf4_moe_combine(Y, place, weights, out, stream=None):
     """out [T][H] = sum_j weights[t][j] * Y[place[t][j]] (weights None: plain sum)."""
-    T, topk, H = _rows(place, [("out", out)], [("Y", Y)], [("weights", weights)])
-    with torch.cuda.device(Y.device):
-        _check("nf4_moe_combine", _load().nf4_moe_combine(
-            _ptr(Y), _DTYPE[Y.dtype], _ptr(place), _ptr(weights), T, topk, H, _ptr(out),
-            _stream(Y.device, stream)))
+    T, topk, H, dtype = _rows(place, (("out", out),), (("Y", Y),),
+                              () if weights is None else (("weights", weights),))
+    _run("nf4_moe_combine", (Y, place, weights, out),
+         (Y.data_ptr(), dtype, place.data_ptr(), _addr(weights), T, topk, H, out.data_ptr()), stream)
 
 
 def nf4_moe_combine_grad(dOut, Y, place, weights, dY, dweights, stream=None):
     """dY [T*topk][H] and dweights fp32 [T][topk] of nf4_moe_combine from dOut [T][H]."""
-    T, topk, H = _rows(place, [("dOut", dOut)], [("Y", Y), ("dY", dY)],
-                       [("weights", weights), ("dweights", dweights)])
-    if weights is None or dweights is None:
-        raise TypeError("weights and dweights must be torch.Tensors")
-    with torch.cuda.device(Y.device):
-        _check("nf4_moe_combine_grad", _load().nf4_moe_combine_grad(
-            _ptr(dOut), _ptr(Y), _DTYPE[Y.dtype], _ptr(place), _ptr(weights), T, topk, H,
-            _ptr(dY), _ptr(dweights), _stream(Y.device, stream)))
+    T, topk, H, dtype = _rows(place, (("dOut", dOut),), (("Y", Y), ("dY", dY)),
+                              (("weights", weights), ("dweights", dweights)))
+    _run("nf4_moe_combine_grad", (dOut, Y, place, weights, dY, dweights),
+         (dOut.data_ptr(), Y.data_ptr(), dtype, place.data_ptr(), weights.data_ptr(), T, topk, H,
+          dY.data_ptr(), dweights.data_ptr()), stream)
 
 
 def mx_pack(W, stream=None, check=True):
@@ -670,31 +670,27 @@ def mx_pack(W, stream=None, check=True):
     scales = torch.empty((N, K // MX_BLOCK), dtype=torch.uint8, device=W.device)
     status = torch.empty(1, dtype=torch.int32, device=W.device) if check else None
     nf4_mx_pack(W, codes, scales, status, stream)
-    if check and _status_on(status, stream):
-        raise ValueError(f"nf4_mx_pack flagged blocks: status bits {int(status.item()):#x}")
+    if check:
+        ts = stream
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            ts = torch.cuda.ExternalStream(_stream(W.device, stream).value, device=W.device)
+        with torch.cuda.stream(ts):  # None: the current one
+            st = int(status.item())
+        if st:
+            raise ValueError(f"nf4_mx_pack flagged blocks: status bits {st:#x}")
     return codes, scales
 
 
-def _status_on(status, stream):
-    """The status word's value, read after the call on `stream`."""
-    if stream is None:
-        return int(status.item())
-    handle = _stream(status.device, stream).value
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=status.device)):
-        return int(status.item())
-
-
 def mx_unpack(codes, scales, dtype=torch.float32, stream=None):
-    N, K = _mx_matrix(codes, scales)
-    W = torch.empty((N, K), dtype=dtype, device=codes.device)
+    W = torch.empty((codes.shape[0], 2 * codes.shape[1]), dtype=dtype, device=codes.device)
     nf4_mx_unpack(codes, scales, W, stream)
     return W
 
 
 def mx_gemm(codes, scales, X, out_dtype=torch.float32, stream=None):
     """Y [M][N] = X . dequant(codes, scales)^T for any M (a vector X: Y [N])."""
-    M = (X.shape[0],) if X.dim() == 2 else ()
-    Y = torch.empty(M + (codes.shape[0],), dtype=out_dtype, device=X.device)
+    shape = (X.shape[0], codes.shape[0]) if X.dim() == 2 else (codes.shape[0],)
+    Y = torch.empty(shape, dtype=out_dtype, device=X.device)
     nf4_mx_gemm(codes, scales, X, Y, stream)
     return Y
 

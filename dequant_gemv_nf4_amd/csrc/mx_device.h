@@ -23,15 +23,56 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, kBufferWord3);
 }
 
-// 16 bytes a lane from memory straight into LDS at base + 16 * lane.  The compiler
-// does not tie these loads to the reads of that memory: lds_loads_done() waits
-// for them (and every other load of the wave) and precedes the barrier after
-// which the data is read.
-__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rsrc, uint8_t *base, int voffset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)base, 16,
-                                           voffset, 0, 0, 0);
+// A raw buffer as its four words, for the loads below.
+__device__ __forceinline__ u32x4_t buffer_words(const void *p, int bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  return u32x4_t{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, (uint32_t)bytes, (uint32_t)kBufferWord3};
 }
-__device__ __forceinline__ void lds_loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+// 16 (4) bytes a lane from memory straight into LDS at lds + 16 (4) * lane; lds is
+// uniform over the wave.  Written out because the compiler, which sees a store to
+// LDS in its builtin for this load, waits for every such load before the next read
+// of LDS, whatever it reads; here only lds_loads_but() waits.  It precedes the barrier
+// after which the data is read and the end of the kernel.  (s_nop: the wait
+// states between a vector instruction that wrote a scalar operand, or m0, and the
+// load.)
+__device__ __forceinline__ void load_lds16(u32x4_t rsrc, uint32_t lds, int voffset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
+               "v"(voffset), "s"(rsrc)
+               : "memory");
+}
+__device__ __forceinline__ void load_lds4(u32x4_t rsrc, uint32_t lds, int voffset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds),
+               "v"(voffset), "s"(rsrc)
+               : "memory");
+}
+// Waits for the wave's loads, all but the newest N.
+template <int N>
+__device__ __forceinline__ void lds_loads_but() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Four bytes at any byte offset of `base`, from the two words around them: a load
+// that is started with `fetch` and finished, when its words are here, with `word`.
+struct LooseWords {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int shift;  // of the base within its word
+  __device__ __forceinline__ LooseWords(const uint8_t *base, int64_t bytes) {
+    shift = (int)((uintptr_t)base & 3);
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base - shift), 0,
+                                             (int)((bytes + shift + 3) & ~int64_t(3)), kBufferWord3);
+  }
+  __device__ __forceinline__ uint32_t fetch(int offset, int i) const {
+    return __builtin_amdgcn_raw_buffer_load_b32(rsrc, ((offset + shift) & ~3) + 4 * i, 0, 0);
+  }
+  __device__ __forceinline__ uint32_t word(int offset, uint32_t lo, uint32_t hi) const {
+    return __builtin_amdgcn_alignbyte(hi, lo, (offset + shift) & 3);
+  }
+};
 
 // 8 codes (one word, low nibble first) times 2^(byte - 127) as bf16: exact, the
 // element and the power of two fit bf16.  `scale` holds the byte in the exponent
@@ -139,11 +180,11 @@ __device__ __forceinline__ bool grid_item(const Grid &g, int *slot, int *block) 
 }
 
 // Row tiles a launch has to allow for: every expert (and the rows of none) can
-// leave one partial tile.
+// leave one partial tile, and no tile is empty.
 inline int64_t slots_for(int64_t R, int64_t E, bool grouped, int bm) {
   if (!grouped) return (R + bm - 1) / bm;
-  const int64_t part = R < E + 1 ? R : E + 1;
-  return R / bm + part;
+  const int64_t n = R / bm + E + 1;
+  return n < R ? n : R;
 }
 
 // Four consecutive outputs of one row, as fp32 or bf16 (one rounding).

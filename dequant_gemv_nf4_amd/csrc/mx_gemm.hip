@@ -27,115 +27,26 @@ struct Args {
   Grid grid;
 };
 
-// ------------------------------------------------------------ few rows ----
-// A workgroup owns 16 CT columns x 16 RT rows; its NW waves take steps w, w + NW,
-// ... of K and add their tiles through LDS in wave order.  Weights come from HBM
-// once, X from the caches.
-template <int RT, int CT, int NW, typename OUT>
-__global__ void __launch_bounds__(64 * NW) mx_rows_kernel(Args p) {
-  __shared__ f32x4_t part[NW][RT * CT][64];
+// ------------------------------------------------------- one to four rows ----
+// A wave's load of codes is 1 KiB of one weight row (2048 k, one block a lane), so
+// every line is read whole; the lane's 32 values of each row of X stay in
+// registers while the wave walks weight rows.  Waves (c, g) of a workgroup:
+// chunk c of K, weight rows g, g + G, ... of the workgroup's; chunks' sums meet in
+// LDS and are added in order.
+template <int MT, int RP, typename OUT>
+__global__ void __launch_bounds__(1024) mx_gemv_kernel(Args p, int chunks, int rows_wg) {
+  extern __shared__ float part1[];  // [chunk][row of the workgroup][MT]
   int slot, block;
   if (!grid_item(p.grid, &slot, &block)) return;
-  const RowTile t = find_tile(p.offsets, p.E, p.R, slot, 16 * RT);
+  const RowTile t = find_tile(p.offsets, p.E, p.R, slot, MT);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int l16 = lane & 15, q = lane >> 4;
-  const int n0 = block * 16 * CT;
-  const int cols = min(16 * CT, p.N - n0);
-  f32x4_t acc[RT][CT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) acc[r][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  if (t.e >= 0) {
-    const int kb = p.K >> 5;  // blocks per row
-    const int64_t first = (int64_t)t.e * p.N + n0;
-    const __amdgpu_buffer_rsrc_t crs = buffer(p.codes + first * (p.K >> 1), (int64_t)cols * (p.K >> 1));
-    const __amdgpu_buffer_rsrc_t srs = buffer(p.scales + first * kb, (int64_t)cols * kb);
-    const __amdgpu_buffer_rsrc_t xrs =
-        buffer(p.X + (int64_t)t.row0 * p.K, (int64_t)t.rows * p.K * 2);
-    const int steps = (kb + 3) >> 2;
-    constexpr int U = RT * CT >= 4 ? 1 : 2;  // steps whose loads are in flight together
-    for (int s0 = wave; s0 < steps; s0 += NW * U) {
-      u32x4_t cw[U][CT], xw[U][RT][4];
-      uint32_t sb[U][CT];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int b = (s0 + u * NW) * 4 + q;
-        const int out = b < kb ? 0 : kOutside;
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const int n = c * 16 + l16;
-          cw[u][c] = __builtin_amdgcn_raw_buffer_load_b128(crs, (n * (p.K >> 1) + b * 16) | out, 0,
-                                                           kLoadStream);
-          sb[u][c] = __builtin_amdgcn_raw_buffer_load_b8(srs, (n * kb + b) | out, 0, 0);
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            xw[u][r][j] = __builtin_amdgcn_raw_buffer_load_b128(
-                xrs, ((r * 16 + l16) * p.K * 2 + b * 64 + j * 16) | out, 0, 0);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            const u32x4_t a = decode8(cw[u][c][j], scale_of(sb[u][c]));
-#pragma unroll
-            for (int r = 0; r < RT; ++r) acc[r][c] = mfma16(a, xw[u][r][j], acc[r][c]);
-          }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) part[wave][r * CT + c][lane] = acc[r][c];
-  __syncthreads();
+  const int groups = (int)(blockDim.x >> 6) / chunks;
+  const int c = wave % chunks, g = wave / chunks;
+  const int n0 = block * rows_wg;
+  const int cols = min(rows_wg, p.N - n0);
   OUT *Y = reinterpret_cast<OUT *>(p.Y);
-  const bool vec = (p.N & 3) == 0;
-  for (int i = threadIdx.x; i < RT * CT * 64; i += 64 * NW) {
-    const int f = i >> 6, l = i & 63;
-    f32x4_t v = part[0][f][l];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) v += part[w][f][l];
-    const int m = f / CT * 16 + (l & 15);
-    const int n = n0 + f % CT * 16 + (l >> 4) * 4;
-    if (m < t.rows) store4<OUT>(Y + (int64_t)(t.row0 + m) * p.N, n, p.N, v, vec);
-  }
-}
-
-// ----------------------------------------------------------- many rows ----
-// A workgroup of 4 waves owns 16 MF rows x 256 columns; wave w decodes columns
-// 64 w .. 64 w + 63 into registers (no weight is decoded twice), the rows'
-// 16 MF x 128 tile of X goes through LDS, double-buffered, loaded there directly.  A
-// row's 16-byte chunk c sits at chunk c ^ (row % 16), so the 16 rows of a
-// fragment read fall into different banks.
-constexpr int kTileCols = 256;
-
-template <int MF, typename OUT>
-__global__ void __launch_bounds__(256, 2) mx_tile_kernel(Args p) {
-  constexpr int BM = 16 * MF;
-  __shared__ __attribute__((aligned(1024))) uint8_t xs[2][BM * 256];
-  int slot, block;
-  if (!grid_item(p.grid, &slot, &block)) return;
-  const RowTile t = find_tile(p.offsets, p.E, p.R, slot, BM);
-  if (t.rows <= 0) return;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int l16 = lane & 15, q = lane >> 4;
-  const int n0 = block * kTileCols;
-  const int cols = min(kTileCols, p.N - n0);
-  f32x4_t acc[4][MF];
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int r = 0; r < MF; ++r) acc[c][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
   if (t.e >= 0) {
     const int kb = p.K >> 5;
     const int64_t first = (int64_t)t.e * p.N + n0;
@@ -143,60 +54,325 @@ __global__ void __launch_bounds__(256, 2) mx_tile_kernel(Args p) {
     const __amdgpu_buffer_rsrc_t srs = buffer(p.scales + first * kb, (int64_t)cols * kb);
     const __amdgpu_buffer_rsrc_t xrs =
         buffer(p.X + (int64_t)t.row0 * p.K, (int64_t)t.rows * p.K * 2);
-    const int steps = (kb + 3) >> 2;
-    // X loads: wave w, load i covers rows 4 (w + 4 i) .. + 3 of the tile
-    const int xrow = wave * 4 + q;
-    const int xchunk = l16 ^ (xrow & 15);  // rows 16 i + xrow share row % 16
-    const auto load_x = [&](int buf, int s) {
-      const int out = s * 16 + xchunk < kb * 4 ? 0 : kOutside;
-#pragma unroll
-      for (int i = 0; i < MF; ++i)
-        load_lds16(xrs, &xs[buf][(i * 16 + wave * 4) * 256],
-                   ((i * 16 + xrow) * p.K * 2 + s * 256 + xchunk * 16) | out);
+    const int b = c * 64 + lane;
+    const int out = b < kb ? 0 : kOutside;
+    u32x4_t cw[RP];
+    uint32_t sb[RP];
+    const auto load = [&](int i, int n) {
+      cw[i] = __builtin_amdgcn_raw_buffer_load_b128(crs, (n * (p.K >> 1) + b * 16) | out, 0, kLoadStream);
+      sb[i] = __builtin_amdgcn_raw_buffer_load_b8(srs, (n * kb + b) | out, 0, 0);
     };
-    u32x4_t cw[4];
-    uint32_t sb[4];
-    const auto load_w = [&](int s) {
-      const int b = s * 4 + q;
-      const int out = b < kb ? 0 : kOutside;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int n = wave * 64 + c * 16 + l16;
-        cw[c] = __builtin_amdgcn_raw_buffer_load_b128(crs, (n * (p.K >> 1) + b * 16) | out, 0, 0);
-        sb[c] = __builtin_amdgcn_raw_buffer_load_b8(srs, (n * kb + b) | out, 0, 0);
-      }
-    };
-    load_x(0, 0);
-    load_w(0);
-    for (int s = 0; s < steps; ++s) {
-      lds_loads_done();
-      __syncthreads();  // the step's rows are in LDS, the other buffer is free
-      u32x4_t c0[4];
-      float sc[4];
+    for (int i = 0; i < RP; ++i) load(i, g + i * groups);
+    u32x4_t x[MT][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        c0[c] = cw[c];
-        sc[c] = scale_of(sb[c]);
-      }
-      if (s + 1 < steps) {
-        load_x((s + 1) & 1, s + 1);
-        load_w(s + 1);
-      }
-      const uint8_t *x = xs[s & 1] + l16 * 256;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u32x4_t b[MF];
+      for (int j = 0; j < 4; ++j)
+        x[m][j] = __builtin_amdgcn_raw_buffer_load_b128(xrs, (m * p.K * 2 + b * 64 + j * 16) | out, 0, 0);
+    for (int n = g; n < cols; n += RP * groups) {
 #pragma unroll
-        for (int r = 0; r < MF; ++r)
-          b[r] = *reinterpret_cast<const u32x4_t *>(x + r * 4096 + (((q * 4 + j) ^ l16) * 16));
+      for (int i = 0; i < RP; ++i) {
+        float acc[MT] = {};
+        const float sc = scale_of(sb[i]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const u32x4_t a = decode8(c0[c][j], sc[c]);
+        for (int j = 0; j < 4; ++j) {
+          const u32x4_t w = decode8(cw[i][j], sc);
 #pragma unroll
-          for (int r = 0; r < MF; ++r) acc[c][r] = mfma16(a, b[r], acc[c][r]);
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+              acc[m] = __builtin_amdgcn_fdot2_f32_bf16(
+                  __builtin_bit_cast(bf16x2_t, (uint32_t)w[h]),
+                  __builtin_bit_cast(bf16x2_t, (uint32_t)x[m][j][h]), acc[m], false);
+        }
+        load(i, n + (RP + i) * groups);
+        const int r = n + i * groups;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const float v = wave_sum(acc[m]);
+          if (lane == 0 && r < cols) part1[(c * rows_wg + r) * MT + m] = v;
         }
       }
     }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < cols * t.rows; i += blockDim.x) {
+    const int m = i / cols, r = i - m * cols;
+    float v = 0.f;
+    if (t.e >= 0) {
+      v = part1[r * MT + m];
+      for (int k = 1; k < chunks; ++k) v += part1[(k * rows_wg + r) * MT + m];
+    }
+    OUT *y = Y + (int64_t)(t.row0 + m) * p.N + n0 + r;
+    if constexpr (sizeof(OUT) == 4)
+      *y = v;
+    else
+      *y = (OUT)bf16_bits(v);
+  }
+}
+
+// ----------------------------------------------------------- more rows ----
+// A workgroup owns 16 MF rows x 16 NF WV columns; its waves form KG groups of WV that
+// share out K, wave w of a group decoding columns 16 NF w .. into registers (no
+// weight is decoded twice).  A stage is 64 KS values of k: the rows' tile of X goes
+// straight into LDS, three stages in rotation (four or five measured the same), one
+// barrier a stage.  Each wave's own
+// codes come the same way, 64 KW values of k at a time (loads of whole 64- or 128-byte
+// pieces of a row, where fragment-shaped loads from memory would touch a line a
+// lane), and a lane's scale bytes for 256 k in one load.
+
+// Permutation of a row's 16-byte chunks (XOR).  A 16-byte read is served 16 lanes at
+// a time, lanes 0-3, 12-15, 20-27 and so on: rows 0-3 and 12-15 of one lane quarter
+// with rows 4-11 of the next.  The permutations put these, too, into 16 different
+// columns of the 256 bytes that LDS reads a cycle.  A row of X is 128 KS bytes.
+template <int KS>
+__device__ __forceinline__ int x_perm(int row) {
+  return KS == 1 ? (row >> 1) & 7 : ((row >> 2) & 3) | (row & 3) << 2;
+}
+// The same for a row of 32 KW bytes of codes, read in words (KS = 1) or 16 bytes.
+template <int KS, int KW>
+__device__ __forceinline__ int w_perm(int row) {
+  return KW == 4 ? (row >> 1) & 7 : KS == 1 ? (row >> 2) & 3 : -(row >> 2) & 3;
+}
+
+template <int MF, int NF, int WV, int KS, int KW, int KG, bool SVEC, typename OUT>
+__global__ void __launch_bounds__(64 * WV *KG, (MF * NF > 32 ? 1 : MF * NF > 16 ? 2 : WV * KG / 2))
+    mx_tile_kernel(Args p) {
+  constexpr int BM = 16 * MF, BN = 16 * NF * WV;
+  constexpr int SG = 4 / KS;                              // stages per scale load (256 k)
+  constexpr int WS = KW / KS;                             // stages per block of codes
+  constexpr int NX = 3, NW = WS == 1 ? NX : 2;            // buffers of X and of codes
+  constexpr int XB = BM * 128 * KS, WB = BN * 32 * KW;    // bytes of one
+  constexpr int XL = MF * KS * 2 / WV, WL = NF * KW / 2;  // loads a wave
+  constexpr int XC = 8 * KS, WC = 2 * KW;                 // chunks a row
+  // Scales of 256 k: through LDS as well, or (KS = 1, where LDS is full, and rows that
+  // are not whole words) in registers
+  constexpr bool SL = SVEC && KS > 1;
+  constexpr int NS = SG == 1 ? 3 : 2, SB = NF > 2 ? 512 : 256, SLN = SB / 256;
+  constexpr int S = SL ? SLN : 0;
+  static_assert((WS == 1 || (WS == 2 && KS == 1)) && XL * WV == MF * KS * 2, "stages");
+  __shared__ __attribute__((aligned(1024))) uint8_t
+      shared[KG][NX * XB + NW * WB + (SL ? NS * SB * WV : 0)];
+  int slot, block;
+  if (!grid_item(p.grid, &slot, &block)) return;
+  const RowTile t = find_tile(p.offsets, p.E, p.R, slot, BM);
+  if (t.rows <= 0) return;
+  const int lane = threadIdx.x & 63;
+  const int wave_all = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wave = wave_all % WV, kg = wave_all / WV;
+  const int l16 = lane & 15, q = lane >> 4;
+  const int n0 = block * BN;
+  const int cols = min(BN, p.N - n0);
+  f32x4_t acc[NF][MF];
+#pragma unroll
+  for (int c = 0; c < NF; ++c)
+#pragma unroll
+    for (int r = 0; r < MF; ++r) acc[c][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  if (t.e >= 0) {
+    const int kb = p.K >> 5, kc = p.K >> 1;
+    const int64_t first = (int64_t)t.e * p.N + n0;
+    // scale groups (256 k), dealt to the K-groups in runs of `per`
+    const int sgs = (kb + 7) >> 3, per = (sgs + KG - 1) / KG;
+    const int g0 = kg * per;
+    uint8_t *const xlds = shared[kg];
+    uint8_t *const wlds = shared[kg] + NX * XB + wave * (WB / WV);  // + i * WB: buffer i
+    uint8_t *const slds = shared[kg] + NX * XB + NW * WB + wave * (NS * SB);
+    const uint32_t xaddr = lds_address(xlds), waddr = lds_address(wlds), saddr = lds_address(slds);
+    // Voffsets are fixed; a stage moves the buffers' base.  Only in a stage that
+    // K ends in (or past it) chunks are masked.
+    int xo[XL], wo[WL];
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      const int idx = (i * WV + wave) * 64 + lane, row = idx / XC;
+      xo[i] = row * p.K * 2 + (idx % XC ^ x_perm<KS>(row)) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < WL; ++i) {
+      const int idx = i * 64 + lane, row = idx / WC;  // within the wave's own columns
+      wo[i] = (wave * 16 * NF + row) * kc + (idx % WC ^ w_perm<KS, KW>(row)) * 16;
+    }
+    const int xbytes = t.rows * p.K * 2, wbytes = cols * kc;
+    const uint8_t *xbase = reinterpret_cast<const uint8_t *>(p.X + (int64_t)t.row0 * p.K);
+    const uint8_t *wbase = p.codes + first * kc;
+    const auto load_x = [&](int buf, int s) {  // s: stage from the start of K
+      const int adv = s * 128 * KS;
+      const u32x4_t rs = buffer_words(xbase + adv, max(xbytes - adv, 0));
+      const int left = kb * 4 - s * XC;  // chunks of the row from here on
+#pragma unroll
+      for (int i = 0; i < XL; ++i) {
+        const int idx = (i * WV + wave) * 64 + lane, row = idx / XC;
+        int o = xo[i];
+        if (left < XC) o = (idx % XC ^ x_perm<KS>(row)) < left ? o : kOutside;
+        load_lds16(rs, xaddr + buf * XB + (i * WV + wave) * 1024, o);
+      }
+    };
+    const auto load_w = [&](int buf, int b) {  // b: block of codes
+      const int adv = b * 32 * KW;
+      const u32x4_t rs = buffer_words(wbase + adv, max(wbytes - adv, 0));
+      const int left = kb - b * WC;
+#pragma unroll
+      for (int i = 0; i < WL; ++i) {
+        const int idx = i * 64 + lane, row = idx / WC;
+        int o = wo[i];
+        if (left < WC) o = (idx % WC ^ w_perm<KS, KW>(row)) < left ? o : kOutside;
+        load_lds16(rs, waddr + buf * WB + i * 1024, o);
+      }
+    };
+    // Column c * 16 + l16 of the wave has 8 scale bytes a group.  In LDS: NS groups in
+    // rotation.  In registers: the three words around them, or two.
+    const uint8_t *sbase = p.scales + first * kb;
+    const LooseWords loose(sbase, (int64_t)cols * kb);
+    constexpr int SWORDS = SVEC ? 2 : 3;
+    u32x2_t sreg[NF];
+    uint32_t snext[NF][SWORDS];
+    const auto load_scales = [&](int buf, int g) {
+      if constexpr (SL) {
+        const u32x4_t rs = buffer_words(sbase + g * 8, max(cols * kb - g * 8, 0));
+#pragma unroll
+        for (int i = 0; i < SLN; ++i) {
+          const int col = i * 32 + (lane >> 1), w = lane & 1;  // 8 bytes a column
+          const int o = (wave * 16 * NF + col) * kb + w * 4;
+          load_lds4(rs, saddr + buf * SB + i * 256,
+                    col < 16 * NF && g * 8 + w * 4 < kb ? o : kOutside);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < NF; ++c)
+#pragma unroll
+          for (int i = 0; i < SWORDS; ++i)
+            snext[c][i] = loose.fetch((wave * 16 * NF + c * 16 + l16) * kb + g * 8, i);
+      }
+    };
+    const auto take_scales = [&](int buf, int g) {
+      // bytes past the row's end are the next row's, perhaps NaN: as words they go
+      const int left = kb - g * 8;
+      const uint64_t own = left <= 0 ? 0 : left < 8 ? ~uint64_t(0) >> (64 - 8 * left) : ~uint64_t(0);
+#pragma unroll
+      for (int c = 0; c < NF; ++c) {
+        if constexpr (SL) {
+          sreg[c] = *reinterpret_cast<const u32x2_t *>(slds + buf * SB + (c * 16 + l16) * 8);
+        } else if constexpr (SVEC) {
+          sreg[c] = u32x2_t{snext[c][0], snext[c][1]};
+        } else {
+          const int o = (wave * 16 * NF + c * 16 + l16) * kb + g * 8;
+          sreg[c] = u32x2_t{loose.word(o, snext[c][0], snext[c][1]),
+                            loose.word(o, snext[c][1], snext[c][2])};
+        }
+        if constexpr (!SL) sreg[c] &= u32x2_t{(uint32_t)own, (uint32_t)(own >> 32)};
+      }
+    };
+    const int s0 = g0 * SG;
+    load_scales(0, g0);
+    load_x(0, s0);
+    load_w(0, s0 / WS);
+    if constexpr (SL && SG == 1) load_scales(1, g0 + 1);
+    load_x(1, s0 + 1);
+    if constexpr (WS == 1) load_w(1, s0 + 1);
+    int buf = 0, wbuf = 0, sbuf = 0;
+    for (int g = g0; g < g0 + per; ++g) {
+      if constexpr (!SL) take_scales(0, g);
+#pragma unroll
+      for (int u = 0; u < SG; ++u) {
+        const int s = g * SG + u;
+        // in flight may stay what the last stage asked for, which is not of this one
+        constexpr int one = XL + WL;
+        if (WS == 1)
+          SG == 1 || u == 1 ? lds_loads_but<S + one>() : lds_loads_but<one>();
+        else
+          u % 2 == 0 ? lds_loads_but<XL>() : lds_loads_but<one>();
+        __syncthreads();  // stage s is in LDS; the buffer of the last one is free
+        if (u == 0) {
+          if constexpr (SL) take_scales(sbuf, g);
+          if constexpr (SL && SG == 1)
+            load_scales(sbuf == 0 ? 2 : sbuf - 1, g + 2);
+          else
+            load_scales(sbuf ^ 1, g + 1);
+        }
+        load_x(buf == 0 ? NX - 1 : buf - 1, s + NX - 1);
+        if constexpr (WS == 1)
+          load_w(buf == 0 ? NX - 1 : buf - 1, s + NX - 1);
+        else if (u % 2 == 0)
+          load_w(wbuf ^ 1, s / 2 + 1);
+        const uint8_t *xt = xlds + buf * XB + l16 * 128 * KS;
+        const uint8_t *wt = wlds + (WS == 1 ? buf : wbuf) * WB + l16 * 32 * KW;
+        if constexpr (KS == 1) {
+          // 64 k: MFMA j has k = 32 j + 8 q .. + 7, one word of block j
+          constexpr int half = KW == 1 ? 0 : 2;
+          uint32_t w[NF][2];
+#pragma unroll
+          for (int c = 0; c < NF; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              w[c][j] = *reinterpret_cast<const uint32_t *>(
+                  wt + c * 512 * KW + ((u % 2 * half + j) ^ w_perm<KS, KW>(l16)) * 16 + q * 4);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            u32x4_t a[NF];
+#pragma unroll
+            for (int c = 0; c < NF; ++c)
+              a[c] = decode8(w[c][j], scale_of((sreg[c][u >> 1] >> (16 * (u & 1) + 8 * j)) & 0xffu));
+#pragma unroll
+            for (int r = 0; r < MF; ++r) {
+              const u32x4_t b = *reinterpret_cast<const u32x4_t *>(
+                  xt + r * 2048 + (((j * 4 + q) ^ x_perm<1>(l16)) * 16));
+#pragma unroll
+              for (int c = 0; c < NF; ++c) acc[c][r] = mfma16(a[c], b, acc[c][r]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < KS / 2; ++kk) {  // 128 k: lane q has block q
+            u32x4_t w[NF];
+            float sc[NF];
+#pragma unroll
+            for (int c = 0; c < NF; ++c) {
+              w[c] = *reinterpret_cast<const u32x4_t *>(
+                  wt + c * 512 * KW + (((kk * 4 + q) ^ w_perm<KS, KW>(l16)) * 16));
+              sc[c] = scale_of((sreg[c][KS == 4 ? kk : u] >> (8 * q)) & 0xffu);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              u32x4_t a[NF];
+#pragma unroll
+              for (int c = 0; c < NF; ++c) a[c] = decode8(w[c][j], sc[c]);
+#pragma unroll
+              for (int r = 0; r < MF; ++r) {
+                const u32x4_t b = *reinterpret_cast<const u32x4_t *>(
+                    xt + r * 2048 * KS + (((kk * 16 + q * 4 + j) ^ x_perm<KS>(l16)) * 16));
+#pragma unroll
+                for (int c = 0; c < NF; ++c) acc[c][r] = mfma16(a[c], b, acc[c][r]);
+              }
+            }
+          }
+        }
+        buf = buf == NX - 1 ? 0 : buf + 1;
+        if (u % 2 == 1) wbuf ^= 1;
+      }
+      sbuf = SG == 1 ? (sbuf == 2 ? 0 : sbuf + 1) : sbuf ^ 1;
+    }
+    lds_loads_but<0>();  // the loads past the end have landed, too
+  }
+  if constexpr (KG > 1) {
+    static_assert(sizeof(shared) >= (KG - 1) * WV * 64 * NF * MF * 16, "partial tiles fit the stages");
+    f32x4_t *part = reinterpret_cast<f32x4_t *>(&shared[0][0]);  // [kg - 1][wave][f][lane]
+    __syncthreads();
+    if (kg > 0)
+#pragma unroll
+      for (int c = 0; c < NF; ++c)
+#pragma unroll
+        for (int r = 0; r < MF; ++r)
+          part[(((kg - 1) * WV + wave) * NF * MF + c * MF + r) * 64 + lane] = acc[c][r];
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int c = 0; c < NF; ++c)
+#pragma unroll
+        for (int r = 0; r < MF; ++r)
+          acc[c][r] += part[((g * WV + wave) * NF * MF + c * MF + r) * 64 + lane];
   }
   OUT *Y = reinterpret_cast<OUT *>(p.Y);
   const bool vec = (p.N & 3) == 0;
@@ -206,44 +382,92 @@ __global__ void __launch_bounds__(256, 2) mx_tile_kernel(Args p) {
     if (m >= t.rows) continue;
     OUT *row = Y + (int64_t)(t.row0 + m) * p.N;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      store4<OUT>(row, n0 + wave * 64 + c * 16 + q * 4, p.N, acc[c][r], vec);
+    for (int c = 0; c < NF; ++c)
+      store4<OUT>(row, n0 + (wave * NF + c) * 16 + q * 4, p.N, acc[c][r], vec);
   }
 }
 
-template <int RT, int CT, int NW>
-static hipError_t launch_rows(Args &a, int out_dtype, hipStream_t s) {
-  a.grid = make_grid(slots_for(a.R, a.E, a.offsets != nullptr, 16 * RT),
-                     (a.N + 16 * CT - 1) / (16 * CT), 8);
+template <int MT>
+static hipError_t launch_gemv(Args &a, int out_dtype, hipStream_t s) {
+  constexpr int RP = 4;  // 8 rows ahead measured slower, 2 within 3 %
+  const int64_t slots = slots_for(a.R, a.E, a.offsets != nullptr, MT);
+  // 16 weight rows a workgroup (grouped: 32, an expert's rows of X are fewer than
+  // the launch allows for), 8 waves, or 4 where there are plenty of workgroups:
+  // N = 28672, K = 4096, M = 2: 17.8 us with 4 waves, 20.1 with 8; N = 4096: 6.6, 6.4
+  const int rows = a.offsets ? 32 : 16;
+  const int chunks = (a.K + 2047) / 2048;
+  const int waves = slots * a.N >= 8192 ? 4 : 8;
+  const int groups = chunks >= waves ? 1 : waves / chunks;
+  a.grid = make_grid(slots, (a.N + rows - 1) / rows, 8);
   const int64_t n = grid_size(a.grid);
-  if (n * 64 * NW >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  const int threads = 64 * chunks * groups;
+  if (n * threads >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  const size_t lds = (size_t)chunks * rows * MT * 4;
   if (out_dtype == NF4_F32)
-    hipLaunchKernelGGL((mx_rows_kernel<RT, CT, NW, float>), dim3((unsigned)n), dim3(64 * NW), 0, s, a);
+    hipLaunchKernelGGL((mx_gemv_kernel<MT, RP, float>), dim3((unsigned)n), dim3(threads), lds, s, a,
+                       chunks, rows);
   else
-    hipLaunchKernelGGL((mx_rows_kernel<RT, CT, NW, uint16_t>), dim3((unsigned)n), dim3(64 * NW), 0,
-                       s, a);
+    hipLaunchKernelGGL((mx_gemv_kernel<MT, RP, uint16_t>), dim3((unsigned)n), dim3(threads), lds, s,
+                       a, chunks, rows);
   return hipGetLastError();
 }
 
-template <int MF>
-static hipError_t launch_tile(Args &a, int out_dtype, hipStream_t s) {
+template <int MF, int NF, int WV, int KS, int KW, int KG, bool SVEC>
+static hipError_t launch_tile_as(Args &a, int out_dtype, hipStream_t s) {
   a.grid = make_grid(slots_for(a.R, a.E, a.offsets != nullptr, 16 * MF),
-                     (a.N + kTileCols - 1) / kTileCols, 8);
+                     (a.N + 16 * NF * WV - 1) / (16 * NF * WV), 8);
   const int64_t n = grid_size(a.grid);
-  if (n * 256 >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  if (n * 64 * WV * KG >= (int64_t(1) << 32)) return hipErrorInvalidValue;
   if (out_dtype == NF4_F32)
-    hipLaunchKernelGGL((mx_tile_kernel<MF, float>), dim3((unsigned)n), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((mx_tile_kernel<MF, NF, WV, KS, KW, KG, SVEC, float>), dim3((unsigned)n),
+                       dim3(64 * WV * KG), 0, s, a);
   else
-    hipLaunchKernelGGL((mx_tile_kernel<MF, uint16_t>), dim3((unsigned)n), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((mx_tile_kernel<MF, NF, WV, KS, KW, KG, SVEC, uint16_t>), dim3((unsigned)n),
+                       dim3(64 * WV * KG), 0, s, a);
   return hipGetLastError();
 }
 
-// Kernel by the rows an expert has on average (dense: all rows).
+template <int MF, int NF, int WV, int KS, int KW, int KG>
+static hipError_t launch_tile(Args &a, int out_dtype, hipStream_t s) {
+  if (a.K % 128 == 0 && aligned_to(a.scales, 4))
+    return launch_tile_as<MF, NF, WV, KS, KW, KG, true>(a, out_dtype, s);
+  return launch_tile_as<MF, NF, WV, KS, KW, KG, false>(a, out_dtype, s);
+}
+
+// The kernel for a product.  Up to two rows (four where the columns are too few to
+// give every CU a tile): the row kernel.  Else the largest tile that is not mostly
+// empty and still gives a CU one and a half tiles to overlap, else a smaller one
+// with K shared out inside the workgroup.  Measured (us): M = 256, N = K = 4096:
+// 64 x 128 tiles 27.5, 32 x 64 18.1, 16 x 64 with two K-groups 23; M = 16, N = 6144:
+// 16 x 64 12.1, with two K-groups 10.7, 16 x 32 with two 8.6; M = 8, N = 4096, K =
+// 14336: 16 x 32 with two K-groups 21.2, with four 17.5; M = 509, N = 28672: 128 x 256
+// 111, 64 x 128 148.
 static hipError_t launch_product(Args &a, int out_dtype, hipStream_t s) {
-  const int64_t rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
-  if (rows <= 16) return launch_rows<1, 1, 8>(a, out_dtype, s);
-  if (rows <= 64) return launch_rows<2, 2, 4>(a, out_dtype, s);
-  return launch_tile<8>(a, out_dtype, s);
+  const bool grouped = a.offsets != nullptr;
+  const auto tiles = [&](int bm, int bn) {
+    return slots_for(a.R, a.E, grouped, bm) * ((a.N + bn - 1) / bn);
+  };
+  // rows an expert has on average; popular ones have more
+  const int64_t mean = grouped ? (a.R + a.E - 1) / a.E : a.R;
+  const int64_t rows = grouped ? mean + mean / 2 : mean;
+  if (mean <= 1) return launch_gemv<1>(a, out_dtype, s);
+  if (mean <= 2) return launch_gemv<2>(a, out_dtype, s);
+  if (mean <= 4 && tiles(16, 64) < 256) return launch_gemv<4>(a, out_dtype, s);
+  constexpr int kFill = 384, kSplit = 192;
+  if (rows > 64 && tiles(128, 256) >= kFill) return launch_tile<8, 4, 4, 1, 2, 1>(a, out_dtype, s);
+  if (rows > 48) {
+    if (tiles(64, 128) >= kFill) return launch_tile<4, 2, 4, 2, 2, 1>(a, out_dtype, s);
+    if (tiles(64, 64) >= kFill) return launch_tile<4, 1, 4, 2, 2, 1>(a, out_dtype, s);
+  }
+  if (rows > 16) {
+    if (tiles(32, 128) >= kFill) return launch_tile<2, 2, 4, 2, 2, 1>(a, out_dtype, s);
+    if (tiles(32, 64) >= kFill) return launch_tile<2, 1, 4, 4, 4, 1>(a, out_dtype, s);
+    if (tiles(32, 64) >= kSplit) return launch_tile<2, 1, 4, 4, 4, 2>(a, out_dtype, s);
+  }
+  if (tiles(16, 64) >= kFill) return launch_tile<1, 1, 4, 4, 4, 1>(a, out_dtype, s);
+  if (tiles(16, 64) >= kSplit) return launch_tile<1, 1, 4, 4, 4, 2>(a, out_dtype, s);
+  if (tiles(16, 32) > 256) return launch_tile<1, 1, 2, 4, 4, 2>(a, out_dtype, s);
+  return launch_tile<1, 1, 2, 4, 4, 4>(a, out_dtype, s);
 }
 
 }  // namespace mx

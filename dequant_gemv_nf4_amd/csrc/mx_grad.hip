@@ -25,20 +25,43 @@ struct GradArgs {
   Grid grid;
 };
 
-// 16 MF rows x 512 columns a workgroup (128 columns a wave); dY goes through LDS in
-// stages of 128 n, laid out as the rows of the forward product.
-template <int MF, typename OUT>
-__global__ void __launch_bounds__(256, 2) mx_grad_kernel(GradArgs p) {
-  constexpr int BM = 16 * MF;
-  __shared__ __attribute__((aligned(1024))) uint8_t xs[2][BM * 256];
+// A workgroup owns 16 MF rows x 128 WV columns; its waves form KG groups of WV that
+// share out the n.  A stage is 64 n: the rows' tile of dY and the 64 rows of codes (64
+// bytes a wave) go straight into LDS, three stages in rotation, one barrier a
+// stage; a lane holds the four scale bytes of one n and passes them on through LDS.
+
+// dY: chunk of 16 bytes of a 128-byte row, permuted as the rows of the product.
+__device__ __forceinline__ int dy_perm(int row) { return (row >> 1) & 7; }
+// Codes: row n of a stage lies at row code_row, its 64-byte pieces permuted by
+// code_perm, so that the rows n, n + 8, n + 16, n + 24 that the lane quarters of a wave
+// read together cover all banks.
+template <int WV>
+__device__ __forceinline__ int code_row(int n) {
+  return WV == 2 ? n ^ ((n >> 4) & 1) : n;
+}
+template <int WV>
+__device__ __forceinline__ int code_perm(int n) {
+  return (n >> 3) & (WV - 1);
+}
+
+template <int MF, int WV, int KG, bool SVEC, typename OUT>
+__global__ void __launch_bounds__(64 * WV *KG, MF > 4 ? 1 : 2) mx_grad_kernel(GradArgs p) {
+  constexpr int BM = 16 * MF, NX = 3;
+  constexpr int XB = BM * 128, WB = 64 * 64 * WV;
+  constexpr int XL = 2 * MF / WV, WL = 4;  // loads a wave
+  static_assert(XL * WV == 2 * MF, "whole loads");
+  __shared__ __attribute__((aligned(1024))) uint8_t shared[KG][NX * (XB + WB)];
+  // the four scale bytes (one per block of 32 of the wave's columns) of each n
+  __shared__ __attribute__((aligned(256))) uint32_t sc[KG][WV][NX][64];
   int slot, block;
   if (!grid_item(p.grid, &slot, &block)) return;
   const RowTile t = find_tile(p.offsets, p.E, p.R, slot, BM);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wave = wave_all % WV, kg = wave_all / WV;
   const int l16 = lane & 15, q = lane >> 4;
-  const int k0 = block * 512 + wave * 128;
+  const int k0 = block * 128 * WV;
   f32x4_t acc[8][MF];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -48,49 +71,99 @@ __global__ void __launch_bounds__(256, 2) mx_grad_kernel(GradArgs p) {
   if (t.e >= 0) {
     const int kb = p.K >> 5, kc = p.K >> 1;
     const int64_t first = (int64_t)t.e * p.N;
-    const __amdgpu_buffer_rsrc_t crs = buffer(p.codes + first * kc, (int64_t)p.N * kc);
-    const __amdgpu_buffer_rsrc_t srs = buffer(p.scales + first * kb, (int64_t)p.N * kb);
-    const __amdgpu_buffer_rsrc_t yrs =
-        buffer(p.dY + (int64_t)t.row0 * p.N, (int64_t)t.rows * p.N * 2);
-    const int stages = (p.N + 127) >> 7;
-    const int xrow = wave * 4 + q;
-    const int xchunk = l16 ^ (xrow & 15);
-    const auto load_y = [&](int buf, int s) {
-      const int out = s * 128 + xchunk * 8 < p.N ? 0 : kOutside;
+    const int stages = (p.N + 63) >> 6, per = (stages + KG - 1) / KG;
+    uint8_t *const xlds = shared[kg];
+    uint8_t *const wlds = shared[kg] + NX * XB;
+    uint32_t *const slds = sc[kg][wave][0];
+    const uint32_t xaddr = lds_address(xlds), waddr = lds_address(wlds), saddr = lds_address(slds);
+    int xo[XL], wo[WL];
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
-        load_lds16(yrs, &xs[buf][(i * 16 + wave * 4) * 256],
-                   ((i * 16 + xrow) * p.N * 2 + s * 256 + xchunk * 16) | out);
+    for (int i = 0; i < XL; ++i) {
+      const int idx = (i * WV + wave) * 64 + lane, row = idx >> 3;
+      xo[i] = row * p.N * 2 + ((idx & 7) ^ dy_perm(row)) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < WL; ++i) {
+      const int idx = (i * WV + wave) * 64 + lane;
+      const int n = code_row<WV>(idx / (4 * WV)), ch = idx % (4 * WV);
+      wo[i] = n * kc + (k0 >> 1) + (ch ^ code_perm<WV>(n) * 4) * 16;
+    }
+    const int xbytes = t.rows * p.N * 2;
+    const uint8_t *xbase = reinterpret_cast<const uint8_t *>(p.dY + (int64_t)t.row0 * p.N);
+    const uint8_t *wbase = p.codes + first * kc;
+    // Past N the codes are outside their buffer and dY's chunks are masked; columns
+    // past K read another row's codes, their outputs are not stored.
+    const auto load_stage = [&](int buf, int s) {
+      const int adv = s * 128;
+      const u32x4_t rs = buffer_words(xbase + adv, max(xbytes - adv, 0));
+      const int left = (p.N >> 3) - s * 8;
+#pragma unroll
+      for (int i = 0; i < XL; ++i) {
+        const int idx = (i * WV + wave) * 64 + lane, row = idx >> 3;
+        int o = xo[i];
+        if (left < 8) o = ((idx & 7) ^ dy_perm(row)) < left ? o : kOutside;
+        load_lds16(rs, xaddr + buf * XB + (i * WV + wave) * 1024, o);
+      }
+      const int rows = max(p.N - s * 64, 0);
+      const u32x4_t ws = buffer_words(wbase + (int64_t)s * 64 * kc, rows * kc);
+#pragma unroll
+      for (int i = 0; i < WL; ++i)
+        load_lds16(ws, waddr + buf * WB + (i * WV + wave) * 1024, wo[i]);
     };
-    // columns past K: another row's codes, their outputs are not stored
-    const int kw = (k0 >> 1) + l16 * 4, ks = (k0 >> 5) + (l16 >> 2);
-    uint32_t cw[8], sb[8];
-    const auto load_w = [&](int n) {  // rows n + 8 q .. + 7; past N: outside the buffer
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = n + q * 8 + i;
-        const int out = r < p.N ? 0 : kOutside;
-        cw[i] = __builtin_amdgcn_raw_buffer_load_b32(crs, (r * kc + kw) | out, 0, 0);
-        sb[i] = __builtin_amdgcn_raw_buffer_load_b8(srs, (r * kb + ks) | out, 0, 0);
+    // lane: the four block scales of this wave's columns at n = 64 s + lane; rows that
+    // are not whole words go through registers, a stage ahead
+    const uint8_t *sbase = p.scales + first * kb;
+    const int so = lane * kb + (k0 >> 5) + wave * 4;
+    uint32_t snext[2];
+    const auto load_scales = [&](int buf, int s) {
+      const int bytes = max(p.N - s * 64, 0) * kb;
+      if constexpr (SVEC) {
+        load_lds4(buffer_words(sbase + (int64_t)s * 64 * kb, bytes), saddr + buf * 256, so);
+      } else {
+        const LooseWords loose(sbase + (int64_t)s * 64 * kb, bytes);
+        snext[0] = loose.fetch(so, 0);
+        snext[1] = loose.fetch(so, 1);
       }
     };
-    load_y(0, 0);
-    load_w(0);
-    for (int s = 0; s < stages; ++s) {
-      lds_loads_done();
-      __syncthreads();
-      if (s + 1 < stages) load_y((s + 1) & 1, s + 1);
-      const uint8_t *x = xs[s & 1] + l16 * 256;
+    const int s0 = kg * per;
+    load_scales(0, s0);
+    load_stage(0, s0);
+    if constexpr (SVEC) load_scales(1, s0 + 1);
+    load_stage(1, s0 + 1);
+    int buf = 0;
+    for (int s = s0; s < s0 + per; ++s) {
+      const int ahead = buf == 0 ? NX - 1 : buf - 1;
+      if constexpr (!SVEC) {
+        const LooseWords loose(sbase + (int64_t)s * 64 * kb, 0);
+        slds[buf * 64 + lane] = loose.word(so, snext[0], snext[1]);
+      }
+      lds_loads_but<XL + WL + (SVEC ? 1 : 0)>();
+      __syncthreads();  // stage s is in LDS; the buffer of the last one is free
+      if constexpr (SVEC)
+        load_scales(ahead, s + 2);
+      else
+        load_scales(0, s + 1);
+      load_stage(ahead, s + 2);
+      const uint8_t *xt = xlds + buf * XB + l16 * 128;
+      const uint8_t *wt = wlds + buf * WB;
 #pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
+      for (int h = 0; h < 2; ++h) {  // 32 n: lane quarter q has 8 of them
+        // row n = 32 h + 8 q + i: code_row and code_perm written out
+        const uint8_t *cr = wt + (h * 32 + q * 8) * 64 * WV + (wave ^ (q & (WV - 1))) * 64 + l16 * 4;
+        const int swap = WV == 2 ? q >> 1 : 0;
         u32x4_t d[8];
+        const u32x4_t *sr = reinterpret_cast<const u32x4_t *>(slds + buf * 64 + h * 32 + q * 8);
+        const u32x4_t s03 = sr[0], s47 = sr[1];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = decode8(cw[i], scale_of(sb[i]));
-        load_w(s * 128 + (i4 + 1) * 32);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t cw = *reinterpret_cast<const uint32_t *>(cr + (i ^ swap) * 64 * WV);
+          const uint32_t sb = i < 4 ? s03[i & 3] : s47[i & 3];
+          d[i] = decode8(cw, scale_of(__builtin_amdgcn_ubfe(sb, 8 * (l16 >> 2), 8)));
+        }
         u32x4_t b[MF];
 #pragma unroll
         for (int r = 0; r < MF; ++r)
-          b[r] = *reinterpret_cast<const u32x4_t *>(x + r * 4096 + (((i4 * 4 + q) ^ l16) * 16));
+          b[r] = *reinterpret_cast<const u32x4_t *>(xt + r * 2048 + (((h * 4 + q) ^ dy_perm(l16)) * 16));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           u32x4_t a;
@@ -102,7 +175,29 @@ __global__ void __launch_bounds__(256, 2) mx_grad_kernel(GradArgs p) {
           for (int r = 0; r < MF; ++r) acc[j][r] = mfma16(a, b[r], acc[j][r]);
         }
       }
+      buf = buf == NX - 1 ? 0 : buf + 1;
     }
+    lds_loads_but<0>();
+  }
+  if constexpr (KG > 1) {
+    static_assert(sizeof(shared) >= (KG - 1) * WV * 64 * 8 * MF * 16, "partial tiles fit the stages");
+    f32x4_t *part = reinterpret_cast<f32x4_t *>(&shared[0][0]);  // [kg - 1][wave][f][lane]
+    __syncthreads();
+    if (kg > 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int r = 0; r < MF; ++r)
+          part[(((kg - 1) * WV + wave) * 8 * MF + j * MF + r) * 64 + lane] = acc[j][r];
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int r = 0; r < MF; ++r)
+          acc[j][r] += part[((g * WV + wave) * 8 * MF + j * MF + r) * 64 + lane];
   }
   OUT *X = reinterpret_cast<OUT *>(p.dX);
 #pragma unroll
@@ -112,7 +207,7 @@ __global__ void __launch_bounds__(256, 2) mx_grad_kernel(GradArgs p) {
     OUT *row = X + (int64_t)(t.row0 + m) * p.K;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int k = k0 + 8 * (4 * q + i);
+      const int k = k0 + wave * 128 + 8 * (4 * q + i);
       if (k >= p.K) continue;
       float v[8];
 #pragma unroll
@@ -130,16 +225,49 @@ __global__ void __launch_bounds__(256, 2) mx_grad_kernel(GradArgs p) {
   }
 }
 
-template <int MF>
-static hipError_t launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
-  a.grid = make_grid(slots_for(a.R, a.E, true, 16 * MF), (a.K + 511) / 512, 8);
+template <int MF, int WV, int KG, bool SVEC>
+static hipError_t launch_grad_as(GradArgs &a, int out_dtype, hipStream_t s) {
+  a.grid = make_grid(slots_for(a.R, a.E, true, 16 * MF), (a.K + 128 * WV - 1) / (128 * WV), 8);
   const int64_t n = grid_size(a.grid);
-  if (n * 256 >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  if (n * 64 * WV * KG >= (int64_t(1) << 32)) return hipErrorInvalidValue;
   if (out_dtype == NF4_F32)
-    hipLaunchKernelGGL((mx_grad_kernel<MF, float>), dim3((unsigned)n), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, float>), dim3((unsigned)n),
+                       dim3(64 * WV * KG), 0, s, a);
   else
-    hipLaunchKernelGGL((mx_grad_kernel<MF, uint16_t>), dim3((unsigned)n), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, uint16_t>), dim3((unsigned)n),
+                       dim3(64 * WV * KG), 0, s, a);
   return hipGetLastError();
+}
+
+template <int MF, int WV, int KG>
+static hipError_t launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
+  if (a.K % 128 == 0 && aligned_to(a.scales, 4))
+    return launch_grad_as<MF, WV, KG, true>(a, out_dtype, s);
+  return launch_grad_as<MF, WV, KG, false>(a, out_dtype, s);
+}
+
+// The largest tile that is not mostly empty and gives every CU work, with N shared out
+// inside the workgroup where tiles are few.  Measured (us, columns x rows of the
+// matrices N x K): 16382 rows of 8 experts of 14336 x 4096: 64 x 512 tiles 1794, 32 x
+// 512 2278; 1000 rows: 64 x 512 228, with two K-groups 195; 1003 rows of 32 of 2048 x
+// 2048: 32 x 512 with two groups 27.7, 64 x 512 with two 34; 300 rows of 8 of 14336 x
+// 4096: 32 x 256 with two groups 103, 32 x 512 with two 154; 8 rows of 8: 16 x 256 with
+// four groups 78, with two 82.
+static hipError_t launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
+  const auto tiles = [&](int bm, int bk) {
+    return slots_for(a.R, a.E, true, bm) * ((a.K + bk - 1) / bk);
+  };
+  const int64_t mean = (a.R + a.E - 1) / a.E, rows = mean + mean / 2;
+  if (rows > 48) {
+    if (tiles(64, 512) >= 512) return launch_grad<4, 4, 1>(a, out_dtype, s);
+    if (tiles(64, 512) >= 160) return launch_grad<4, 4, 2>(a, out_dtype, s);
+  }
+  if (rows > 16) {
+    if (tiles(32, 512) >= 224) return launch_grad<2, 4, 2>(a, out_dtype, s);
+    if (tiles(32, 256) >= 192) return launch_grad<2, 2, 2>(a, out_dtype, s);
+  }
+  if (tiles(16, 256) >= 384) return launch_grad<1, 2, 2>(a, out_dtype, s);
+  return launch_grad<1, 2, 4>(a, out_dtype, s);
 }
 
 }  // namespace mx
@@ -162,7 +290,7 @@ int nf4_mx_gemm_grouped_grad(const uint8_t *codes, const uint8_t *scales, int64_
   if (int r = nf4::device_status()) return r;
   if (R == 0) return NF4_OK;
   nf4::mx::GradArgs a{codes, scales, dY, offsets, dX, R, (int)E, (int)N, (int)K, {}};
-  return nf4::launch_status(nf4::mx::launch_grad<4>(a, out_dtype, (hipStream_t)stream));
+  return nf4::launch_status(nf4::mx::launch_rows_grad(a, out_dtype, (hipStream_t)stream));
 }
 
 }  // extern "C"

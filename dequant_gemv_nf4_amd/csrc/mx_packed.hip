@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(64 * NW) mx_packed_rows_kernel(PackedArgs p) {
 // ----------------------------------------------------------- many rows ----
 // A workgroup owns a 256 x 256 tile; WN x WM waves, each 16 NF columns x 16 MF
 // rows.  A stage is 256 k: 128 bytes a row of either operand, loaded straight into
-// LDS (16-byte chunk c of a row at chunk c ^ (row % 8)), and 8 scale bytes a row;
+// LDS (16-byte chunk c of a row at chunk c ^ (row / 2 % 8), so that the 16
+// rows of a fragment fall into different banks), and 8 scale bytes a row;
 // double-buffered, one barrier a stage.
 template <int WN, int WM, int NF, int MF, bool SVEC, typename OUT>
 __global__ void __launch_bounds__(64 * WN * WM, WN *WM / 4) mx_packed_tile_kernel(PackedArgs p) {
@@ -124,9 +125,9 @@ __global__ void __launch_bounds__(64 * WN * WM, WN *WM / 4) mx_packed_tile_kerne
   const int64_t m0 = (int64_t)slot * BM;
   const int rows = (int)min((int64_t)BM, p.M - m0);
   const int kb = p.K >> 5, kc = p.K >> 1;
-  const __amdgpu_buffer_rsrc_t crs = buffer(p.codes + (int64_t)n0 * kc, (int64_t)cols * kc);
+  const u32x4_t crs = buffer_words(p.codes + (int64_t)n0 * kc, cols * kc);
   const __amdgpu_buffer_rsrc_t srs = buffer(p.scales + (int64_t)n0 * kb, (int64_t)cols * kb);
-  const __amdgpu_buffer_rsrc_t xrs = buffer(p.xcodes + m0 * kc, (int64_t)rows * kc);
+  const u32x4_t xrs = buffer_words(p.xcodes + m0 * kc, rows * kc);
   const __amdgpu_buffer_rsrc_t ars = buffer(p.xscales + m0 * kb, (int64_t)rows * kb);
   f32x4_t acc[NF][MF];
 #pragma unroll
@@ -134,19 +135,22 @@ __global__ void __launch_bounds__(64 * WN * WM, WN *WM / 4) mx_packed_tile_kerne
 #pragma unroll
     for (int r = 0; r < MF; ++r) acc[c][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int stages = (kb + 7) >> 3;
-  // a wave's load covers 8 rows; lane: row lane / 8, chunk (lane % 8) ^ (row % 8)
-  const int lrow = lane >> 3, lchunk = (lane & 7) ^ lrow;
+  const uint32_t tiles = lds_address(tile);
+  // a wave's load covers 8 rows, the first one 8 (wave + a multiple of 2); lane: row
+  // lane / 8, chunk (lane % 8) ^ (row / 2 % 8)
+  static_assert(WN * WM % 2 == 0, "row / 2 % 8 of a load depends on the wave alone");
+  const int lrow = lane >> 3, lchunk = (lane & 7) ^ ((wave & 1) * 4 + (lrow >> 1));
   const auto load_codes = [&](int buf, int s) {
     const int out = s * 8 + lchunk < kb ? 0 : kOutside;
 #pragma unroll
     for (int i = 0; i < BN / 8 / (WN * WM); ++i) {
       const int r = (i * WN * WM + wave) * 8;
-      load_lds16(crs, &tile[buf][r * 128], ((r + lrow) * kc + s * 128 + lchunk * 16) | out);
+      load_lds16(crs, tiles + buf * ROWS * 128 + r * 128, ((r + lrow) * kc + s * 128 + lchunk * 16) | out);
     }
 #pragma unroll
     for (int i = 0; i < BM / 8 / (WN * WM); ++i) {
       const int r = (i * WN * WM + wave) * 8;
-      load_lds16(xrs, &tile[buf][(BN + r) * 128], ((r + lrow) * kc + s * 128 + lchunk * 16) | out);
+      load_lds16(xrs, tiles + buf * ROWS * 128 + (BN + r) * 128, ((r + lrow) * kc + s * 128 + lchunk * 16) | out);
     }
   };
   // scales: thread -> rows tid, tid + NT, ... of the BN + BM
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(64 * WN * WM, WN *WM / 4) mx_packed_tile_kerne
 #pragma unroll
     for (int i = 0; i < SR; ++i)
       if (i * NT + tid < ROWS) sc[buf][i * NT + tid] = sreg[i];
-    lds_loads_done();
+    lds_loads_but<0>();
     __syncthreads();  // the stage is in LDS, the other buffer is free
     if (s + 1 < stages) {
       load_codes(buf ^ 1, s + 1);
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(64 * WN * WM, WN *WM / 4) mx_packed_tile_kerne
     for (int r = 0; r < MF; ++r) sx[r] = sc[buf][BN + wm * 16 * MF + r * 16 + l16];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int ch = ((h * 4 + q) ^ (l16 & 7)) * 16;
+      const int ch = ((h * 4 + q) ^ (l16 >> 1)) * 16;
       u32x4_t b[MF];
       uint32_t bs[MF];
 #pragma unroll

@@ -186,6 +186,36 @@ def test_nan_and_infinity_stay_in_their_row_and_column(nf4, M):
     assert bool(torch.isfinite(P[rest][:, torch.arange(N, device=DEV) != 33]).all())
 
 
+@pytest.mark.parametrize("K", [32, 96, 128, 224, 384, 416, 640])
+@pytest.mark.parametrize("M", [1, 3, 20, 40, 100, 600])
+def test_nan_scale_next_to_a_row_that_ends_inside_a_step(nf4, M, K):
+    """Every second weight row NaN from its first block on, and every second row of
+    X: the rows between, whose last step ends inside their neighbour, stay clean."""
+    N = 512
+    codes, scales = packed((N, K), K)
+    scales[1::2] = 255
+    X = normal((M, K), M, BF)
+    X[1::2] = float("nan")
+    want, mag = ref.product(X[0::2], ref.values(codes, scales)[0::2])
+    Y = nf4.mx_gemm(codes, scales, X)
+    ref.close(Y[0::2, 0::2].contiguous(), want, mag, K)
+    assert bool(torch.isnan(Y[:, 1::2]).all()) and bool(torch.isnan(Y[1::2]).all())
+    off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    G = nf4.mx_gemm_grouped(codes[None], scales[None], X, off)
+    ref.close(G[0::2, 0::2].contiguous(), want, mag, K)
+    # the gradient: NaN columns stay apart (the sum runs over the rows)
+    codes, scales = packed((64, K), K + 1)
+    scales[:, K // 64:] = 255
+    dY = normal((M, 64), M, BF)
+    dY[1::2] = float("nan")
+    v = ref.values(codes, scales)
+    clean = K // 64 * 32
+    dX = nf4.mx_gemm_grouped_grad(codes[None], scales[None], dY, off)
+    want, mag = ref.product(dY[0::2], v[:, :clean].t())
+    ref.close(dX[0::2, :clean].contiguous(), want, mag, 64)
+    assert bool(torch.isnan(dX[:, clean:]).all())
+
+
 @pytest.mark.parametrize("M", [2, 40, 150])
 def test_extreme_scales(nf4, M):
     """Weights near the smallest scale times large activations, and the reverse:
