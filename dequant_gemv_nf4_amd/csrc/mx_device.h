@@ -37,9 +37,9 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 // uniform over the wave.  Written out because the compiler, which sees a store to
 // LDS in its builtin for this load, waits for every such load before the next read
 // of LDS, whatever it reads; here only lds_loads_but() waits.  It precedes the barrier
-// after which the data is read and the end of the kernel.  (s_nop: the wait
-// states between a vector instruction that wrote a scalar operand, or m0, and the
-// load.)
+// after which the data is read and the end of the kernel.  (s_nop 4: the wait
+// states after a vector instruction that wrote a scalar operand; s_nop 0: after m0.)
+// The forms for several loads, STEP bytes of LDS apart, wait once.
 __device__ __forceinline__ void load_lds16(u32x4_t rsrc, uint32_t lds, int voffset) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
                "v"(voffset), "s"(rsrc)
@@ -49,6 +49,31 @@ __device__ __forceinline__ void load_lds4(u32x4_t rsrc, uint32_t lds, int voffse
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds),
                "v"(voffset), "s"(rsrc)
                : "memory");
+}
+template <int STEP>
+__device__ __forceinline__ void load_lds16x2(u32x4_t r0, u32x4_t r1, uint32_t lds, int v0, int v1) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+               "s_add_u32 m0, m0, %5\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %4, 0 offen lds" ::"s"(lds),
+               "v"(v0), "v"(v1), "s"(r0), "s"(r1), "n"(STEP)
+               : "memory", "scc");
+}
+// N loads of one buffer
+template <int N, int STEP>
+__device__ __forceinline__ void load_lds16xn(u32x4_t rsrc, uint32_t lds, const int *v) {
+  int i = 0;
+#pragma unroll
+  for (; i + 3 < N; i += 4)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %5, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %5, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %5, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds" ::"s"(
+                     lds + i * STEP),
+                 "v"(v[i]), "v"(v[i + 1]), "v"(v[i + 2]), "v"(v[i + 3]), "s"(rsrc), "n"(STEP)
+                 : "memory", "scc");
+#pragma unroll
+  for (; i + 1 < N; i += 2) load_lds16x2<STEP>(rsrc, rsrc, lds + i * STEP, v[i], v[i + 1]);
+#pragma unroll
+  for (; i < N; ++i) load_lds16(rsrc, lds + i * STEP, v[i]);
 }
 // Waits for the wave's loads, all but the newest N.
 template <int N>

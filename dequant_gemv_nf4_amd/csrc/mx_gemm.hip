@@ -200,25 +200,27 @@ __global__ void __launch_bounds__(64 * WV *KG, (MF * NF > 32 ? 1 : MF * NF > 16 
       const int adv = s * 128 * KS;
       const u32x4_t rs = buffer_words(xbase + adv, max(xbytes - adv, 0));
       const int left = kb * 4 - s * XC;  // chunks of the row from here on
+      int o[XL];
 #pragma unroll
       for (int i = 0; i < XL; ++i) {
         const int idx = (i * WV + wave) * 64 + lane, row = idx / XC;
-        int o = xo[i];
-        if (left < XC) o = (idx % XC ^ x_perm<KS>(row)) < left ? o : kOutside;
-        load_lds16(rs, xaddr + buf * XB + (i * WV + wave) * 1024, o);
+        o[i] = xo[i];
+        if (left < XC) o[i] = (idx % XC ^ x_perm<KS>(row)) < left ? o[i] : kOutside;
       }
+      load_lds16xn<XL, WV * 1024>(rs, xaddr + buf * XB + wave * 1024, o);
     };
     const auto load_w = [&](int buf, int b) {  // b: block of codes
       const int adv = b * 32 * KW;
       const u32x4_t rs = buffer_words(wbase + adv, max(wbytes - adv, 0));
       const int left = kb - b * WC;
+      int o[WL];
 #pragma unroll
       for (int i = 0; i < WL; ++i) {
         const int idx = i * 64 + lane, row = idx / WC;
-        int o = wo[i];
-        if (left < WC) o = (idx % WC ^ w_perm<KS, KW>(row)) < left ? o : kOutside;
-        load_lds16(rs, waddr + buf * WB + i * 1024, o);
+        o[i] = wo[i];
+        if (left < WC) o[i] = (idx % WC ^ w_perm<KS, KW>(row)) < left ? o[i] : kOutside;
       }
+      load_lds16xn<WL, 1024>(rs, waddr + buf * WB, o);
     };
     // Column c * 16 + l16 of the wave has 8 scale bytes a group.  In LDS: NS groups in
     // rotation.  In registers: the three words around them, or two.

@@ -97,18 +97,17 @@ __global__ void __launch_bounds__(64 * WV *KG, MF > 4 ? 1 : 2) mx_grad_kernel(Gr
       const int adv = s * 128;
       const u32x4_t rs = buffer_words(xbase + adv, max(xbytes - adv, 0));
       const int left = (p.N >> 3) - s * 8;
+      int o[XL];
 #pragma unroll
       for (int i = 0; i < XL; ++i) {
         const int idx = (i * WV + wave) * 64 + lane, row = idx >> 3;
-        int o = xo[i];
-        if (left < 8) o = ((idx & 7) ^ dy_perm(row)) < left ? o : kOutside;
-        load_lds16(rs, xaddr + buf * XB + (i * WV + wave) * 1024, o);
+        o[i] = xo[i];
+        if (left < 8) o[i] = ((idx & 7) ^ dy_perm(row)) < left ? o[i] : kOutside;
       }
+      load_lds16xn<XL, WV * 1024>(rs, xaddr + buf * XB + wave * 1024, o);
       const int rows = max(p.N - s * 64, 0);
       const u32x4_t ws = buffer_words(wbase + (int64_t)s * 64 * kc, rows * kc);
-#pragma unroll
-      for (int i = 0; i < WL; ++i)
-        load_lds16(ws, waddr + buf * WB + (i * WV + wave) * 1024, wo[i]);
+      load_lds16xn<WL, WV * 1024>(ws, waddr + buf * WB + wave * 1024, wo);
     };
     // lane: the four block scales of this wave's columns at n = 64 s + lane; rows that
     // are not whole words go through registers, a stage ahead

@@ -32,196 +32,192 @@ __device__ __forceinline__ f32x4_t mfma_scaled(u32x4_t a, uint32_t sa, u32x4_t b
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-// ------------------------------------------------------------ few rows ----
-// 16 CT columns x 16 RT rows a workgroup, K dealt out to its NW waves by steps;
-// tiles meet in LDS and are added in wave order.
-template <int RT, int CT, int NW, typename OUT>
-__global__ void __launch_bounds__(64 * NW) mx_packed_rows_kernel(PackedArgs p) {
-  __shared__ f32x4_t part[NW][RT * CT][64];
+// A workgroup owns 16 NF WN columns x 16 MF WM rows; its waves form KG groups of WN x WM
+// that share out K.  A stage is 128 KS values of k: 64 KS bytes a row of either operand,
+// loaded straight into LDS, NB stages in rotation, one barrier a stage (whole 128-byte
+// pieces: 64-byte ones and a stage more in flight took 8 % longer).  Scales come
+// the same way, 16 bytes (512 k) a row.
+
+// Permutation (XOR) of the 16-byte chunks of a row of 64 KS bytes: the rows that LDS
+// serves together in a fragment read (0-3 and 12-15 of one lane quarter with 4-11
+// of the next) fall into different banks.
+template <int KS>
+__device__ __forceinline__ int row_perm(int row) {
+  return KS == 2 ? (row >> 1) & 7 : ((row >> 2) & 3) | (row & 3) << 2;
+}
+
+template <int WN, int WM, int NF, int MF, int KS, int KG, int NB, bool SVEC, typename OUT>
+__global__ void __launch_bounds__(64 * WN *WM *KG, NF *MF > 16 ? 1 : 2) mx_packed_kernel(PackedArgs p) {
+  constexpr int WV = WN * WM, BN = 16 * NF * WN, BM = 16 * MF * WM, ROWS = BN + BM;
+  constexpr int RB = 64 * KS, RC = 4 * KS, RL = 1024 / RB;  // bytes and chunks a row, rows a load
+  constexpr int TB = ROWS * RB, L = TB / 1024 / WV;  // bytes of a stage, loads a wave
+  constexpr int SG = 4 / KS;                         // stages per scale load
+  constexpr int S = (ROWS + 64 * WV - 1) / (64 * WV), SB = S * WV * 1024, NS = SG == 1 ? 3 : 2;
+  static_assert(L * WV * 1024 == TB && BN % 64 == 0, "whole loads");
+  __shared__ __attribute__((aligned(1024))) uint8_t shared[KG][NB * TB + NS * SB];
   int slot, block;
   if (!grid_item(p.grid, &slot, &block)) return;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int l16 = lane & 15, q = lane >> 4;
-  const int n0 = block * 16 * CT, cols = min(16 * CT, p.N - n0);
-  const int64_t m0 = (int64_t)slot * 16 * RT;
-  const int rows = (int)min((int64_t)16 * RT, p.M - m0);
-  const int kb = p.K >> 5, kc = p.K >> 1;
-  const __amdgpu_buffer_rsrc_t crs = buffer(p.codes + (int64_t)n0 * kc, (int64_t)cols * kc);
-  const __amdgpu_buffer_rsrc_t srs = buffer(p.scales + (int64_t)n0 * kb, (int64_t)cols * kb);
-  const __amdgpu_buffer_rsrc_t xrs = buffer(p.xcodes + m0 * kc, (int64_t)rows * kc);
-  const __amdgpu_buffer_rsrc_t ars = buffer(p.xscales + m0 * kb, (int64_t)rows * kb);
-  f32x4_t acc[RT][CT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) acc[r][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int steps = (kb + 3) >> 2;
-  constexpr int U = 2;
-  for (int s0 = wave; s0 < steps; s0 += NW * U) {
-    u32x4_t cw[U][CT], xw[U][RT];
-    uint32_t cs[U][CT], xb[U][RT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int b = (s0 + u * NW) * 4 + q;
-      const int out = b < kb ? 0 : kOutside;
-#pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        const int n = c * 16 + l16;
-        cw[u][c] = __builtin_amdgcn_raw_buffer_load_b128(crs, (n * kc + b * 16) | out, 0, kLoadStream);
-        cs[u][c] = __builtin_amdgcn_raw_buffer_load_b8(srs, (n * kb + b) | out, 0, 0);
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int m = r * 16 + l16;
-        xw[u][r] = __builtin_amdgcn_raw_buffer_load_b128(xrs, (m * kc + b * 16) | out, 0, 0);
-        xb[u][r] = __builtin_amdgcn_raw_buffer_load_b8(ars, (m * kb + b) | out, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-          acc[r][c] = mfma_scaled(cw[u][c], cs[u][c], xw[u][r], xb[u][r], acc[r][c]);
-  }
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) part[wave][r * CT + c][lane] = acc[r][c];
-  __syncthreads();
-  OUT *Y = reinterpret_cast<OUT *>(p.Y);
-  const bool vec = (p.N & 3) == 0;
-  for (int i = threadIdx.x; i < RT * CT * 64; i += 64 * NW) {
-    const int f = i >> 6, l = i & 63;
-    f32x4_t v = part[0][f][l];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) v += part[w][f][l];
-    const int m = f / CT * 16 + (l & 15);
-    const int n = n0 + f % CT * 16 + (l >> 4) * 4;
-    if (m < rows) store4<OUT>(Y + (m0 + m) * p.N, n, p.N, v, vec);
-  }
-}
-
-// ----------------------------------------------------------- many rows ----
-// A workgroup owns a 256 x 256 tile; WN x WM waves, each 16 NF columns x 16 MF
-// rows.  A stage is 256 k: 128 bytes a row of either operand, loaded straight into
-// LDS (16-byte chunk c of a row at chunk c ^ (row / 2 % 8), so that the 16
-// rows of a fragment fall into different banks), and 8 scale bytes a row;
-// double-buffered, one barrier a stage.
-template <int WN, int WM, int NF, int MF, bool SVEC, typename OUT>
-__global__ void __launch_bounds__(64 * WN * WM, WN *WM / 4) mx_packed_tile_kernel(PackedArgs p) {
-  constexpr int BN = 16 * NF * WN, BM = 16 * MF * WM, NT = 64 * WN * WM, ROWS = BN + BM;
-  __shared__ __attribute__((aligned(1024))) uint8_t tile[2][ROWS * 128];
-  __shared__ u32x2_t sc[2][ROWS];
-  int slot, block;
-  if (!grid_item(p.grid, &slot, &block)) return;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wave = wave_all % WV, kg = wave_all / WV;
   const int l16 = lane & 15, q = lane >> 4;
   const int wn = wave % WN, wm = wave / WN;
   const int n0 = block * BN, cols = min(BN, p.N - n0);
   const int64_t m0 = (int64_t)slot * BM;
   const int rows = (int)min((int64_t)BM, p.M - m0);
   const int kb = p.K >> 5, kc = p.K >> 1;
-  const u32x4_t crs = buffer_words(p.codes + (int64_t)n0 * kc, cols * kc);
-  const __amdgpu_buffer_rsrc_t srs = buffer(p.scales + (int64_t)n0 * kb, (int64_t)cols * kb);
-  const u32x4_t xrs = buffer_words(p.xcodes + m0 * kc, rows * kc);
-  const __amdgpu_buffer_rsrc_t ars = buffer(p.xscales + m0 * kb, (int64_t)rows * kb);
+  const uint8_t *const wbase = p.codes + (int64_t)n0 * kc, *const xbase = p.xcodes + m0 * kc;
+  const uint8_t *const wsbase = p.scales + (int64_t)n0 * kb, *const xsbase = p.xscales + m0 * kb;
   f32x4_t acc[NF][MF];
 #pragma unroll
   for (int c = 0; c < NF; ++c)
 #pragma unroll
     for (int r = 0; r < MF; ++r) acc[c][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int stages = (kb + 7) >> 3;
-  const uint32_t tiles = lds_address(tile);
-  // a wave's load covers 8 rows, the first one 8 (wave + a multiple of 2); lane: row
-  // lane / 8, chunk (lane % 8) ^ (row / 2 % 8)
-  static_assert(WN * WM % 2 == 0, "row / 2 % 8 of a load depends on the wave alone");
-  const int lrow = lane >> 3, lchunk = (lane & 7) ^ ((wave & 1) * 4 + (lrow >> 1));
-  const auto load_codes = [&](int buf, int s) {
-    const int out = s * 8 + lchunk < kb ? 0 : kOutside;
+  const int groups = (kb + 15) >> 4, per = (groups + KG - 1) / KG, g0 = kg * per;
+  uint8_t *const tiles = shared[kg], *const slds = shared[kg] + NB * TB;
+  const uint32_t taddr = lds_address(tiles), saddr = lds_address(slds);
+  // load i of a wave: RL rows from row (i * WV + wave) * RL on, of W up to BN, then of X
+  int vo[L];
 #pragma unroll
-    for (int i = 0; i < BN / 8 / (WN * WM); ++i) {
-      const int r = (i * WN * WM + wave) * 8;
-      load_lds16(crs, tiles + buf * ROWS * 128 + r * 128, ((r + lrow) * kc + s * 128 + lchunk * 16) | out);
-    }
+  for (int i = 0; i < L; ++i) {
+    const int row = (i * WV + wave) * RL + lane / RC;
+    vo[i] = (row < BN ? row : row - BN) * kc + ((lane % RC) ^ row_perm<KS>(row)) * 16;
+  }
+  const auto load_stage = [&](int buf, int s) {
+    const int adv = s * RB;
+    const u32x4_t wrs = buffer_words(wbase + adv, max(cols * kc - adv, 0));
+    const u32x4_t xrs = buffer_words(xbase + adv, max(rows * kc - adv, 0));
+    const int left = kb - s * RC;
+    int o[L];
 #pragma unroll
-    for (int i = 0; i < BM / 8 / (WN * WM); ++i) {
-      const int r = (i * WN * WM + wave) * 8;
-      load_lds16(xrs, tiles + buf * ROWS * 128 + (BN + r) * 128, ((r + lrow) * kc + s * 128 + lchunk * 16) | out);
+    for (int i = 0; i < L; ++i) {
+      o[i] = vo[i];
+      if (left < RC)
+        o[i] = ((lane % RC) ^ row_perm<KS>((i * WV + wave) * RL + lane / RC)) < left ? o[i] : kOutside;
     }
+    const uint32_t at = taddr + buf * TB + wave * 1024;
+    const auto rs = [&](int i) { return (i * WV + wave) * RL < BN ? wrs : xrs; };
+#pragma unroll
+    for (int i = 0; i + 1 < L; i += 2)
+      load_lds16x2<WV * 1024>(rs(i), rs(i + 1), at + i * WV * 1024, o[i], o[i + 1]);
+    if constexpr (L % 2 == 1) load_lds16(rs(L - 1), at + (L - 1) * WV * 1024, o[L - 1]);
   };
-  // scales: thread -> rows tid, tid + NT, ... of the BN + BM
-  constexpr int SR = (ROWS + NT - 1) / NT;
-  u32x2_t sreg[SR];
-  const auto load_scales = [&](int s) {
+  uint32_t sreg[S][5];
+  const auto load_scales = [&](int buf, int g) {
 #pragma unroll
-    for (int i = 0; i < SR; ++i) {
-      const int r = i * NT + tid;
-      const bool w = r < BN;
-      const int off = (w ? r : r - BN) * kb + s * 8;
-      if constexpr (SVEC) {
-        // rows are whole words: two words, each inside the row or outside
-        const int o0 = r < ROWS && s * 8 < kb ? off : kOutside;
-        const int o1 = r < ROWS && s * 8 + 4 < kb ? off + 4 : kOutside;
-        const uint32_t a0 = __builtin_amdgcn_raw_buffer_load_b32(srs, w ? o0 : kOutside, 0, 0);
-        const uint32_t a1 = __builtin_amdgcn_raw_buffer_load_b32(srs, w ? o1 : kOutside, 0, 0);
-        const uint32_t b0 = __builtin_amdgcn_raw_buffer_load_b32(ars, w ? kOutside : o0, 0, 0);
-        const uint32_t b1 = __builtin_amdgcn_raw_buffer_load_b32(ars, w ? kOutside : o1, 0, 0);
-        sreg[i] = u32x2_t{a0 | b0, a1 | b1};
+    for (int i = 0; i < S; ++i) {
+      const int row0 = (i * WV + wave) * 64;
+      const bool w = row0 < BN;
+      const int o = (row0 + lane - (w ? 0 : BN)) * kb;
+      if constexpr (SVEC) {  // rows are whole words
+        const u32x4_t rs = buffer_words((w ? wsbase : xsbase) + g * 16, max((w ? cols : rows) * kb - g * 16, 0));
+        load_lds16(rs, saddr + buf * SB + row0 * 16, o);
       } else {
-        uint32_t v[2] = {0u, 0u};
+        const LooseWords loose(w ? wsbase : xsbase, (int64_t)(w ? cols : rows) * kb);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int o = r < ROWS && s * 8 + k < kb ? off + k : kOutside;
-          const uint32_t a = __builtin_amdgcn_raw_buffer_load_b8(srs, w ? o : kOutside, 0, 0);
-          const uint32_t b = __builtin_amdgcn_raw_buffer_load_b8(ars, w ? kOutside : o, 0, 0);
-          v[k >> 2] |= (a | b) << (8 * (k & 3));
-        }
-        sreg[i] = u32x2_t{v[0], v[1]};
+        for (int k = 0; k < 5; ++k) sreg[i][k] = loose.fetch(o + g * 16, k);
       }
     }
   };
-  load_codes(0, 0);
-  load_scales(0);
-  for (int s = 0; s < stages; ++s) {
-    const int buf = s & 1;
+  const auto put_scales = [&](int buf, int g) {  // !SVEC
 #pragma unroll
-    for (int i = 0; i < SR; ++i)
-      if (i * NT + tid < ROWS) sc[buf][i * NT + tid] = sreg[i];
-    lds_loads_but<0>();
-    __syncthreads();  // the stage is in LDS, the other buffer is free
-    if (s + 1 < stages) {
-      load_codes(buf ^ 1, s + 1);
-      load_scales(s + 1);
+    for (int i = 0; i < S; ++i) {
+      const int row0 = (i * WV + wave) * 64;
+      const bool w = row0 < BN;
+      const LooseWords loose(w ? wsbase : xsbase, 0);
+      const int o = (row0 + lane - (w ? 0 : BN)) * kb + g * 16;
+      u32x4_t v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = loose.word(o, sreg[i][k], sreg[i][k + 1]);
+      *reinterpret_cast<u32x4_t *>(slds + buf * SB + (row0 + lane) * 16) = v;
     }
-    const uint8_t *wt = &tile[buf][(wn * 16 * NF + l16) * 128];
-    const uint8_t *xt = &tile[buf][(BN + wm * 16 * MF + l16) * 128];
-    u32x2_t sw[NF], sx[MF];
+  };
+  // The fragments of 128 k: lane l has row l % 16 and block l / 16 of either operand.
+  struct Frags {
+    u32x4_t a[NF], b[MF];
+    uint32_t as[NF], bs[MF];
+  };
+  const auto read = [&](Frags &f, int buf, int sbuf, int u, int s, int h) __attribute__((always_inline)) {
+    const uint8_t *wt = tiles + buf * TB + (wn * 16 * NF + l16) * RB;
+    const uint8_t *xt = tiles + buf * TB + (BN + wm * 16 * MF + l16) * RB;
+    const uint8_t *ws = slds + sbuf * SB + (wn * 16 * NF + l16) * 16 + (u * KS + h) * 4;
+    const uint8_t *xs = slds + sbuf * SB + (BN + wm * 16 * MF + l16) * 16 + (u * KS + h) * 4;
+    // scale bytes past the row's end are the next row's, perhaps NaN
+    const int left = kb - (s * KS + h) * 4;
+    const uint32_t own = left >= 4 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - 8 * left);
+    const int ch = ((h * 4 + q) ^ row_perm<KS>(l16)) * 16;
 #pragma unroll
-    for (int c = 0; c < NF; ++c) sw[c] = sc[buf][wn * 16 * NF + c * 16 + l16];
-#pragma unroll
-    for (int r = 0; r < MF; ++r) sx[r] = sc[buf][BN + wm * 16 * MF + r * 16 + l16];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int ch = ((h * 4 + q) ^ (l16 >> 1)) * 16;
-      u32x4_t b[MF];
-      uint32_t bs[MF];
-#pragma unroll
-      for (int r = 0; r < MF; ++r) {
-        b[r] = *reinterpret_cast<const u32x4_t *>(xt + r * 2048 + ch);
-        bs[r] = sx[r][h] >> (8 * q);
-      }
-#pragma unroll
-      for (int c = 0; c < NF; ++c) {
-        const u32x4_t a = *reinterpret_cast<const u32x4_t *>(wt + c * 2048 + ch);
-        const uint32_t as = sw[c][h] >> (8 * q);
-#pragma unroll
-        for (int r = 0; r < MF; ++r) acc[c][r] = mfma_scaled(a, as, b[r], bs[r], acc[c][r]);
-      }
+    for (int r = 0; r < MF; ++r) {
+      f.b[r] = *reinterpret_cast<const u32x4_t *>(xt + r * 16 * RB + ch);
+      f.bs[r] = (*reinterpret_cast<const uint32_t *>(xs + r * 256) & own) >> (8 * q);
     }
+#pragma unroll
+    for (int c = 0; c < NF; ++c) {
+      f.a[c] = *reinterpret_cast<const u32x4_t *>(wt + c * 16 * RB + ch);
+      f.as[c] = (*reinterpret_cast<const uint32_t *>(ws + c * 256) & own) >> (8 * q);
+    }
+  };
+  const auto multiply = [&](const Frags &f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < NF; ++c)
+#pragma unroll
+      for (int r = 0; r < MF; ++r) acc[c][r] = mfma_scaled(f.a[c], f.as[c], f.b[r], f.bs[r], acc[c][r]);
+  };
+  constexpr int ss = SVEC ? S : 0;
+  int buf = 0, sbuf = 0;
+  load_scales(0, g0);
+  load_stage(0, g0 * SG);
+  if constexpr (SVEC && SG == 1) load_scales(1, g0 + 1);
+#pragma unroll
+  for (int i = 1; i < NB - 1; ++i) load_stage(i, g0 * SG + i);
+  for (int g = g0; g < g0 + per; ++g) {
+#pragma unroll
+    for (int u = 0; u < SG; ++u) {
+      const int s = g * SG + u;
+      if (!SVEC && u == 0) put_scales(sbuf, g);
+      // in flight may stay (NB = 3) the next stage and the scales asked for before it
+      if (NB == 2)
+        lds_loads_but<0>();
+      else
+        SG == 1 || u == 1 ? lds_loads_but<L + ss>() : lds_loads_but<L>();
+      __syncthreads();  // stage s is in LDS; the buffer of the last one is free
+      if (u == 0) {
+        if constexpr (SVEC && SG == 1)
+          load_scales(sbuf == 0 ? 2 : sbuf - 1, g + 2);
+        else
+          load_scales(sbuf == NS - 1 ? 0 : sbuf + 1, g + 1);
+      }
+      load_stage(buf == 0 ? NB - 1 : buf - 1, s + NB - 1);
+#pragma unroll
+      for (int h = 0; h < KS; ++h) {
+        Frags f;
+        read(f, buf, sbuf, u, s, h);
+        multiply(f);
+      }
+      buf = buf == NB - 1 ? 0 : buf + 1;
+    }
+    sbuf = sbuf == NS - 1 ? 0 : sbuf + 1;
+  }
+  lds_loads_but<0>();
+  if constexpr (KG > 1) {
+    static_assert(sizeof(shared) >= (KG - 1) * WV * 64 * NF * MF * 16, "partial tiles fit the stages");
+    f32x4_t *part = reinterpret_cast<f32x4_t *>(&shared[0][0]);  // [kg - 1][wave][f][lane]
+    __syncthreads();
+    if (kg > 0)
+#pragma unroll
+      for (int c = 0; c < NF; ++c)
+#pragma unroll
+        for (int r = 0; r < MF; ++r)
+          part[(((kg - 1) * WV + wave) * NF * MF + c * MF + r) * 64 + lane] = acc[c][r];
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int c = 0; c < NF; ++c)
+#pragma unroll
+        for (int r = 0; r < MF; ++r)
+          acc[c][r] += part[((g * WV + wave) * NF * MF + c * MF + r) * 64 + lane];
   }
   OUT *Y = reinterpret_cast<OUT *>(p.Y);
   const bool vec = (p.N & 3) == 0;
@@ -236,41 +232,50 @@ __global__ void __launch_bounds__(64 * WN * WM, WN *WM / 4) mx_packed_tile_kerne
   }
 }
 
-template <int RT, int CT, int NW>
-static hipError_t launch_packed_rows(PackedArgs &a, int out_dtype, hipStream_t s) {
-  a.grid = make_grid((a.M + 16 * RT - 1) / (16 * RT), (a.N + 16 * CT - 1) / (16 * CT), 8);
-  const int64_t n = grid_size(a.grid);
-  if (n * 64 * NW >= (int64_t(1) << 32)) return hipErrorInvalidValue;
-  if (out_dtype == NF4_F32)
-    hipLaunchKernelGGL((mx_packed_rows_kernel<RT, CT, NW, float>), dim3((unsigned)n), dim3(64 * NW),
-                       0, s, a);
-  else
-    hipLaunchKernelGGL((mx_packed_rows_kernel<RT, CT, NW, uint16_t>), dim3((unsigned)n),
-                       dim3(64 * NW), 0, s, a);
-  return hipGetLastError();
-}
-
-template <int WN, int WM, int NF, int MF, bool SVEC>
-static hipError_t launch_packed_tile(PackedArgs &a, int out_dtype, hipStream_t s) {
-  constexpr int BN = 16 * NF * WN, BM = 16 * MF * WM, NT = 64 * WN * WM;
+template <int WN, int WM, int NF, int MF, int KS, int KG, int NB, bool SVEC>
+static hipError_t launch_packed_as(PackedArgs &a, int out_dtype, hipStream_t s) {
+  constexpr int BN = 16 * NF * WN, BM = 16 * MF * WM, NT = 64 * WN * WM * KG;
   a.grid = make_grid((a.M + BM - 1) / BM, (a.N + BN - 1) / BN, 8);
   const int64_t n = grid_size(a.grid);
   if (n * NT >= (int64_t(1) << 32)) return hipErrorInvalidValue;
   if (out_dtype == NF4_F32)
-    hipLaunchKernelGGL((mx_packed_tile_kernel<WN, WM, NF, MF, SVEC, float>), dim3((unsigned)n),
+    hipLaunchKernelGGL((mx_packed_kernel<WN, WM, NF, MF, KS, KG, NB, SVEC, float>), dim3((unsigned)n),
                        dim3(NT), 0, s, a);
   else
-    hipLaunchKernelGGL((mx_packed_tile_kernel<WN, WM, NF, MF, SVEC, uint16_t>), dim3((unsigned)n),
+    hipLaunchKernelGGL((mx_packed_kernel<WN, WM, NF, MF, KS, KG, NB, SVEC, uint16_t>), dim3((unsigned)n),
                        dim3(NT), 0, s, a);
   return hipGetLastError();
 }
 
+template <int WN, int WM, int NF, int MF, int KS, int KG, int NB>
+static hipError_t launch_tile(PackedArgs &a, int out_dtype, hipStream_t s) {
+  if (a.K % 128 == 0 && aligned_to(a.scales, 4) && aligned_to(a.xscales, 4))
+    return launch_packed_as<WN, WM, NF, MF, KS, KG, NB, true>(a, out_dtype, s);
+  return launch_packed_as<WN, WM, NF, MF, KS, KG, NB, false>(a, out_dtype, s);
+}
+
+// The largest tile that is not mostly empty and leaves few CUs without one, else a
+// small one with K shared out inside the workgroup.  Measured (us), M x N x K: 4096 x 28672 x
+// 4096: 256 x 256 tiles 314, 128 x 128 354; 2048 x 4096 x 14336: 128 x 128 79 (512
+// tiles), 256 x 256 111 (128); 512 x 4096 x 4096: 64 x 128 13.7, 128 x 128 18.1; 256 x
+// 4096 x 4096: 64 x 64 with two K-groups 9.4, with one 10.0; 37 x 6144 x 4096: 32 x 64
+// with two 7.4, 64 x 64 with two 8.5; 16 x 4096 x 14336: 16 x 64 with two 13.2, with
+// one 15.8; 1 x 28672 x 4096: with two 16.4, with one 14.5.
 static hipError_t launch_packed(PackedArgs &a, int out_dtype, hipStream_t s) {
-  if (a.M <= 16) return launch_packed_rows<1, 1, 8>(a, out_dtype, s);
-  if (a.M <= 128) return launch_packed_rows<2, 2, 4>(a, out_dtype, s);
-  const bool svec = a.K % 128 == 0 && aligned_to(a.scales, 4) && aligned_to(a.xscales, 4);
-  if (svec) return launch_packed_tile<2, 4, 8, 4, true>(a, out_dtype, s);
-  return launch_packed_tile<2, 4, 8, 4, false>(a, out_dtype, s);
+  const auto tiles = [&](int bm, int bn) {
+    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+  };
+  constexpr int kFill = 192;
+  if (a.M > 128 && tiles(256, 256) >= kFill)
+    return launch_tile<2, 4, 8, 4, 2, 1, 2>(a, out_dtype, s);
+  if (a.M > 64 && tiles(128, 128) >= kFill) return launch_tile<2, 2, 4, 4, 2, 1, 2>(a, out_dtype, s);
+  if (a.M > 32) {
+    if (tiles(64, 128) >= kFill) return launch_tile<2, 2, 4, 2, 2, 1, 3>(a, out_dtype, s);
+    if (tiles(64, 64) >= kFill) return launch_tile<2, 2, 2, 2, 2, 2, 3>(a, out_dtype, s);
+  }
+  if (a.M > 16 && tiles(32, 64) >= 64) return launch_tile<4, 1, 1, 2, 2, 2, 3>(a, out_dtype, s);
+  if (tiles(16, 64) >= 384) return launch_tile<4, 1, 1, 1, 4, 1, 2>(a, out_dtype, s);
+  return launch_tile<4, 1, 1, 1, 4, 2, 3>(a, out_dtype, s);
 }
 
 }  // namespace mx
