@@ -666,10 +666,14 @@ def mx_pack(W, stream=None, check=True):
     that hold NaN or infinity (a host synchronisation)."""
     _need(W, "W", _FLOATS, (2,))
     N, K = W.shape
-    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
-    scales = torch.empty((N, K // MX_BLOCK), dtype=torch.uint8, device=W.device)
-    status = torch.empty(1, dtype=torch.int32, device=W.device) if check else None
-    nf4_mx_pack(W, codes, scales, status, stream)
+    if K % MX_BLOCK:
+        raise ValueError(f"each block of {MX_BLOCK} along K needs scales of its own: K = {K}")
+    dev = W.device
+    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((N, K // MX_BLOCK), dtype=torch.uint8, device=dev)
+    status = torch.empty(1, dtype=torch.int32, device=dev) if check else None
+    _run("nf4_mx_pack", (W,), (W.data_ptr(), _DTYPE[W.dtype], N, K, codes.data_ptr(),
+                               scales.data_ptr(), _addr(status)), stream)
     if check:
         ts = stream
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
@@ -720,7 +724,9 @@ def moe_sort(experts, num_experts, stream=None):
     offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
     order = torch.empty(experts.numel(), dtype=torch.int32, device=dev)
     place = torch.empty(experts.shape, dtype=torch.int32, device=dev)
-    nf4_moe_sort(experts, num_experts, offsets, order, place, None, stream)
+    T, topk = experts.shape
+    _run("nf4_moe_sort", (experts,), (experts.data_ptr(), T, topk, num_experts, offsets.data_ptr(),
+                                      order.data_ptr(), place.data_ptr(), None), stream)
     return offsets, order, place
 
 

@@ -14,27 +14,44 @@ namespace nf4 {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------ sort ----
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
+// Each wave owns up to kSortGroups groups of 64 consecutive slots, whose keys it holds in
+// registers from one load.  Up to 64 * kSortGroups slots a wave one workgroup counts,
+// scans and ranks by itself; beyond that three kernels do, a workgroup per chunk.
+constexpr int kSortGroups = 8;
 constexpr int kSortMaxE = NF4_MOE_MAX_E;
-// Slots one workgroup sorts.  At least kSortMaxE + 1, so that a chunk's counts
-// fit the part of `place` that belongs to the chunk.
-constexpr int kSortChunk = 4096;
-static_assert(kSortMaxE < kSortThreads && kSortMaxE < kSortChunk, "one thread per key");
+// Slots of a chunk (the last one takes what is left, less than two chunks).  More
+// than kSortMaxE, so that a chunk's counts fit the part of `place` that is the chunk's.
+constexpr int kSortChunk = 2048;
+constexpr int kChunkWaves = 8;
+static_assert(kSortMaxE < kSortChunk && 2 * kSortChunk <= kChunkWaves * 64 * kSortGroups, "chunks");
+static_assert(kSortMaxE < 1024, "one thread per key in the scan");
 
-__device__ __forceinline__ int sort_key(const int64_t *experts, int64_t f, int E, int *bad) {
-  const int64_t id = experts[f];
-  const bool in = id >= 0 && id < E;
-  if (!in && id != -1) *bad = 1;
-  return in ? (int)id : E;
+// Keys of the wave's slots from `a` up to `b` (kept, ~none above E): lane l of group i
+// holds slot a + 64 i + l.  Returns whether an id was neither -1 nor an expert.
+__device__ __forceinline__ bool load_keys(const int64_t *experts, int64_t a, int64_t b, int E,
+                                          int lane, int key[kSortGroups]) {
+  int64_t id[kSortGroups];
+#pragma unroll
+  for (int i = 0; i < kSortGroups; ++i) {
+    const int64_t f = a + i * 64 + lane;
+    id[i] = f < b ? experts[f] : -1;
+  }
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kSortGroups; ++i) {
+    const bool in = id[i] >= 0 && id[i] < E;
+    bad |= !in && id[i] != -1;
+    key[i] = in ? (int)id[i] : E;
+  }
+  return bad;
 }
 
-// Counts of this wave's slots [f0, f1) per key, into cnt[0 .. E].
-__device__ __forceinline__ int count_keys(const int64_t *experts, int64_t f0, int64_t f1, int E,
-                                          int *cnt, int lane) {
-  int bad = 0;
-  for (int64_t f = f0 + lane; f < f1; f += 64) atomicAdd(&cnt[sort_key(experts, f, E, &bad)], 1);
-  return bad;
+// Adds the wave's keys to cnt[0 .. E].
+__device__ __forceinline__ void count_keys(const int key[kSortGroups], int64_t a, int64_t b,
+                                           int *cnt, int lane) {
+#pragma unroll
+  for (int i = 0; i < kSortGroups; ++i)
+    if (a + i * 64 + lane < b) atomicAdd(&cnt[key[i]], 1);
 }
 
 // Lanes of the wave that hold the same key, by one ballot per key bit.
@@ -48,7 +65,8 @@ __device__ __forceinline__ uint64_t same_key(int key, bool active, int bits) {
   return m;
 }
 
-// Exclusive prefix over the threads of the workgroup (kSortThreads).
+// Exclusive prefix over the threads of the workgroup.
+template <int WAVES>
 __device__ __forceinline__ int block_exclusive(int v, int *wsum) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int s = v;
@@ -61,52 +79,54 @@ __device__ __forceinline__ int block_exclusive(int v, int *wsum) {
   __syncthreads();
   int base = 0;
 #pragma unroll
-  for (int w = 0; w < kSortWaves; ++w) base += w < wave ? wsum[w] : 0;
+  for (int w = 0; w < WAVES; ++w) base += w < wave ? wsum[w] : 0;
   return base + s - v;
 }
 
-// The chunk of workgroup b: kSortChunk slots, the last one with what is left.
-__device__ __forceinline__ void sort_chunk(int64_t R, int64_t *f0, int64_t *f1) {
+// The slots of workgroup b, then of a wave: runs in slot order.
+template <int WAVES>
+__device__ __forceinline__ void wave_slots(int64_t R, int64_t *f0, int64_t *a, int64_t *b) {
   *f0 = (int64_t)blockIdx.x * kSortChunk;
-  *f1 = blockIdx.x + 1 == gridDim.x ? R : *f0 + kSortChunk;
-}
-
-// Each wave's slots lie together, in order, so ranks follow the slot order.
-__device__ __forceinline__ void wave_range(int64_t f0, int64_t f1, int64_t *a, int64_t *b) {
-  const int64_t groups = (f1 - f0 + 63) / 64;
-  const int64_t per = (groups + kSortWaves - 1) / kSortWaves * 64;
-  const int64_t lo = f0 + (threadIdx.x >> 6) * per;
+  const int64_t f1 = blockIdx.x + 1 == gridDim.x ? R : *f0 + kSortChunk;
+  const int64_t groups = (f1 - *f0 + 63) / 64;
+  const int64_t per = (groups + WAVES - 1) / WAVES * 64;
+  const int64_t lo = *f0 + (threadIdx.x >> 6) * per;
   *a = lo < f1 ? lo : f1;
   *b = lo + per < f1 ? lo + per : f1;
 }
 
-__global__ void __launch_bounds__(kSortThreads)
+__global__ void __launch_bounds__(64 * kChunkWaves)
     moe_count_kernel(const int64_t *__restrict__ experts, int64_t R, int E,
                      int32_t *__restrict__ place, int32_t *status) {
   __shared__ int cnt[kSortMaxE + 1];
-  int64_t f0, f1, a, b;
-  sort_chunk(R, &f0, &f1);
-  for (int e = threadIdx.x; e <= E; e += kSortThreads) cnt[e] = 0;
+  int64_t f0, a, b;
+  wave_slots<kChunkWaves>(R, &f0, &a, &b);
+  const int lane = threadIdx.x & 63;
+  int key[kSortGroups];
+  const bool bad = load_keys(experts, a, b, E, lane, key);
+  for (int e = threadIdx.x; e <= E; e += 64 * kChunkWaves) cnt[e] = 0;
   __syncthreads();
-  wave_range(f0, f1, &a, &b);
-  const int bad = count_keys(experts, a, b, E, cnt, threadIdx.x & 63);
+  count_keys(key, a, b, cnt, lane);
   if (bad && status) atomicOr(status, NF4_MOE_BAD_ID);
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += kSortThreads) place[f0 + e] = cnt[e];
+  for (int e = threadIdx.x; e <= E; e += 64 * kChunkWaves) place[f0 + e] = cnt[e];
 }
 
-// One workgroup: the chunks' counts become each chunk's first row per key.
-__global__ void __launch_bounds__(kSortThreads)
+// One workgroup: the chunks' counts become each chunk's first row per key.  Thread e
+// has key e; key E (no expert) follows every expert's rows.
+__global__ void __launch_bounds__(1024)
     moe_scan_kernel(int nchunks, int E, int32_t *__restrict__ place, int32_t *__restrict__ offsets) {
-  __shared__ int wsum[kSortWaves];
-  // thread e has key e; key E (no expert) follows every expert's rows
+  __shared__ int wsum[16];
   const int e = threadIdx.x;
   int n = 0;
   if (e <= E)
-    for (int c = 0; c < nchunks; ++c) n += place[(int64_t)c * kSortChunk + e];
-  int row = block_exclusive(n, wsum);
-  if (e <= E) offsets[e] = row;
+    for (int c0 = 0; c0 < nchunks; c0 += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n += c0 + i < nchunks ? place[(int64_t)(c0 + i) * kSortChunk + e] : 0;
+    }
+  int row = block_exclusive<16>(n, wsum);
   if (e > E) return;
+  offsets[e] = row;
   for (int c0 = 0; c0 < nchunks; c0 += 8) {
     int v[8];
 #pragma unroll
@@ -121,61 +141,65 @@ __global__ void __launch_bounds__(kSortThreads)
 }
 
 // Ranks and writes a chunk's slots.  SINGLE: the chunk is everything, and this
-// kernel counts and scans by itself (one launch for up to 2 * kSortChunk - 1 slots).
-template <bool SINGLE>
-__global__ void __launch_bounds__(kSortThreads)
+// kernel counts and scans by itself (E < 64 WAVES).
+template <int WAVES, bool SINGLE>
+__global__ void __launch_bounds__(64 * WAVES)
     moe_scatter_kernel(const int64_t *__restrict__ experts, int64_t R, int E, int bits,
                        int32_t *__restrict__ offsets, int32_t *__restrict__ order,
                        int32_t *__restrict__ place, int32_t *status) {
-  extern __shared__ int cnt[];  // [kSortWaves][E + 1], then wave sums
-  int *wsum = cnt + kSortWaves * (E + 1);
+  extern __shared__ int cnt[];  // [WAVES][E + 1], then wave sums
+  int *wsum = cnt + WAVES * (E + 1);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t f0, f1, a, b;
-  sort_chunk(R, &f0, &f1);
-  for (int i = threadIdx.x; i < kSortWaves * (E + 1); i += kSortThreads) cnt[i] = 0;
+  int64_t f0, a, b;
+  wave_slots<WAVES>(R, &f0, &a, &b);
+  int key[kSortGroups];
+  const bool bad = load_keys(experts, a, b, E, lane, key);
+  for (int i = threadIdx.x; i < WAVES * (E + 1); i += 64 * WAVES) cnt[i] = 0;
   __syncthreads();
-  wave_range(f0, f1, &a, &b);
   int *mine = cnt + wave * (E + 1);
-  const int bad = count_keys(experts, a, b, E, mine, lane);
+  count_keys(key, a, b, mine, lane);
   if (SINGLE && bad && status) atomicOr(status, NF4_MOE_BAD_ID);
   __syncthreads();
   // first row of each key in this chunk, then of each wave
   const int e = threadIdx.x;
-  int base = 0;
   if constexpr (SINGLE) {
     int n = 0;
     if (e <= E)
-      for (int w = 0; w < kSortWaves; ++w) n += cnt[w * (E + 1) + e];
-    base = block_exclusive(n, wsum);
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) n += cnt[w * (E + 1) + e];
+    const int base = block_exclusive<WAVES>(n, wsum);
+    if (e <= E) offsets[e] = base;
     if (e <= E) {
-      offsets[e] = base;
-      for (int w = 0; w < kSortWaves; ++w) {
+      int row = base;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
         const int v = cnt[w * (E + 1) + e];
-        cnt[w * (E + 1) + e] = base;
-        base += v;
+        cnt[w * (E + 1) + e] = row;
+        row += v;
       }
     }
   } else {
-    for (int k = e; k <= E; k += kSortThreads) {
-      base = place[f0 + k];
-      for (int w = 0; w < kSortWaves; ++w) {
+    for (int k = e; k <= E; k += 64 * WAVES) {
+      int row = place[f0 + k];
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
         const int v = cnt[w * (E + 1) + k];
-        cnt[w * (E + 1) + k] = base;
-        base += v;
+        cnt[w * (E + 1) + k] = row;
+        row += v;
       }
     }
   }
   __syncthreads();  // also: this chunk's part of `place` is read before it is written
   const uint64_t below = lane ? ~uint64_t(0) >> (64 - lane) : 0;
-  for (int64_t g = a; g < b; g += 64) {
-    const int64_t f = g + lane;
+#pragma unroll
+  for (int i = 0; i < kSortGroups; ++i) {
+    const int64_t f = a + i * 64 + lane;
+    if (a + i * 64 >= b) break;
     const bool active = f < b;
-    int ignored = 0;
-    const int key = active ? sort_key(experts, f, E, &ignored) : 0;
-    const uint64_t peers = same_key(key, active, bits);
+    const uint64_t peers = same_key(active ? key[i] : 0, active, bits);
     if (active) {
-      const int row = mine[key] + __popcll(peers & below);
-      const bool kept = key < E;
+      const int row = mine[key[i]] + __popcll(peers & below);
+      const bool kept = key[i] < E;
       place[f] = kept ? row : ~row;
       order[row] = kept ? (int)f : ~(int)f;
     }
@@ -183,77 +207,97 @@ __global__ void __launch_bounds__(kSortThreads)
     // the next group reads what the leaders left
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (active && (peers & below) == 0) mine[key] += __popcll(peers);
+    if (active && (peers & below) == 0) mine[key[i]] += __popcll(peers);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
 }
 
+template <int WAVES, bool SINGLE>
+static void launch_scatter(unsigned chunks, const int64_t *experts, int64_t R, int E,
+                           int32_t *offsets, int32_t *order, int32_t *place, int32_t *status,
+                           hipStream_t s) {
+  int bits = 1;
+  while ((1 << bits) <= E) ++bits;
+  const size_t lds = (size_t)(WAVES * (E + 1) + WAVES) * sizeof(int);
+  hipLaunchKernelGGL((moe_scatter_kernel<WAVES, SINGLE>), dim3(chunks), dim3(64 * WAVES), lds, s,
+                     experts, R, E, bits, offsets, order, place, status);
+}
+
 __global__ void moe_clear_status_kernel(int32_t *status) { *status = 0; }
 
 // ------------------------------------------------------- rows by place ----
-// A row is cut into chunks of V bytes; 2^shift threads share a token, each taking
-// every 2^shift-th chunk.  V is 16 where rows and pointers allow it, else the
-// element.
+// A row is cut into chunks of 16 bytes; 2^shift threads share a token, each taking
+// every 2^shift-th chunk.  The last chunk of a row that is no whole number of them
+// ends with the row and overlaps the one before (rows shorter than a chunk go by the
+// element).  ALIGNED: rows and arrays are multiples of 16 bytes; otherwise they have
+// the alignment of an element, which the vector loads and stores of the hardware
+// take as well (1000 x 3 rows of 1001 bf16: combine 8.8 us by the element).
+// STREAM: the rows are more than the L2 caches hold and go past them (8191 x 4 rows
+// of 4 KiB: combine 35.4 -> 29.4 us, gather 35.1 -> 26.7; rows that fit are
+// slower so: 4000 x 2 of 1.3 KiB, combine 8.3 -> 10.7).
 struct RowMap {
   int shift;   // log2 of the threads per token
   int chunks;  // chunks per row
+  int bytes;   // of a row
 };
 
-template <int V>
-struct Chunk;
-template <>
-struct Chunk<16> {
-  typedef u32x4 type;
-};
-template <>
-struct Chunk<4> {
-  typedef uint32_t type;
-};
-template <>
-struct Chunk<2> {
-  typedef uint16_t type;
-};
-
-// fp32 values of a chunk and back (bf16: one rounding to nearest even)
-template <typename T, int V>
-struct Conv {
-  static constexpr int n = V / (int)sizeof(T);
-  typedef typename Chunk<V>::type raw;
-  static __device__ __forceinline__ void load(const raw &c, float *v) {
-    if constexpr (V == 16) {
+template <typename T, int V, bool ALIGNED, bool STREAM>
+struct Rows {
+  static constexpr int n = V / (int)sizeof(T);  // values of a chunk
+  typedef Rows<T, V, ALIGNED, false> Kept;      // (the gather's own rows: 32.1 us past the caches)
+  struct __attribute__((packed, aligned(sizeof(T)))) Loose {
+    u32x4 v;
+  };
+  static __device__ __forceinline__ int offset(const RowMap &m, int c) {
+    return V == 16 && !ALIGNED ? min(c * 16, m.bytes - 16) : c * V;
+  }
+  // values at the front of chunk c that the chunk before has, too
+  static __device__ __forceinline__ int shared(const RowMap &m, int c) {
+    return (c * V - offset(m, c)) / (int)sizeof(T);
+  }
+  static __device__ __forceinline__ const uint8_t *at(const void *p, const RowMap &m, int64_t row, int c) {
+    return reinterpret_cast<const uint8_t *>(p) + row * m.bytes + offset(m, c);
+  }
+  static __device__ __forceinline__ u32x4 load(const void *p, const RowMap &m, int64_t row, int c) {
+    const uint8_t *q = at(p, m, row, c);
+    if constexpr (V == 16 && ALIGNED && STREAM)
+      return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(q));
+    else if constexpr (V == 16 && ALIGNED)
+      return *reinterpret_cast<const u32x4 *>(q);
+    else if constexpr (V == 16)
+      return reinterpret_cast<const Loose *>(q)->v;
+    else
+      return u32x4{(uint32_t)*reinterpret_cast<const T *>(q), 0u, 0u, 0u};
+  }
+  static __device__ __forceinline__ void store(void *p, const RowMap &m, int64_t row, int c, u32x4 v) {
+    uint8_t *q = const_cast<uint8_t *>(at(p, m, row, c));
+    if constexpr (V == 16 && ALIGNED && STREAM)
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(q));
+    else if constexpr (V == 16 && ALIGNED)
+      *reinterpret_cast<u32x4 *>(q) = v;
+    else if constexpr (V == 16)
+      reinterpret_cast<Loose *>(q)->v = v;
+    else
+      *reinterpret_cast<T *>(q) = (T)v[0];
+  }
+  // fp32 values of a chunk and back (bf16: one rounding to nearest even)
+  static __device__ __forceinline__ void values(const u32x4 &c, float *v) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-          v[i] = __uint_as_float(c[i]);
-        } else {
-          v[2 * i] = bf16_lo(c[i]);
-          v[2 * i + 1] = bf16_hi(c[i]);
-        }
-      }
-    } else if constexpr (sizeof(T) == 4) {
-      v[0] = __uint_as_float(c);
-    } else {
-      v[0] = __uint_as_float((uint32_t)c << 16);
-    }
+    for (int i = 0; i < n; ++i)
+      v[i] = sizeof(T) == 4 ? __uint_as_float(c[i]) : i % 2 ? bf16_hi(c[i / 2]) : bf16_lo(c[i / 2]);
   }
   static __device__ __forceinline__ uint32_t bits(float f) {
-    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
+    return sizeof(T) == 4 ? __float_as_uint(f) : (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
   }
-  static __device__ __forceinline__ raw store(const float *v) {
-    raw c;
-    if constexpr (V == 16) {
+  static __device__ __forceinline__ u32x4 chunk(const float *v) {
+    u32x4 c = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4)
-          c[i] = __float_as_uint(v[i]);
-        else
-          c[i] = bits(v[2 * i]) | (bits(v[2 * i + 1]) << 16);
-      }
-    } else if constexpr (sizeof(T) == 4) {
-      c = __float_as_uint(v[0]);
-    } else {
-      c = (uint16_t)bits(v[0]);
+    for (int i = 0; i < n; ++i) {
+      if constexpr (sizeof(T) == 4)
+        c[i] = bits(v[i]);
+      else
+        c[i / 2] |= bits(v[i]) << (16 * (i % 2));
     }
     return c;
   }
@@ -263,42 +307,38 @@ struct Conv {
 __device__ __forceinline__ int kept_row(int p, int R) { return p >= 0 && p < R ? p : -1; }
 
 // P[row] = X[t] for every slot of token t, zeros in the rows without an expert.
-template <int V>
+template <typename ROWS>
 __global__ void __launch_bounds__(256)
-    moe_gather_kernel(const typename Chunk<V>::type *__restrict__ X,
-                      const int32_t *__restrict__ place, int64_t T, int topk, RowMap map,
-                      typename Chunk<V>::type *__restrict__ out) {
-  typedef typename Chunk<V>::type raw;
+    moe_gather_kernel(const void *__restrict__ X, const int32_t *__restrict__ place, int64_t T,
+                      int topk, RowMap map, void *__restrict__ out) {
   const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t t = g >> map.shift;
   if (t >= T) return;
   const int R = (int)(T * topk);
   for (int c = (int)(g & ((1 << map.shift) - 1)); c < map.chunks; c += 1 << map.shift) {
-    const raw v = X[t * map.chunks + c];
+    const u32x4 v = ROWS::Kept::load(X, map, t, c);
     for (int j = 0; j < topk; ++j) {
       const int p = place[t * topk + j];
       const int row = p < 0 ? ~p : p;
-      if (row < R) out[(int64_t)row * map.chunks + c] = p < 0 ? raw{} : v;
+      if (row < R) ROWS::store(out, map, row, c, p < 0 ? u32x4{0u, 0u, 0u, 0u} : v);
     }
   }
 }
 
 // out[t] = sum_j w[t,j] Y[place[t,j]] in fp32, j in order (WEIGHTED false: w = 1).
-template <typename T, int V, bool WEIGHTED>
+template <typename ROWS, bool WEIGHTED>
 __global__ void __launch_bounds__(256)
-    moe_combine_kernel(const typename Chunk<V>::type *__restrict__ Y,
-                       const int32_t *__restrict__ place, const float *__restrict__ weights,
-                       int64_t T_, int topk, RowMap map, typename Chunk<V>::type *__restrict__ out) {
-  typedef Conv<T, V> C;
-  typedef typename C::raw raw;
+    moe_combine_kernel(const void *__restrict__ Y, const int32_t *__restrict__ place,
+                       const float *__restrict__ weights, int64_t T, int topk, RowMap map,
+                       void *__restrict__ out) {
   const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t t = g >> map.shift;
-  if (t >= T_) return;
-  const int R = (int)(T_ * topk);
+  if (t >= T) return;
+  const int R = (int)(T * topk);
   for (int c = (int)(g & ((1 << map.shift) - 1)); c < map.chunks; c += 1 << map.shift) {
-    float acc[C::n] = {};
+    float acc[ROWS::n] = {};
     for (int j0 = 0; j0 < topk; j0 += 4) {
-      raw y[4];
+      u32x4 y[4];
       float w[4];
       bool on[4];
 #pragma unroll
@@ -307,20 +347,20 @@ __global__ void __launch_bounds__(256)
         on[j] = row >= 0;
         w[j] = 1.0f;
         if (on[j]) {
-          y[j] = Y[(int64_t)row * map.chunks + c];
+          y[j] = ROWS::load(Y, map, row, c);
           if constexpr (WEIGHTED) w[j] = weights[t * topk + j0 + j];
         }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (!on[j]) continue;
-        float v[C::n];
-        C::load(y[j], v);
+        float v[ROWS::n];
+        ROWS::values(y[j], v);
 #pragma unroll
-        for (int i = 0; i < C::n; ++i) acc[i] = WEIGHTED ? fmaf(w[j], v[i], acc[i]) : acc[i] + v[i];
+        for (int i = 0; i < ROWS::n; ++i) acc[i] = WEIGHTED ? fmaf(w[j], v[i], acc[i]) : acc[i] + v[i];
       }
     }
-    out[t * map.chunks + c] = C::store(acc);
+    ROWS::store(out, map, t, c, ROWS::chunk(acc));
   }
 }
 
@@ -328,21 +368,18 @@ __global__ void __launch_bounds__(256)
 // L threads per token (64: four tokens a workgroup; 256: one).  Slots are taken
 // four at a time; each thread's partial sums are added over the wave, then over
 // the waves in order.
-template <typename T, int V, int L>
+template <typename ROWS, int L>
 __global__ void __launch_bounds__(256)
-    moe_combine_grad_kernel(const typename Chunk<V>::type *__restrict__ dOut,
-                            const typename Chunk<V>::type *__restrict__ Y,
+    moe_combine_grad_kernel(const void *__restrict__ dOut, const void *__restrict__ Y,
                             const int32_t *__restrict__ place, const float *__restrict__ weights,
-                            int64_t T_, int topk, int chunks,
-                            typename Chunk<V>::type *__restrict__ dY, float *__restrict__ dw) {
-  typedef Conv<T, V> C;
-  typedef typename C::raw raw;
+                            int64_t T, int topk, RowMap map, void *__restrict__ dY,
+                            float *__restrict__ dw) {
   __shared__ float part[4][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = L == 256 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
-  if (t >= T_) return;  // a whole wave (L = 64, no barrier below) or workgroup
+  if (t >= T) return;  // a whole wave (L = 64, no barrier below) or workgroup
   const int first = L == 256 ? (int)threadIdx.x : lane;
-  const int R = (int)(T_ * topk);
+  const int R = (int)(T * topk);
   for (int j0 = 0; j0 < topk; j0 += 4) {
     int row[4];
     bool on[4];
@@ -354,27 +391,28 @@ __global__ void __launch_bounds__(256)
       on[j] = p >= 0 && p < R;
       w[j] = on[j] ? weights[t * topk + j0 + j] : 0.f;
     }
-    for (int c = first; c < chunks; c += L) {
-      const raw g = dOut[t * chunks + c];
-      raw y[4];
+    for (int c = first; c < map.chunks; c += L) {
+      const u32x4 g = ROWS::load(dOut, map, t, c);
+      u32x4 y[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (on[j]) y[j] = Y[(int64_t)row[j] * chunks + c];
-      float gv[C::n];
-      C::load(g, gv);
+        if (on[j]) y[j] = ROWS::load(Y, map, row[j], c);
+      float gv[ROWS::n];
+      ROWS::values(g, gv);
+      const int dup = ROWS::shared(map, c);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (on[j]) {
-          float v[C::n], d[C::n];
-          C::load(y[j], v);
+          float v[ROWS::n], d[ROWS::n];
+          ROWS::values(y[j], v);
 #pragma unroll
-          for (int i = 0; i < C::n; ++i) {
-            dot[j] = fmaf(gv[i], v[i], dot[j]);
+          for (int i = 0; i < ROWS::n; ++i) {
+            dot[j] = i < dup ? dot[j] : fmaf(gv[i], v[i], dot[j]);
             d[i] = w[j] * gv[i];
           }
-          dY[(int64_t)row[j] * chunks + c] = C::store(d);
+          ROWS::store(dY, map, row[j], c, ROWS::chunk(d));
         } else if (row[j] < R) {
-          dY[(int64_t)row[j] * chunks + c] = raw{};
+          ROWS::store(dY, map, row[j], c, u32x4{0u, 0u, 0u, 0u});
         }
       }
     }
@@ -407,55 +445,34 @@ static int check_rows(int64_t T, int64_t topk, int64_t H) {
   return NF4_OK;
 }
 
-static int chunk_bytes(int64_t H, int esize, const void *a, const void *b, const void *c) {
-  if (H * esize % 16 == 0 && aligned_to(a, 16) && aligned_to(b, 16) && aligned_to(c, 16)) return 16;
-  return esize;
-}
-
 // Threads per token: as many as the row has chunks, up to a workgroup.
-static RowMap row_map(int64_t chunks) {
-  RowMap m{0, (int)chunks};
-  while (m.shift < 8 && (1 << m.shift) < chunks) ++m.shift;
+static RowMap row_map(int64_t H, int esize, int v) {
+  RowMap m{0, (int)((H * esize + v - 1) / v), (int)(H * esize)};
+  while (m.shift < 8 && (1 << m.shift) < m.chunks) ++m.shift;
   return m;
 }
 
 static dim3 row_grid(int64_t T, RowMap m) { return dim3((unsigned)(((T << m.shift) + 255) >> 8)); }
 
-template <int V>
-static void launch_gather(const void *X, const int32_t *place, int64_t T, int64_t topk,
-                          int64_t chunks, void *out, hipStream_t s) {
-  typedef typename Chunk<V>::type raw;
-  const RowMap m = row_map(chunks);
-  hipLaunchKernelGGL(moe_gather_kernel<V>, row_grid(T, m), dim3(256), 0, s, (const raw *)X, place,
-                     T, (int)topk, m, (raw *)out);
-}
-
-template <typename T, int V>
-static void launch_combine(const void *Y, const int32_t *place, const float *weights, int64_t T_,
-                           int64_t topk, int64_t chunks, void *out, hipStream_t s) {
-  typedef typename Chunk<V>::type raw;
-  const RowMap m = row_map(chunks);
-  if (weights)
-    hipLaunchKernelGGL((moe_combine_kernel<T, V, true>), row_grid(T_, m), dim3(256), 0, s,
-                       (const raw *)Y, place, weights, T_, (int)topk, m, (raw *)out);
+// Calls f with the Rows type for this call and its map.
+template <typename T, typename F>
+static void with_rows_of(int64_t H, int64_t rows, bool aligned16, F f) {
+  constexpr int es = (int)sizeof(T);
+  if (H * es < 16)
+    f(Rows<T, es, true, false>(), row_map(H, es, es));
+  else if (!aligned16 || H * es % 16 != 0)
+    f(Rows<T, 16, false, false>(), row_map(H, es, 16));
+  else if (rows * H * es < (int64_t(32) << 20))  // 8 L2 caches of 4 MiB
+    f(Rows<T, 16, true, false>(), row_map(H, es, 16));
   else
-    hipLaunchKernelGGL((moe_combine_kernel<T, V, false>), row_grid(T_, m), dim3(256), 0, s,
-                       (const raw *)Y, place, weights, T_, (int)topk, m, (raw *)out);
+    f(Rows<T, 16, true, true>(), row_map(H, es, 16));
 }
-
-template <typename T, int V>
-static void launch_combine_grad(const void *dOut, const void *Y, const int32_t *place,
-                                const float *weights, int64_t T_, int64_t topk, int64_t chunks,
-                                void *dY, float *dw, hipStream_t s) {
-  typedef typename Chunk<V>::type raw;
-  if (chunks >= 256)
-    hipLaunchKernelGGL((moe_combine_grad_kernel<T, V, 256>), dim3((unsigned)T_), dim3(256), 0, s,
-                       (const raw *)dOut, (const raw *)Y, place, weights, T_, (int)topk,
-                       (int)chunks, (raw *)dY, dw);
+template <typename F>
+static void with_rows(int dtype, int64_t H, int64_t rows, bool aligned16, F f) {
+  if (dtype == NF4_F32)
+    with_rows_of<uint32_t>(H, rows, aligned16, f);
   else
-    hipLaunchKernelGGL((moe_combine_grad_kernel<T, V, 64>), dim3((unsigned)((T_ + 3) / 4)),
-                       dim3(256), 0, s, (const raw *)dOut, (const raw *)Y, place, weights, T_,
-                       (int)topk, (int)chunks, (raw *)dY, dw);
+    with_rows_of<uint16_t>(H, rows, aligned16, f);
 }
 
 }  // namespace nf4
@@ -478,23 +495,21 @@ int nf4_moe_sort(const int64_t *experts, int64_t T, int64_t topk, int64_t E, int
     if (hipGetLastError() != hipSuccess) return NF4_ELAUNCH;
   }
   const int64_t R = T * topk;
-  int bits = 1;
-  while ((1 << bits) <= E) ++bits;
-  const size_t lds = (size_t)(nf4::kSortWaves * (E + 1) + nf4::kSortWaves) * sizeof(int);
-  const int64_t chunks = R / nf4::kSortChunk;
-  const dim3 wg(nf4::kSortThreads);
-  if (chunks <= 1) {
-    hipLaunchKernelGGL(nf4::moe_scatter_kernel<true>, dim3(1), wg, lds, s, experts, R, (int)E,
-                       bits, offsets, order, place, dev_status);
+  constexpr int64_t kWave = 64 * nf4::kSortGroups;
+  if (R < 4 * kWave && E < 256) {
+    nf4::launch_scatter<4, true>(1, experts, R, (int)E, offsets, order, place, dev_status, s);
+  } else if (R < 16 * kWave) {
+    nf4::launch_scatter<16, true>(1, experts, R, (int)E, offsets, order, place, dev_status, s);
   } else {
-    hipLaunchKernelGGL(nf4::moe_count_kernel, dim3((unsigned)chunks), wg, 0, s, experts, R, (int)E,
-                       place, dev_status);
+    const unsigned chunks = (unsigned)(R / nf4::kSortChunk);
+    hipLaunchKernelGGL(nf4::moe_count_kernel, dim3(chunks), dim3(64 * nf4::kChunkWaves), 0, s,
+                       experts, R, (int)E, place, dev_status);
     if (hipGetLastError() != hipSuccess) return NF4_ELAUNCH;
-    hipLaunchKernelGGL(nf4::moe_scan_kernel, dim3(1), wg, 0, s, (int)chunks, (int)E, place,
+    hipLaunchKernelGGL(nf4::moe_scan_kernel, dim3(1), dim3(1024), 0, s, (int)chunks, (int)E, place,
                        offsets);
     if (hipGetLastError() != hipSuccess) return NF4_ELAUNCH;
-    hipLaunchKernelGGL(nf4::moe_scatter_kernel<false>, dim3((unsigned)chunks), wg, lds, s, experts,
-                       R, (int)E, bits, offsets, order, place, dev_status);
+    nf4::launch_scatter<nf4::kChunkWaves, false>(chunks, experts, R, (int)E, offsets, order, place,
+                                                 dev_status, s);
   }
   return nf4::launch_status(hipGetLastError());
 }
@@ -509,14 +524,11 @@ int nf4_moe_gather(const void *X, int dtype, const int32_t *place, int64_t T, in
   if (int r = nf4::device_status()) return r;
   if (T == 0) return NF4_OK;
   hipStream_t s = (hipStream_t)stream;
-  const int v = nf4::chunk_bytes(H, es, X, out, out);
-  const int64_t chunks = H * es / v;
-  if (v == 16)
-    nf4::launch_gather<16>(X, place, T, topk, chunks, out, s);
-  else if (v == 4)
-    nf4::launch_gather<4>(X, place, T, topk, chunks, out, s);
-  else
-    nf4::launch_gather<2>(X, place, T, topk, chunks, out, s);
+  nf4::with_rows(dtype, H, T * topk, nf4::aligned_to(X, 16) && nf4::aligned_to(out, 16),
+                 [&](auto rows, nf4::RowMap m) {
+                   hipLaunchKernelGGL(nf4::moe_gather_kernel<decltype(rows)>, nf4::row_grid(T, m),
+                                      dim3(256), 0, s, X, place, T, (int)topk, m, out);
+                 });
   return nf4::launch_status(hipGetLastError());
 }
 
@@ -531,16 +543,17 @@ int nf4_moe_combine(const void *Y, int dtype, const int32_t *place, const float 
   if (int r = nf4::device_status()) return r;
   if (T == 0) return NF4_OK;
   hipStream_t s = (hipStream_t)stream;
-  const int v = nf4::chunk_bytes(H, es, Y, out, out);
-  const int64_t chunks = H * es / v;
-  if (v == 16 && es == 4)
-    nf4::launch_combine<float, 16>(Y, place, weights, T, topk, chunks, out, s);
-  else if (v == 16)
-    nf4::launch_combine<uint16_t, 16>(Y, place, weights, T, topk, chunks, out, s);
-  else if (es == 4)
-    nf4::launch_combine<float, 4>(Y, place, weights, T, topk, chunks, out, s);
-  else
-    nf4::launch_combine<uint16_t, 2>(Y, place, weights, T, topk, chunks, out, s);
+  nf4::with_rows(dtype, H, T * topk, nf4::aligned_to(Y, 16) && nf4::aligned_to(out, 16),
+                 [&](auto rows, nf4::RowMap m) {
+                   if (weights)
+                     hipLaunchKernelGGL((nf4::moe_combine_kernel<decltype(rows), true>),
+                                        nf4::row_grid(T, m), dim3(256), 0, s, Y, place, weights, T,
+                                        (int)topk, m, out);
+                   else
+                     hipLaunchKernelGGL((nf4::moe_combine_kernel<decltype(rows), false>),
+                                        nf4::row_grid(T, m), dim3(256), 0, s, Y, place, weights, T,
+                                        (int)topk, m, out);
+                 });
   return nf4::launch_status(hipGetLastError());
 }
 
@@ -557,16 +570,16 @@ int nf4_moe_combine_grad(const void *dOut, const void *Y, int dtype, const int32
   if (int r = nf4::device_status()) return r;
   if (T == 0) return NF4_OK;
   hipStream_t s = (hipStream_t)stream;
-  const int v = nf4::chunk_bytes(H, es, dOut, Y, dY);
-  const int64_t chunks = H * es / v;
-  if (v == 16 && es == 4)
-    nf4::launch_combine_grad<float, 16>(dOut, Y, place, weights, T, topk, chunks, dY, dweights, s);
-  else if (v == 16)
-    nf4::launch_combine_grad<uint16_t, 16>(dOut, Y, place, weights, T, topk, chunks, dY, dweights, s);
-  else if (es == 4)
-    nf4::launch_combine_grad<float, 4>(dOut, Y, place, weights, T, topk, chunks, dY, dweights, s);
-  else
-    nf4::launch_combine_grad<uint16_t, 2>(dOut, Y, place, weights, T, topk, chunks, dY, dweights, s);
+  const bool aligned16 = nf4::aligned_to(dOut, 16) && nf4::aligned_to(Y, 16) && nf4::aligned_to(dY, 16);
+  nf4::with_rows(dtype, H, T * topk, aligned16, [&](auto rows, nf4::RowMap m) {
+    if (m.chunks >= 256)
+      hipLaunchKernelGGL((nf4::moe_combine_grad_kernel<decltype(rows), 256>), dim3((unsigned)T),
+                         dim3(256), 0, s, dOut, Y, place, weights, T, (int)topk, m, dY, dweights);
+    else
+      hipLaunchKernelGGL((nf4::moe_combine_grad_kernel<decltype(rows), 64>),
+                         dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, dOut, Y, place, weights, T,
+                         (int)topk, m, dY, dweights);
+  });
   return nf4::launch_status(hipGetLastError());
 }
 
