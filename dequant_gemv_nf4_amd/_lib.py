@@ -725,7 +725,7 @@ def moe_sort(experts, num_experts, stream=None):
     order = torch.empty(experts.numel(), dtype=torch.int32, device=dev)
     place = torch.empty(experts.shape, dtype=torch.int32, device=dev)
     T, topk = experts.shape
-    _run("nf4_moe_sort", (experts,), (experts.data_ptr(), T, topk, num_experts, offsets.data_ptr(),
+    _run("nf4_moe_sort", (experts,), (experts.data_ptr(), T, topk, int(num_experts), offsets.data_ptr(),
                                       order.data_ptr(), place.data_ptr(), None), stream)
     return offsets, order, place
 

@@ -137,7 +137,7 @@ __device__ __forceinline__ int w_perm(int row) {
 }
 
 template <int MF, int NF, int WV, int KS, int KW, int KG, bool SVEC, typename OUT>
-__global__ void __launch_bounds__(64 * WV *KG, (MF * NF > 32 ? 1 : MF * NF > 16 ? 2 : WV * KG / 2))
+__global__ void __launch_bounds__(64 * WV *KG, 2)
     mx_tile_kernel(Args p) {
   constexpr int BM = 16 * MF, BN = 16 * NF * WV;
   constexpr int SG = 4 / KS;                              // stages per scale load (256 k)
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(64 * WV *KG, (MF * NF > 32 ? 1 : MF * NF > 16 
 }
 
 template <int MT>
-static hipError_t launch_gemv(Args &a, int out_dtype, hipStream_t s) {
+static int launch_gemv(Args &a, int out_dtype, hipStream_t s) {
   constexpr int RP = 4;  // 8 rows ahead measured slower, 2 within 3 %
   const int64_t slots = slots_for(a.R, a.E, a.offsets != nullptr, MT);
   // 16 weight rows a workgroup (grouped: 32, an expert's rows of X are fewer than
@@ -403,7 +403,7 @@ static hipError_t launch_gemv(Args &a, int out_dtype, hipStream_t s) {
   a.grid = make_grid(slots, (a.N + rows - 1) / rows, 8);
   const int64_t n = grid_size(a.grid);
   const int threads = 64 * chunks * groups;
-  if (n * threads >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  if (n * threads >= (int64_t(1) << 32)) return NF4_ERANGE;
   const size_t lds = (size_t)chunks * rows * MT * 4;
   if (out_dtype == NF4_F32)
     hipLaunchKernelGGL((mx_gemv_kernel<MT, RP, float>), dim3((unsigned)n), dim3(threads), lds, s, a,
@@ -411,26 +411,26 @@ static hipError_t launch_gemv(Args &a, int out_dtype, hipStream_t s) {
   else
     hipLaunchKernelGGL((mx_gemv_kernel<MT, RP, uint16_t>), dim3((unsigned)n), dim3(threads), lds, s,
                        a, chunks, rows);
-  return hipGetLastError();
+  return launch_status(hipGetLastError());
 }
 
 template <int MF, int NF, int WV, int KS, int KW, int KG, bool SVEC>
-static hipError_t launch_tile_as(Args &a, int out_dtype, hipStream_t s) {
+static int launch_tile_as(Args &a, int out_dtype, hipStream_t s) {
   a.grid = make_grid(slots_for(a.R, a.E, a.offsets != nullptr, 16 * MF),
                      (a.N + 16 * NF * WV - 1) / (16 * NF * WV), 8);
   const int64_t n = grid_size(a.grid);
-  if (n * 64 * WV * KG >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  if (n * 64 * WV * KG >= (int64_t(1) << 32)) return NF4_ERANGE;
   if (out_dtype == NF4_F32)
     hipLaunchKernelGGL((mx_tile_kernel<MF, NF, WV, KS, KW, KG, SVEC, float>), dim3((unsigned)n),
                        dim3(64 * WV * KG), 0, s, a);
   else
     hipLaunchKernelGGL((mx_tile_kernel<MF, NF, WV, KS, KW, KG, SVEC, uint16_t>), dim3((unsigned)n),
                        dim3(64 * WV * KG), 0, s, a);
-  return hipGetLastError();
+  return launch_status(hipGetLastError());
 }
 
 template <int MF, int NF, int WV, int KS, int KW, int KG>
-static hipError_t launch_tile(Args &a, int out_dtype, hipStream_t s) {
+static int launch_tile(Args &a, int out_dtype, hipStream_t s) {
   if (a.K % 128 == 0 && aligned_to(a.scales, 4))
     return launch_tile_as<MF, NF, WV, KS, KW, KG, true>(a, out_dtype, s);
   return launch_tile_as<MF, NF, WV, KS, KW, KG, false>(a, out_dtype, s);
@@ -444,7 +444,7 @@ static hipError_t launch_tile(Args &a, int out_dtype, hipStream_t s) {
 // 16 x 64 12.1, with two K-groups 10.7, 16 x 32 with two 8.6; M = 8, N = 4096, K =
 // 14336: 16 x 32 with two K-groups 21.2, with four 17.5; M = 509, N = 28672: 128 x 256
 // 111, 64 x 128 148.
-static hipError_t launch_product(Args &a, int out_dtype, hipStream_t s) {
+static int launch_product(Args &a, int out_dtype, hipStream_t s) {
   const bool grouped = a.offsets != nullptr;
   const auto tiles = [&](int bm, int bn) {
     return slots_for(a.R, a.E, grouped, bm) * ((a.N + bn - 1) / bn);
@@ -486,7 +486,7 @@ int nf4_mx_gemm(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t 
     return NF4_EALIGN;
   if (int r = nf4::device_status()) return r;
   nf4::mx::Args a{codes, scales, X, nullptr, Y, M, 1, (int)N, (int)K, {}};
-  return nf4::launch_status(nf4::mx::launch_product(a, out_dtype, (hipStream_t)stream));
+  return nf4::mx::launch_product(a, out_dtype, (hipStream_t)stream);
 }
 
 int nf4_mx_gemm_grouped(const uint8_t *codes, const uint8_t *scales, int64_t E, int64_t N,
@@ -503,7 +503,7 @@ int nf4_mx_gemm_grouped(const uint8_t *codes, const uint8_t *scales, int64_t E, 
   if (int r = nf4::device_status()) return r;
   if (R == 0) return NF4_OK;
   nf4::mx::Args a{codes, scales, X, offsets, Y, R, (int)E, (int)N, (int)K, {}};
-  return nf4::launch_status(nf4::mx::launch_product(a, out_dtype, (hipStream_t)stream));
+  return nf4::mx::launch_product(a, out_dtype, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -45,7 +45,7 @@ __device__ __forceinline__ int code_perm(int n) {
 }
 
 template <int MF, int WV, int KG, bool SVEC, typename OUT>
-__global__ void __launch_bounds__(64 * WV *KG, MF > 4 ? 1 : 2) mx_grad_kernel(GradArgs p) {
+__global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
   constexpr int BM = 16 * MF, NX = 3;
   constexpr int XB = BM * 128, WB = 64 * 64 * WV;
   constexpr int XL = 2 * MF / WV, WL = 4;  // loads a wave
@@ -225,21 +225,21 @@ __global__ void __launch_bounds__(64 * WV *KG, MF > 4 ? 1 : 2) mx_grad_kernel(Gr
 }
 
 template <int MF, int WV, int KG, bool SVEC>
-static hipError_t launch_grad_as(GradArgs &a, int out_dtype, hipStream_t s) {
+static int launch_grad_as(GradArgs &a, int out_dtype, hipStream_t s) {
   a.grid = make_grid(slots_for(a.R, a.E, true, 16 * MF), (a.K + 128 * WV - 1) / (128 * WV), 8);
   const int64_t n = grid_size(a.grid);
-  if (n * 64 * WV * KG >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  if (n * 64 * WV * KG >= (int64_t(1) << 32)) return NF4_ERANGE;
   if (out_dtype == NF4_F32)
     hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, float>), dim3((unsigned)n),
                        dim3(64 * WV * KG), 0, s, a);
   else
     hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, uint16_t>), dim3((unsigned)n),
                        dim3(64 * WV * KG), 0, s, a);
-  return hipGetLastError();
+  return launch_status(hipGetLastError());
 }
 
 template <int MF, int WV, int KG>
-static hipError_t launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
+static int launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
   if (a.K % 128 == 0 && aligned_to(a.scales, 4))
     return launch_grad_as<MF, WV, KG, true>(a, out_dtype, s);
   return launch_grad_as<MF, WV, KG, false>(a, out_dtype, s);
@@ -252,7 +252,7 @@ static hipError_t launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
 // 2048: 32 x 512 with two groups 27.7, 64 x 512 with two 34; 300 rows of 8 of 14336 x
 // 4096: 32 x 256 with two groups 103, 32 x 512 with two 154; 8 rows of 8: 16 x 256 with
 // four groups 78, with two 82.
-static hipError_t launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
+static int launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
   const auto tiles = [&](int bm, int bk) {
     return slots_for(a.R, a.E, true, bm) * ((a.K + bk - 1) / bk);
   };
@@ -289,7 +289,7 @@ int nf4_mx_gemm_grouped_grad(const uint8_t *codes, const uint8_t *scales, int64_
   if (int r = nf4::device_status()) return r;
   if (R == 0) return NF4_OK;
   nf4::mx::GradArgs a{codes, scales, dY, offsets, dX, R, (int)E, (int)N, (int)K, {}};
-  return nf4::launch_status(nf4::mx::launch_rows_grad(a, out_dtype, (hipStream_t)stream));
+  return nf4::mx::launch_rows_grad(a, out_dtype, (hipStream_t)stream);
 }
 
 }  // extern "C"

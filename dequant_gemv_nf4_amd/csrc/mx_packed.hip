@@ -233,22 +233,22 @@ __global__ void __launch_bounds__(64 * WN *WM *KG, NF *MF > 16 ? 1 : 2) mx_packe
 }
 
 template <int WN, int WM, int NF, int MF, int KS, int KG, int NB, bool SVEC>
-static hipError_t launch_packed_as(PackedArgs &a, int out_dtype, hipStream_t s) {
+static int launch_packed_as(PackedArgs &a, int out_dtype, hipStream_t s) {
   constexpr int BN = 16 * NF * WN, BM = 16 * MF * WM, NT = 64 * WN * WM * KG;
   a.grid = make_grid((a.M + BM - 1) / BM, (a.N + BN - 1) / BN, 8);
   const int64_t n = grid_size(a.grid);
-  if (n * NT >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  if (n * NT >= (int64_t(1) << 32)) return NF4_ERANGE;
   if (out_dtype == NF4_F32)
     hipLaunchKernelGGL((mx_packed_kernel<WN, WM, NF, MF, KS, KG, NB, SVEC, float>), dim3((unsigned)n),
                        dim3(NT), 0, s, a);
   else
     hipLaunchKernelGGL((mx_packed_kernel<WN, WM, NF, MF, KS, KG, NB, SVEC, uint16_t>), dim3((unsigned)n),
                        dim3(NT), 0, s, a);
-  return hipGetLastError();
+  return launch_status(hipGetLastError());
 }
 
 template <int WN, int WM, int NF, int MF, int KS, int KG, int NB>
-static hipError_t launch_tile(PackedArgs &a, int out_dtype, hipStream_t s) {
+static int launch_tile(PackedArgs &a, int out_dtype, hipStream_t s) {
   if (a.K % 128 == 0 && aligned_to(a.scales, 4) && aligned_to(a.xscales, 4))
     return launch_packed_as<WN, WM, NF, MF, KS, KG, NB, true>(a, out_dtype, s);
   return launch_packed_as<WN, WM, NF, MF, KS, KG, NB, false>(a, out_dtype, s);
@@ -261,7 +261,7 @@ static hipError_t launch_tile(PackedArgs &a, int out_dtype, hipStream_t s) {
 // 4096 x 4096: 64 x 64 with two K-groups 9.4, with one 10.0; 37 x 6144 x 4096: 32 x 64
 // with two 7.4, 64 x 64 with two 8.5; 16 x 4096 x 14336: 16 x 64 with two 13.2, with
 // one 15.8; 1 x 28672 x 4096: with two 16.4, with one 14.5.
-static hipError_t launch_packed(PackedArgs &a, int out_dtype, hipStream_t s) {
+static int launch_packed(PackedArgs &a, int out_dtype, hipStream_t s) {
   const auto tiles = [&](int bm, int bn) {
     return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
   };
@@ -294,7 +294,7 @@ int nf4_mx_gemm_packed(const uint8_t *codes, const uint8_t *scales, int64_t N, i
     return NF4_EALIGN;
   if (int r = nf4::device_status()) return r;
   nf4::mx::PackedArgs a{codes, scales, xcodes, xscales, Y, M, (int)N, (int)K, {}};
-  return nf4::launch_status(nf4::mx::launch_packed(a, out_dtype, (hipStream_t)stream));
+  return nf4::mx::launch_packed(a, out_dtype, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -320,7 +320,8 @@ int nf4_mx_unpack(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_
 /*
  * nf4_mx_gemm -- Y[m][n] = sum_k X[m][k] * v(n,k), X bf16 [M][K], any M >= 1
  * (M = 1 is the decode product), Y [M][N] fp32 or bf16 (rounded once).
- * Alignment: codes, X and Y 16 bytes.  Errors: NF4_ERANGE for M < 1 or M >= 2^26.
+ * Alignment: codes, X and Y 16 bytes.  Errors: NF4_ERANGE for M < 1 or M >= 2^26, and
+ * for a product whose tiles are more than one launch holds (2^32 work-items).
  */
 int nf4_mx_gemm(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K,
                 const uint16_t *X, int64_t M, void *Y, int out_dtype, void *stream);
@@ -366,7 +367,9 @@ int nf4_moe_sort(const int64_t *experts, int64_t T, int64_t topk, int64_t E, int
  * nf4_moe_combine of the rows' gradients without weights.
  * The row operators take any H >= 1 up to 2^20, and are fastest where a row is a
  * multiple of 16 bytes and the arrays are 16-byte aligned (else the alignment of
- * an element).  Entries of place beyond [~(R-1), R-1] are skipped.
+ * an element).  place names every row once, as nf4_moe_sort writes it: a row named
+ * twice is written twice, in no order, one that is never named is left as it was, and
+ * entries beyond [~(R-1), R-1] are skipped.
  */
 int nf4_moe_gather(const void *X, int dtype, const int32_t *place, int64_t T, int64_t topk,
                    int64_t H, void *out, void *stream);

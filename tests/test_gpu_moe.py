@@ -167,6 +167,57 @@ def test_gradients_are_difference_quotients(nf4):
     assert float(h(X + D) - h(X - D)) / 2 == float((dX.double() * D.double()).sum())
 
 
+def test_an_expert_twice_in_one_token(nf4):
+    T, topk, E, H = 70, 4, 3, 40
+    e = torch.tensor([[2, 2, 0, 2]], device=DEV).repeat(T, 1)
+    check_sort(nf4, e, E)
+    _, _, place = nf4.moe_sort(e, E)
+    X = normal((T, H), 1)
+    rows = nf4.moe_gather(X, place)
+    assert torch.equal(rows[place.long()], X.unsqueeze(1).expand(T, topk, H))
+    w = torch.ones((T, topk), device=DEV)
+    w[:, 1] = -1.0
+    w[:, 2:] = 0.0
+    assert not bool(nf4.moe_combine(rows, place, w).any())
+
+
+def test_most_slots_of_a_token_and_most_experts(nf4):
+    T, topk, E, H = 5, 512, 512, 36
+    e = torch.stack([torch.randperm(E, generator=gen(t), device=DEV) for t in range(T)])
+    e[3] = -1
+    check_sort(nf4, e, E)
+    _, _, place = nf4.moe_sort(e, E)
+    Y, w, dOut = normal((T * topk, H), 1), normal((T, topk), 2), normal((T, H), 3)
+    on = place >= 0
+    y = torch.where(on.unsqueeze(2), Y.double()[place.clamp(min=0).long()], 0.0)
+    terms = y * w.double().unsqueeze(2)
+    ref.close(nf4.moe_combine(Y, place, w), terms.sum(1), terms.abs().sum(1), topk, "combine")
+    dY, dw = nf4.moe_combine_grad(dOut, Y, place, w)
+    terms = dOut.double().unsqueeze(1) * y
+    ref.close(dw, terms.sum(2), terms.abs().sum(2), H, "dweights")
+    want = dOut.double().unsqueeze(1) * w.double().unsqueeze(2)
+    ref.close(dY[place[on].long()], want[on], want[on].abs(), 1, "dY")
+
+
+def test_rows_beyond_32_bit_offsets(nf4):
+    T, topk, H = 70000, 4, 8192
+    place = torch.randperm(T * topk, generator=gen(1), device=DEV).int().reshape(T, topk)
+    X = normal((T, H), 2, BF)
+    rows = nf4.moe_gather(X, place)
+    assert rows.numel() * 2 > 1 << 32
+    for j in range(topk):
+        assert torch.equal(rows[place[-50:, j].long()], X[-50:])
+        assert torch.equal(rows[place[:50, j].long()], X[:50])
+    top = int(place.reshape(-1).argmax())  # the slot of the last row
+    assert torch.equal(rows[-1], X[top // topk])
+    w = torch.full((T, topk), 0.25, device=DEV)
+    assert torch.equal(nf4.moe_combine(rows, place, w), X)
+    dY, dw = nf4.moe_combine_grad(X, rows, place, w)
+    assert torch.equal(dY[-1], X[top // topk] * 0.25)
+    want = X[-50:].double().square().sum(1, keepdim=True).expand(50, topk)
+    ref.close(dw[-50:], want, want, H, "dweights")
+
+
 def test_place_entries_outside_the_rows_are_skipped(nf4):
     T, topk, H = 6, 2, 64
     place = torch.arange(T * topk, dtype=torch.int32, device=DEV).reshape(T, topk)

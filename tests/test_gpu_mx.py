@@ -112,6 +112,20 @@ def test_unpack_every_code_at_every_scale(nf4, dtype):
     gpu_guard.check(buf)
 
 
+def test_pack_beyond_32_bit_offsets(nf4):
+    """A matrix of more than 2^32 bytes, packed and unpacked: its last rows."""
+    N, K, last = 70000, 32768, 3
+    W = torch.zeros((N, K), dtype=BF, device=DEV)
+    assert W.numel() * 2 > 1 << 32
+    W[-last:] = normal((last, K), 5, BF)
+    codes, scales = nf4.mx_pack(W)
+    rc, rs, _ = ref.quantise(W[-last:].cpu())
+    assert torch.equal(codes[-last:].cpu(), rc) and torch.equal(scales[-last:].cpu(), rs)
+    assert not bool(codes[:-last].any()) and not bool(scales[:-last].any())
+    nf4.nf4_mx_unpack(codes, scales, W)
+    assert torch.equal(W[-last:].double(), ref.values(codes[-last:], scales[-last:]))
+
+
 # ------------------------------------------------------------- products ----
 MS = [1, 2, 15, 16, 17, 33, 64, 65, 129, 300]
 SHAPES = [(1, 32), (15, 64), (17, 96), (100, 1056), (257, 512), (512, 4128), (2048, 384), (36, 14336)]
@@ -333,6 +347,101 @@ def test_stack_beyond_32_bit_offsets(nf4):
         ref.close(nf4.mx_gemm_grouped(codes, scales, X, off), want, mag, K)
         want, mag = ref.product(dY, v.t())
         ref.close(nf4.mx_gemm_grouped_grad(codes, scales, dY, off), want, mag, N)
+
+
+@pytest.mark.parametrize("M", [1, 3, 40, 300])
+def test_extreme_scales_of_two_packed_matrices(nf4, M):
+    """The smallest scales times the largest, either way round, and both in the middle."""
+    N, K = 70, 256
+    for lo, slo in ((0, 250), (250, 0), (127, 127)):
+        codes, scales = packed((N, K), lo + 1, lo, lo + 4)
+        xcodes, xscales = packed((M, K), slo + 2, slo, slo + 4)
+        want, mag = ref.product(ref.values(xcodes, xscales), ref.values(codes, scales))
+        ref.close(nf4.mx_gemm_packed(codes, scales, xcodes, xscales), want, mag, K, f"{lo} {slo}")
+
+
+@pytest.mark.parametrize("M", [1, 2, 20, 300])
+def test_subnormal_rows(nf4, M):
+    """Rows of bf16 subnormals times weights that bring them back to ordinary values."""
+    N, K = 50, 160
+    codes, scales = packed((N, K), 3, 240, 245)
+    X = (normal((M, K), 4).sign() * 2.0 ** -130).to(BF)
+    assert bool((X != 0).all()) and float(X.float().abs().max()) < 2.0 ** -126
+    want, mag = ref.product(X, ref.values(codes, scales))
+    ref.close(nf4.mx_gemm(codes, scales, X), want, mag, K)
+    off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    dY = (normal((M, 48), 4).sign() * 2.0 ** -130).to(BF)
+    codes, scales = packed((48, K), 3, 240, 245)
+    want, mag = ref.product(dY, ref.values(codes, scales).t())
+    ref.close(nf4.mx_gemm_grouped_grad(codes[None], scales[None], dY, off), want, mag, 48)
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 70, 400])
+def test_longest_rows(nf4, M):
+    """K = 32768 (sixteen chunks of the row kernel), and a gradient over many rows of
+    a narrow matrix."""
+    N, K = 37, 32768
+    codes, scales = packed((N, K), 1)
+    X = normal((M, K), 2, BF)
+    want, mag = ref.product(X, ref.values(codes, scales))
+    ref.close(nf4.mx_gemm(codes, scales, X), want, mag, K)
+    off = torch.tensor([0, M, M, M], dtype=torch.int32, device=DEV)
+    three = [t.expand(3, *t.shape).contiguous() for t in (codes, scales)]
+    ref.close(nf4.mx_gemm_grouped(*three, X, off), want, mag, K)
+    N, K = (1 << 18) + 8, 64
+    codes, scales = packed((N, K), 3)
+    dY = normal((M, N), 4, BF)
+    want, mag = ref.product(dY, ref.values(codes, scales).t())
+    off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    ref.close(nf4.mx_gemm_grouped_grad(codes[None], scales[None], dY, off), want, mag, N)
+
+
+def test_rows_and_outputs_beyond_32_bit_offsets(nf4):
+    """More than 2^32 bytes of X, of Y, of packed rows and of dX: the last rows."""
+    last = 9
+    N, K, M = 48, 16384, 140000
+    codes, scales = packed((N, K), 1)
+    v = ref.values(codes, scales)
+    X = torch.zeros((M, K), dtype=BF, device=DEV)
+    X[-last:] = normal((last, K), 2, BF)
+    assert X.numel() * 2 > 1 << 32
+    want, mag = ref.product(X[-last:], v)
+    Y = nf4.mx_gemm(codes, scales, X)
+    ref.close(Y[-last:], want, mag, K)
+    assert not bool(Y[:-last].any())
+    off = torch.tensor([0, M - last - 3, M - 2], dtype=torch.int32, device=DEV)
+    two = [torch.stack([t, t]) for t in (codes, scales)]
+    Y = nf4.mx_gemm_grouped(*two, X, off)
+    ref.close(Y[M - last:M - 2], want[:-2], mag[:-2], K)
+    assert not bool(Y[-2:].any())
+    dY = torch.zeros((M, N), dtype=BF, device=DEV)
+    dY[-last:] = normal((last, N), 3, BF)
+    want, mag = ref.product(dY[-last:], v.t())
+    dX = X
+    nf4.nf4_mx_gemm_grouped_grad(*two, dY, off, dX)
+    ref.close(dX[M - last:M - 2], want[:-2], mag[:-2], N)
+    assert not bool(dX[-2:].any())
+    del X, dX, dY, Y
+    N, K, M = 65536, 64, 40000
+    codes, scales = packed((N, K), 5)
+    X = normal((M, K), 6, BF)
+    Y = torch.empty((M, N), dtype=BF, device=DEV)
+    assert Y.numel() * 2 > 1 << 32
+    xc, xs = nf4.mx_pack(X)
+    for rows, call in ((X, lambda: nf4.nf4_mx_gemm(codes, scales, X, Y)),
+                       (nf4.mx_unpack(xc, xs), lambda: nf4.nf4_mx_gemm_packed(codes, scales, xc, xs, Y))):
+        Y.fill_(float("nan"))
+        call()
+        want, mag = ref.product(rows[-last:], ref.values(codes, scales))
+        ref.close(Y[-last:], want, mag, K)
+        assert not bool(torch.isnan(Y).any())
+    del Y
+    K, M = 32768, 300000
+    codes, scales = packed((48, K), 7)
+    xc, xs = packed((M, K), 8)
+    assert xc.numel() > 1 << 32
+    want, mag = ref.product(ref.values(xc[-last:], xs[-last:]), ref.values(codes, scales))
+    ref.close(nf4.mx_gemm_packed(codes, scales, xc, xs)[-last:], want, mag, K)
 
 
 # ------------------------------------------------------ streams, graphs ----
