@@ -32,77 +32,120 @@ struct Args {
 // every line is read whole; the lane's 32 values of each row of X stay in
 // registers while the wave walks weight rows.  Waves (c, g) of a workgroup:
 // chunk c of K, weight rows g, g + G, ... of the workgroup's; chunks' sums meet in
-// LDS and are added in order.
-template <int MT, int RP, typename OUT>
-__global__ void __launch_bounds__(1024) mx_gemv_kernel(Args p, int chunks, int rows_wg) {
-  extern __shared__ float part1[];  // [chunk][row of the workgroup][MT]
-  int slot, block;
-  if (!grid_item(p.grid, &slot, &block)) return;
-  const RowTile t = find_tile(p.offsets, p.E, p.R, slot, MT);
-  if (t.rows <= 0) return;
+// LDS and are added in order.  A tile is up to TR rows; the walk is compiled for
+// one, two and TR of them and chosen by how many there are, so an expert with
+// several rows reads its weights once and one with a single row pays for one.
+// Bound by memory where the matrix is large: M = 1, 57344 x 8192 40 us, 6.2 TB/s of codes
+// and scales; 28672 x 4096 13.7 us (4.6 TB/s); 4096 x 14336 9.3 us (3.4), 4096 x 4096
+// 5.4 us (1.6), where starting and filling the pipeline is most of it.  60 rows of 64
+// experts of 4096 x 4096 48.7 us, 5.5 TB/s.
+
+constexpr int kAhead = 4;  // weight rows a wave has in flight
+
+// The sums over the wave of four values a lane, in 10 instructions (44 one at a
+// time): halves, then rows of 16 lanes change places, so each step adds two values'
+// parts at once.  The lanes of row r of 16 end with value 2 (r % 2) + r / 2.
+__device__ __forceinline__ float sum4(const float (&v)[4]) {
+  const auto add = [](auto s) { return __uint_as_float(s[0]) + __uint_as_float(s[1]); };
+  const float a = add(__builtin_amdgcn_permlane32_swap(__float_as_uint(v[0]), __float_as_uint(v[1]), false, false));
+  const float b = add(__builtin_amdgcn_permlane32_swap(__float_as_uint(v[2]), __float_as_uint(v[3]), false, false));
+  float s = add(__builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false));
+  s += dpp_f32<0xB1>(s);   // quad_perm [1,0,3,2]
+  s += dpp_f32<0x4E>(s);   // quad_perm [2,3,0,1]
+  s += dpp_f32<0x141>(s);  // row_half_mirror
+  s += dpp_f32<0x140>(s);  // row_mirror
+  return s;
+}
+
+// MT rows of X (of the TR that `part` is laid out for) against `cols` weight rows.
+template <int MT, int TR>
+__device__ __forceinline__ void walk_rows(const Args &p, const RowTile &t, int n0, int cols, int chunks,
+                                          int rows_wg, float *part) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int groups = (int)(blockDim.x >> 6) / chunks;
   const int c = wave % chunks, g = wave / chunks;
-  const int n0 = block * rows_wg;
-  const int cols = min(rows_wg, p.N - n0);
-  OUT *Y = reinterpret_cast<OUT *>(p.Y);
-  if (t.e >= 0) {
-    const int kb = p.K >> 5;
-    const int64_t first = (int64_t)t.e * p.N + n0;
-    const __amdgpu_buffer_rsrc_t crs = buffer(p.codes + first * (p.K >> 1), (int64_t)cols * (p.K >> 1));
-    const __amdgpu_buffer_rsrc_t srs = buffer(p.scales + first * kb, (int64_t)cols * kb);
-    const __amdgpu_buffer_rsrc_t xrs =
-        buffer(p.X + (int64_t)t.row0 * p.K, (int64_t)t.rows * p.K * 2);
-    const int b = c * 64 + lane;
-    const int out = b < kb ? 0 : kOutside;
-    u32x4_t cw[RP];
-    uint32_t sb[RP];
-    const auto load = [&](int i, int n) {
-      cw[i] = __builtin_amdgcn_raw_buffer_load_b128(crs, (n * (p.K >> 1) + b * 16) | out, 0, kLoadStream);
-      sb[i] = __builtin_amdgcn_raw_buffer_load_b8(srs, (n * kb + b) | out, 0, 0);
-    };
+  const int kb = p.K >> 5, kc = p.K >> 1;
+  const int64_t first = (int64_t)t.e * p.N + n0;
+  const uint8_t *const cbase = p.codes + first * kc, *const sbase = p.scales + first * kb;
+  const __amdgpu_buffer_rsrc_t xrs =
+      buffer(p.X + (int64_t)t.row0 * p.K, (int64_t)t.rows * p.K * 2);
+  const int b = c * 64 + lane;
+  const int out = b < kb ? 0 : kOutside;
+  const int co = b * 16 | out, so = b | out;
+  u32x4_t cw[kAhead];
+  uint32_t sb[kAhead];
+  // The row is the loads' uniform offset; past the last one the buffers are empty.
+  const auto load = [&](int i, int n) __attribute__((always_inline)) {
+    const bool in = n < cols;
+    cw[i] = __builtin_amdgcn_raw_buffer_load_b128(buffer(cbase, in ? cols * kc : 0), co, in ? n * kc : 0,
+                                                  kLoadStream);
+    sb[i] = __builtin_amdgcn_raw_buffer_load_b8(buffer(sbase, in ? cols * kb : 0), so, in ? n * kb : 0, 0);
+  };
 #pragma unroll
-    for (int i = 0; i < RP; ++i) load(i, g + i * groups);
-    u32x4_t x[MT][4];
+  for (int i = 0; i < kAhead; ++i) load(i, g + i * groups);
+  u32x4_t x[MT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[m][j] = __builtin_amdgcn_raw_buffer_load_b128(xrs, (m * p.K * 2 + b * 64 + j * 16) | out, 0, 0);
-    for (int n = g; n < cols; n += RP * groups) {
+    for (int j = 0; j < 4; ++j)
+      x[m][j] = __builtin_amdgcn_raw_buffer_load_b128(xrs, (m * p.K * 2 + b * 64 + j * 16) | out, 0, 0);
+  constexpr int RS = 4 / MT;  // weight rows summed together
+  const int mine = (lane >> 4 & 1) * 2 + (lane >> 5);
+  for (int n = g; n < cols; n += kAhead * groups) {
+    float acc[4];
 #pragma unroll
-      for (int i = 0; i < RP; ++i) {
-        float acc[MT] = {};
-        const float sc = scale_of(sb[i]);
+    for (int i = 0; i < kAhead; ++i) {
+      float *a = acc + i % RS * MT;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4_t w = decode8(cw[i][j], sc);
+      for (int m = 0; m < MT; ++m) a[m] = 0.f;
+      const float sc = scale_of(sb[i]);
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
+      for (int j = 0; j < 4; ++j) {
+        const u32x4_t w = decode8(cw[i][j], sc);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-              acc[m] = __builtin_amdgcn_fdot2_f32_bf16(
-                  __builtin_bit_cast(bf16x2_t, (uint32_t)w[h]),
-                  __builtin_bit_cast(bf16x2_t, (uint32_t)x[m][j][h]), acc[m], false);
-        }
-        load(i, n + (RP + i) * groups);
-        const int r = n + i * groups;
+        for (int h = 0; h < 4; ++h)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const float v = wave_sum(acc[m]);
-          if (lane == 0 && r < cols) part1[(c * rows_wg + r) * MT + m] = v;
-        }
+          for (int m = 0; m < MT; ++m)
+            a[m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, (uint32_t)w[h]),
+                                                   __builtin_bit_cast(bf16x2_t, (uint32_t)x[m][j][h]),
+                                                   a[m], false);
+      }
+      load(i, n + (kAhead + i) * groups);
+      if (i % RS == RS - 1) {
+        const float v = sum4(acc);
+        const int r = n + (i - (RS - 1) + mine / MT) * groups;
+        if ((lane & 15) == 0 && r < cols) part[(c * rows_wg + r) * TR + mine % MT] = v;
       }
     }
   }
+}
+
+template <int TR, typename OUT>
+__global__ void __launch_bounds__(1024) mx_gemv_kernel(Args p, int chunks, int rows_wg) {
+  extern __shared__ float part1[];  // [chunk][row of the workgroup][TR]
+  int slot, block;
+  if (!grid_item(p.grid, &slot, &block)) return;
+  const RowTile t = find_tile(p.offsets, p.E, p.R, slot, TR);
+  if (t.rows <= 0) return;
+  const int n0 = block * rows_wg;
+  const int cols = min(rows_wg, p.N - n0);
+  if (t.e >= 0) {
+    if (t.rows == 1)
+      walk_rows<1, TR>(p, t, n0, cols, chunks, rows_wg, part1);
+    else if (TR > 2 && t.rows == 2)
+      walk_rows<2, TR>(p, t, n0, cols, chunks, rows_wg, part1);
+    else
+      walk_rows<TR, TR>(p, t, n0, cols, chunks, rows_wg, part1);
+  }
   __syncthreads();
+  OUT *Y = reinterpret_cast<OUT *>(p.Y);
   for (int i = threadIdx.x; i < cols * t.rows; i += blockDim.x) {
     const int m = i / cols, r = i - m * cols;
     float v = 0.f;
     if (t.e >= 0) {
-      v = part1[r * MT + m];
-      for (int k = 1; k < chunks; ++k) v += part1[(k * rows_wg + r) * MT + m];
+      v = part1[r * TR + m];
+      for (int k = 1; k < chunks; ++k) v += part1[(k * rows_wg + r) * TR + m];
     }
     OUT *y = Y + (int64_t)(t.row0 + m) * p.N + n0 + r;
     if constexpr (sizeof(OUT) == 4)
@@ -389,28 +432,30 @@ __global__ void __launch_bounds__(64 * WV *KG, 2)
   }
 }
 
-template <int MT>
+template <int TR>
 static int launch_gemv(Args &a, int out_dtype, hipStream_t s) {
-  constexpr int RP = 4;  // 8 rows ahead measured slower, 2 within 3 %
-  const int64_t slots = slots_for(a.R, a.E, a.offsets != nullptr, MT);
-  // 16 weight rows a workgroup (grouped: 32, an expert's rows of X are fewer than
-  // the launch allows for), 8 waves, or 4 where there are plenty of workgroups:
-  // N = 28672, K = 4096, M = 2: 17.8 us with 4 waves, 20.1 with 8; N = 4096: 6.6, 6.4
-  const int rows = a.offsets ? 32 : 16;
+  const int64_t slots = slots_for(a.R, a.E, a.offsets != nullptr, TR);
+  // Weight rows a workgroup.  Dense 16 (4096 x 14336, M = 1: 9.3 us, 8 rows 9.6, 32 13.4).
+  // Grouped, where tiles that turn out empty start workgroups as well: 128, or 32 where
+  // those would be few (30 rows of 16 experts of 4096 x 4096: 28.3 us, 32 rows 29.7; 8 of 8
+  // of 2048 x 2048: 11.5, 32 rows 6.3).
+  const int rows = !a.offsets ? 16 : slots * ((a.N + 127) / 128) >= 640 ? 128 : 32;
   const int chunks = (a.K + 2047) / 2048;
+  // 8 waves, or 4 where there are plenty of workgroups: 28672 x 4096, M = 1: 13.7 us with
+  // 4 waves, 14.8 with 8; 4096 x 4096: 5.8, 5.4
   const int waves = slots * a.N >= 8192 ? 4 : 8;
   const int groups = chunks >= waves ? 1 : waves / chunks;
   a.grid = make_grid(slots, (a.N + rows - 1) / rows, 8);
   const int64_t n = grid_size(a.grid);
   const int threads = 64 * chunks * groups;
   if (n * threads >= (int64_t(1) << 32)) return NF4_ERANGE;
-  const size_t lds = (size_t)chunks * rows * MT * 4;
+  const size_t lds = (size_t)chunks * rows * TR * 4;
   if (out_dtype == NF4_F32)
-    hipLaunchKernelGGL((mx_gemv_kernel<MT, RP, float>), dim3((unsigned)n), dim3(threads), lds, s, a,
-                       chunks, rows);
+    hipLaunchKernelGGL((mx_gemv_kernel<TR, float>), dim3((unsigned)n), dim3(threads), lds, s, a, chunks,
+                       rows);
   else
-    hipLaunchKernelGGL((mx_gemv_kernel<MT, RP, uint16_t>), dim3((unsigned)n), dim3(threads), lds, s,
-                       a, chunks, rows);
+    hipLaunchKernelGGL((mx_gemv_kernel<TR, uint16_t>), dim3((unsigned)n), dim3(threads), lds, s, a,
+                       chunks, rows);
   return launch_status(hipGetLastError());
 }
 
@@ -452,7 +497,10 @@ static int launch_product(Args &a, int out_dtype, hipStream_t s) {
   // rows an expert has on average; popular ones have more
   const int64_t mean = grouped ? (a.R + a.E - 1) / a.E : a.R;
   const int64_t rows = grouped ? mean + mean / 2 : mean;
-  if (mean <= 1) return launch_gemv<1>(a, out_dtype, s);
+  // Grouped, one row an expert: more than one is rare in a few rows, and the tile of one
+  // is faster then (8 rows of 8 experts of 28672 x 4096 57 us, two a tile 62; 60 of 64 of
+  // 4096 x 4096: 63, two a tile 47)
+  if (mean <= 1 && a.R <= 8) return launch_gemv<1>(a, out_dtype, s);
   if (mean <= 2) return launch_gemv<2>(a, out_dtype, s);
   if (mean <= 4 && tiles(16, 64) < 256) return launch_gemv<4>(a, out_dtype, s);
   constexpr int kFill = 384, kSplit = 192;
