@@ -29,6 +29,13 @@ struct GradArgs {
 // share out the n.  A stage is 64 n: the rows' tile of dY and the 64 rows of codes (64
 // bytes a wave) go straight into LDS, three stages in rotation, one barrier a
 // stage; a lane holds the four scale bytes of one n and passes them on through LDS.
+// Decoding (two vector instructions a matrix instruction) runs 32 n ahead: a pair of
+// columns makes room for the next 32 n's as soon as it is multiplied (before: all of
+// it between the matrix instructions of two blocks; 1000 rows of 8 experts 203 -> 191
+// us, 2000 387 -> 364, 16382 1758 -> 1745).  So a wave waits for stage s + 1 in the
+// middle of stage s, when all of s is in its registers, and stage s + 3 goes where s was.
+// Bound by the issue of vector instructions beside the matrix instructions, and by the
+// card's clock, which such loads hold near 2 GHz.
 
 // dY: chunk of 16 bytes of a 128-byte row, permuted as the rows of the product.
 __device__ __forceinline__ int dy_perm(int row) { return (row >> 1) & 7; }
@@ -42,6 +49,16 @@ __device__ __forceinline__ int code_row(int n) {
 template <int WV>
 __device__ __forceinline__ int code_perm(int n) {
   return (n >> 3) & (WV - 1);
+}
+
+// pair j of the 8 codes of w, as decode8
+__device__ __forceinline__ uint32_t decode2(uint32_t w, float scale, int j) {
+  switch (j) {
+    case 0: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+    case 1: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+    case 2: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+    default: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+  }
 }
 
 template <int MF, int WV, int KG, bool SVEC, typename OUT>
@@ -124,57 +141,79 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
         snext[1] = loose.fetch(so, 1);
       }
     };
+    // The words of 32 n: row n = 32 h + 8 q + i (code_row and code_perm written out)
+    struct Raw {
+      uint32_t w[8];
+      float s[8];
+    };
+    const auto read = [&](Raw &w, u32x4_t *b, int buf, int h) __attribute__((always_inline)) {
+      const uint8_t *cr = wlds + buf * WB + (h * 32 + q * 8) * 64 * WV + (wave ^ (q & (WV - 1))) * 64 + l16 * 4;
+      const int swap = WV == 2 ? q >> 1 : 0;
+      const u32x4_t *sr = reinterpret_cast<const u32x4_t *>(slds + buf * 64 + h * 32 + q * 8);
+      const u32x4_t s03 = sr[0], s47 = sr[1];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w.w[i] = *reinterpret_cast<const uint32_t *>(cr + (i ^ swap) * 64 * WV);
+        w.s[i] = scale_of(__builtin_amdgcn_ubfe(i < 4 ? s03[i & 3] : s47[i & 3], 8 * (l16 >> 2), 8));
+      }
+      const uint8_t *xt = xlds + buf * XB + l16 * 128 + ((h * 4 + q) ^ dy_perm(l16)) * 16;
+#pragma unroll
+      for (int r = 0; r < MF; ++r) b[r] = *reinterpret_cast<const u32x4_t *>(xt + r * 2048);
+    };
+    uint32_t d[4][8];  // pairs along k: columns 2 j, 2 j + 1 of the lane's 8, of 8 n
+    const auto decode = [&](const Raw &w, int j) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[j][i] = decode2(w.w[i], w.s[i], j);
+    };
+    // multiplies 32 n; a pair of columns that is done makes room for the next 32 n's
+    const auto multiply = [&](const u32x4_t *b, const Raw &next) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u32x4_t a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          a[i] = __builtin_amdgcn_perm(d[j >> 1][2 * i + 1], d[j >> 1][2 * i],
+                                       (j & 1) ? 0x07060302u : 0x05040100u);
+#pragma unroll
+        for (int r = 0; r < MF; ++r) acc[j][r] = mfma16(a, b[r], acc[j][r]);
+        if (j & 1) decode(next, j >> 1);
+      }
+    };
     const int s0 = kg * per;
-    load_scales(0, s0);
-    load_stage(0, s0);
-    if constexpr (SVEC) load_scales(1, s0 + 1);
-    load_stage(1, s0 + 1);
-    int buf = 0;
-    for (int s = s0; s < s0 + per; ++s) {
-      const int ahead = buf == 0 ? NX - 1 : buf - 1;
+    constexpr int one = XL + WL + (SVEC ? 1 : 0);
+    const auto put_scales = [&](int buf, int s) __attribute__((always_inline)) {
       if constexpr (!SVEC) {
         const LooseWords loose(sbase + (int64_t)s * 64 * kb, 0);
         slds[buf * 64 + lane] = loose.word(so, snext[0], snext[1]);
       }
-      lds_loads_but<XL + WL + (SVEC ? 1 : 0)>();
-      __syncthreads();  // stage s is in LDS; the buffer of the last one is free
-      if constexpr (SVEC)
-        load_scales(ahead, s + 2);
-      else
-        load_scales(0, s + 1);
-      load_stage(ahead, s + 2);
-      const uint8_t *xt = xlds + buf * XB + l16 * 128;
-      const uint8_t *wt = wlds + buf * WB;
+    };
+    load_scales(0, s0);
+    load_stage(0, s0);
+    put_scales(0, s0);
+    load_scales(1, s0 + 1);
+    load_stage(1, s0 + 1);
+    if constexpr (SVEC) load_scales(2, s0 + 2);
+    load_stage(2, s0 + 2);
+    lds_loads_but<2 * one>();
+    __syncthreads();
+    Raw w;
+    u32x4_t b0[MF], b1[MF];
+    read(w, b0, 0, 0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // 32 n: lane quarter q has 8 of them
-        // row n = 32 h + 8 q + i: code_row and code_perm written out
-        const uint8_t *cr = wt + (h * 32 + q * 8) * 64 * WV + (wave ^ (q & (WV - 1))) * 64 + l16 * 4;
-        const int swap = WV == 2 ? q >> 1 : 0;
-        u32x4_t d[8];
-        const u32x4_t *sr = reinterpret_cast<const u32x4_t *>(slds + buf * 64 + h * 32 + q * 8);
-        const u32x4_t s03 = sr[0], s47 = sr[1];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t cw = *reinterpret_cast<const uint32_t *>(cr + (i ^ swap) * 64 * WV);
-          const uint32_t sb = i < 4 ? s03[i & 3] : s47[i & 3];
-          d[i] = decode8(cw, scale_of(__builtin_amdgcn_ubfe(sb, 8 * (l16 >> 2), 8)));
-        }
-        u32x4_t b[MF];
-#pragma unroll
-        for (int r = 0; r < MF; ++r)
-          b[r] = *reinterpret_cast<const u32x4_t *>(xt + r * 2048 + (((h * 4 + q) ^ dy_perm(l16)) * 16));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          u32x4_t a;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            a[i] = __builtin_amdgcn_perm(d[2 * i + 1][j >> 1], d[2 * i][j >> 1],
-                                         (j & 1) ? 0x07060302u : 0x05040100u);
-#pragma unroll
-          for (int r = 0; r < MF; ++r) acc[j][r] = mfma16(a, b[r], acc[j][r]);
-        }
-      }
-      buf = buf == NX - 1 ? 0 : buf + 1;
+    for (int j = 0; j < 4; ++j) decode(w, j);
+    int buf = 0;
+    for (int s = s0; s < s0 + per; ++s) {
+      const int next = buf == NX - 1 ? 0 : buf + 1;
+      read(w, b1, buf, 1);
+      multiply(b0, w);
+      put_scales(next, s + 1);
+      lds_loads_but<one>();
+      __syncthreads();  // stage s + 1 is in LDS; all of stage s has been read
+      load_scales(buf, SVEC ? s + 3 : s + 2);
+      load_stage(buf, s + 3);
+      buf = next;
+      read(w, b0, buf, 0);
+      multiply(b1, w);
     }
     lds_loads_but<0>();
   }
@@ -246,19 +285,20 @@ static int launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
 }
 
 // The largest tile that is not mostly empty and gives every CU work, with N shared out
-// inside the workgroup where tiles are few.  Measured (us, columns x rows of the
-// matrices N x K): 16382 rows of 8 experts of 14336 x 4096: 64 x 512 tiles 1794, 32 x
-// 512 2278; 1000 rows: 64 x 512 228, with two K-groups 195; 1003 rows of 32 of 2048 x
-// 2048: 32 x 512 with two groups 27.7, 64 x 512 with two 34; 300 rows of 8 of 14336 x
-// 4096: 32 x 256 with two groups 103, 32 x 512 with two 154; 8 rows of 8: 16 x 256 with
-// four groups 78, with two 82.
+// inside the workgroup where tiles are few.  Measured (us, rows of experts of
+// columns x rows of the matrices N x K): 16382 of 8 of 14336 x 4096: 64 x 512 tiles 1734
+// (1.11 PFLOP/s), 32 x 512 2205; 2000 rows: 64 x 512 332, with two K-groups 365, 32 x 256
+// with two 368; 1000 rows: 64 x 512 216, with two 192; 1003 of 32 of 2048 x 2048: 32 x 512
+// with two groups 26.4, 64 x 512 with two 34.9; 300 of 8 of 14336 x 4096: 32 x 256 with two
+// 105, 32 x 512 with two 137; 100 of 8 of 2048 x 4096: 16 x 256 with two 16.9, with four
+// 17.4; 8 of 8 of 14336 x 4096: with four 69.4, with two 76.4.
 static int launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
   const auto tiles = [&](int bm, int bk) {
     return slots_for(a.R, a.E, true, bm) * ((a.K + bk - 1) / bk);
   };
   const int64_t mean = (a.R + a.E - 1) / a.E, rows = mean + mean / 2;
   if (rows > 48) {
-    if (tiles(64, 512) >= 512) return launch_grad<4, 4, 1>(a, out_dtype, s);
+    if (tiles(64, 512) >= 256) return launch_grad<4, 4, 1>(a, out_dtype, s);
     if (tiles(64, 512) >= 160) return launch_grad<4, 4, 2>(a, out_dtype, s);
   }
   if (rows > 16) {
