@@ -335,16 +335,24 @@ __global__ void __launch_bounds__(64 * WV *KG, 2)
           else
             load_scales(sbuf ^ 1, g + 1);
         }
-        load_x(buf == 0 ? NX - 1 : buf - 1, s + NX - 1);
-        if constexpr (WS == 1)
-          load_w(buf == 0 ? NX - 1 : buf - 1, s + NX - 1);
-        else if (u % 2 == 0)
-          load_w(wbuf ^ 1, s / 2 + 1);
+        const auto ahead_x = [&]() __attribute__((always_inline)) {
+          load_x(buf == 0 ? NX - 1 : buf - 1, s + NX - 1);
+        };
+        const auto ahead_w = [&]() __attribute__((always_inline)) {
+          if constexpr (WS == 1)
+            load_w(buf == 0 ? NX - 1 : buf - 1, s + NX - 1);
+          else if (u % 2 == 0)
+            load_w(wbuf ^ 1, s / 2 + 1);
+        };
         const uint8_t *xt = xlds + buf * XB + l16 * 128 * KS;
         const uint8_t *wt = wlds + (WS == 1 ? buf : wbuf) * WB + l16 * 32 * KW;
         if constexpr (KS == 1) {
-          // 64 k: MFMA j has k = 32 j + 8 q .. + 7, one word of block j
-          constexpr int half = KW == 1 ? 0 : 2;
+          // 64 k: MFMA j has k = 32 j + 8 q .. + 7, one word of block j.  The order is held:
+          // four fragments of X are read ahead of their products, the second block is
+          // decoded between the first one's, and the next stages' loads go out once the
+          // matrix cores are fed (16382 rows of 8 experts of 14336 x 4096: 1520 -> 1450 us,
+          // the loads alone 1515 -> 1450; 509 x 28672 x 4096: 123 -> 112).
+          constexpr int half = KW == 1 ? 0 : 2, RB = 4;
           uint32_t w[NF][2];
 #pragma unroll
           for (int c = 0; c < NF; ++c)
@@ -352,21 +360,32 @@ __global__ void __launch_bounds__(64 * WV *KG, 2)
             for (int j = 0; j < 2; ++j)
               w[c][j] = *reinterpret_cast<const uint32_t *>(
                   wt + c * 512 * KW + ((u % 2 * half + j) ^ w_perm<KS, KW>(l16)) * 16 + q * 4);
+          u32x4_t b[RB], a[2][NF];
+          const auto read = [&](int t) __attribute__((always_inline)) {
+            b[t % RB] = *reinterpret_cast<const u32x4_t *>(
+                xt + t % MF * 2048 + ((t / MF * 4 + q) ^ x_perm<1>(l16)) * 16);
+          };
+          const auto decode = [&](int j, int c) __attribute__((always_inline)) {
+            a[j][c] = decode8(w[c][j], scale_of((sreg[c][u >> 1] >> (16 * (u & 1) + 8 * j)) & 0xffu));
+          };
+          static_assert(MF >= NF && MF > 5, "the second block is decoded in the first one's time");
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            u32x4_t a[NF];
+          for (int t = 0; t < RB; ++t) read(t);
 #pragma unroll
-            for (int c = 0; c < NF; ++c)
-              a[c] = decode8(w[c][j], scale_of((sreg[c][u >> 1] >> (16 * (u & 1) + 8 * j)) & 0xffu));
+          for (int c = 0; c < NF; ++c) decode(0, c);
 #pragma unroll
-            for (int r = 0; r < MF; ++r) {
-              const u32x4_t b = *reinterpret_cast<const u32x4_t *>(
-                  xt + r * 2048 + (((j * 4 + q) ^ x_perm<1>(l16)) * 16));
+          for (int t = 0; t < 2 * MF; ++t) {
 #pragma unroll
-              for (int c = 0; c < NF; ++c) acc[c][r] = mfma16(a[c], b, acc[c][r]);
-            }
+            for (int c = 0; c < NF; ++c) acc[c][t % MF] = mfma16(a[t / MF][c], b[t % RB], acc[c][t % MF]);
+            if (t + RB < 2 * MF) read(t + RB);
+            if (t < NF) decode(1, t);
+            if (t == 5) ahead_x();
+            if (t == 8) ahead_w();
+            __builtin_amdgcn_sched_barrier(0);
           }
         } else {
+          ahead_x();
+          ahead_w();
 #pragma unroll
           for (int kk = 0; kk < KS / 2; ++kk) {  // 128 k: lane q has block q
             u32x4_t w[NF];
