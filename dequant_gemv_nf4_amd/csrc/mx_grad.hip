@@ -32,7 +32,8 @@ struct GradArgs {
 // Decoding (two vector instructions a matrix instruction) runs 32 n ahead: a pair of
 // columns makes room for the next 32 n's as soon as it is multiplied (before: all of
 // it between the matrix instructions of two blocks; 1000 rows of 8 experts 203 -> 191
-// us, 2000 387 -> 364, 16382 1758 -> 1745).  So a wave waits for stage s + 1 in the
+// us, 2000 387 -> 364, 16382 1758 -> 1745), and the next stage's loads go out after its
+// first products (16382 rows 1732 -> 1660 us).  So a wave waits for stage s + 1 in the
 // middle of stage s, when all of s is in its registers, and stage s + 3 goes where s was.
 // Bound by the issue of vector instructions beside the matrix instructions, and by the
 // card's clock, which such loads hold near 2 GHz.
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
       for (int i = 0; i < 8; ++i) d[j][i] = decode2(w.w[i], w.s[i], j);
     };
     // multiplies 32 n; a pair of columns that is done makes room for the next 32 n's
-    const auto multiply = [&](const u32x4_t *b, const Raw &next) __attribute__((always_inline)) {
+    const auto multiply = [&](const u32x4_t *b, const Raw &next, auto more) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         u32x4_t a;
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
 #pragma unroll
         for (int r = 0; r < MF; ++r) acc[j][r] = mfma16(a, b[r], acc[j][r]);
         if (j & 1) decode(next, j >> 1);
+        more(j);
       }
     };
     const int s0 = kg * per;
@@ -205,15 +207,17 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
     for (int s = s0; s < s0 + per; ++s) {
       const int next = buf == NX - 1 ? 0 : buf + 1;
       read(w, b1, buf, 1);
-      multiply(b0, w);
+      multiply(b0, w, [](int) {});
       put_scales(next, s + 1);
       lds_loads_but<one>();
       __syncthreads();  // stage s + 1 is in LDS; all of stage s has been read
-      load_scales(buf, SVEC ? s + 3 : s + 2);
-      load_stage(buf, s + 3);
+      read(w, b0, next, 0);
+      multiply(b1, w, [&](int j) __attribute__((always_inline)) {
+        if (j != 1) return;  // the loads go out once the matrix cores are fed
+        load_scales(buf, SVEC ? s + 3 : s + 2);
+        load_stage(buf, s + 3);
+      });
       buf = next;
-      read(w, b0, buf, 0);
-      multiply(b1, w);
     }
     lds_loads_but<0>();
   }
@@ -286,8 +290,8 @@ static int launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
 
 // The largest tile that is not mostly empty and gives every CU work, with N shared out
 // inside the workgroup where tiles are few.  Measured (us, rows of experts of
-// columns x rows of the matrices N x K): 16382 of 8 of 14336 x 4096: 64 x 512 tiles 1734
-// (1.11 PFLOP/s), 32 x 512 2205; 2000 rows: 64 x 512 332, with two K-groups 365, 32 x 256
+// columns x rows of the matrices N x K): 16382 of 8 of 14336 x 4096: 64 x 512 tiles 1660
+// (1.16 PFLOP/s), 32 x 512 2205; 2000 rows: 64 x 512 332, with two K-groups 365, 32 x 256
 // with two 368; 1000 rows: 64 x 512 216, with two 192; 1003 of 32 of 2048 x 2048: 32 x 512
 // with two groups 26.4, 64 x 512 with two 34.9; 300 of 8 of 14336 x 4096: 32 x 256 with two
 // 105, 32 x 512 with two 137; 100 of 8 of 2048 x 4096: 16 x 256 with two 16.9, with four
