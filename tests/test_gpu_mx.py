@@ -396,6 +396,54 @@ def test_longest_rows(nf4, M):
     ref.close(nf4.mx_gemm_grouped_grad(codes[None], scales[None], dY, off), want, mag, N)
 
 
+@pytest.mark.parametrize("nan", [False, True])
+@pytest.mark.parametrize("K", [32, 96, 128, 224, 640, 1056])
+def test_largest_tiles(nf4, K, nan):
+    """Enough rows and columns for the largest tiles, the last of each cut short; with
+    `nan`, every second row of either side."""
+    M, N = 3000, 4204
+    codes, scales = packed((N, K), K)
+    X = normal((M, K), K + 1, BF)
+    if nan:
+        scales[1::2] = 255
+        X[1::2] = float("nan")
+    xc, xs = nf4.mx_pack(X, check=False)
+    u, v = nf4.mx_unpack(xc, xs), ref.values(codes, scales)
+    for rows, call in ((X, lambda Y: nf4.nf4_mx_gemm(codes, scales, X, Y)),
+                       (u, lambda Y: nf4.nf4_mx_gemm_packed(codes, scales, xc, xs, Y))):
+        step = 2 if nan else 1
+        want, mag = ref.product(rows[::step], v[::step])
+        for dtype in (F32, BF):
+            buf, Y = gpu_guard.alloc((M, N), dtype, DEV)
+            call(Y)
+            torch.cuda.synchronize()
+            gpu_guard.check(buf)
+            ref.close(Y[::step, ::step].contiguous(), want, mag, K, f"K={K} {dtype}")
+            assert not nan or bool(torch.isnan(Y[1::2]).all() and torch.isnan(Y[:, 1::2]).all())
+
+
+@pytest.mark.parametrize("K", [1024, 2016, 3040])
+@pytest.mark.parametrize("N", [8, 72, 264, 1032])
+def test_gradient_of_many_rows(nf4, N, K):
+    """The tiles of 64 rows, with and without N shared out, N ending inside a stage."""
+    counts = [1900, 0, 1100, 37]
+    R = sum(counts) + 5
+    codes, scales = packed((4, N, K), N + K)
+    dY = normal((R, N), N, BF)
+    off = offsets_of(counts)
+    for dtype in (F32, BF):
+        buf, dX = gpu_guard.alloc((R, K), dtype, DEV)
+        nf4.nf4_mx_gemm_grouped_grad(codes, scales, dY, off, dX)
+        torch.cuda.synchronize()
+        gpu_guard.check(buf)
+        a = 0
+        for e, c in enumerate(counts):
+            want, mag = ref.product(dY[a:a + c], ref.values(codes[e], scales[e]).t())
+            ref.close(dX[a:a + c], want, mag, N, f"expert {e}")
+            a += c
+        assert not bool(dX[a:].any())
+
+
 def test_rows_and_outputs_beyond_32_bit_offsets(nf4):
     """More than 2^32 bytes of X, of Y, of packed rows and of dX: the last rows."""
     last = 9
