@@ -69,6 +69,26 @@ def test_sort_of_many_slots(nf4):
     check_sort(nf4, ids(40000, 5, 100, 3), 100)
 
 
+@pytest.mark.parametrize("E", [1, 63, 64, 127, 128, 255, 256, 511, 512])
+def test_sort_shares_the_chunks_out(nf4, E):
+    """Every division of the chunks' counts over the scan's threads, exactly: keys in
+    ascending order, equal keys in order of slot."""
+    T, topk = 30001, 4
+    e = ids(T, topk, E, E)
+    e[::701] = E - 1
+    offsets, order, place = nf4.moe_sort(e, E)
+    key = torch.where(e < 0, torch.full_like(e, E), e).reshape(-1)
+    want = torch.argsort(key, stable=True)
+    counts = torch.bincount(key, minlength=E + 1)
+    assert offsets.tolist() == [0] + torch.cumsum(counts[:E], 0).tolist()
+    kept = int(offsets[-1])
+    assert torch.equal(order[:kept].long(), want[:kept])
+    assert torch.equal(-order[kept:].long() - 1, want[kept:])
+    row = torch.empty_like(want)
+    row[want] = torch.arange(want.numel(), device=DEV)
+    assert torch.equal(place.reshape(-1).long(), torch.where(key == E, -row - 1, row))
+
+
 @pytest.mark.parametrize("T", [7, 5000])
 def test_sort_one_expert_no_expert_and_bad_ids(nf4, T):
     E = 6
