@@ -164,6 +164,9 @@ __global__ void __launch_bounds__(1024) mx_gemv_kernel(Args p, int chunks, int r
 // codes come the same way, 64 KW values of k at a time (loads of whole 64- or 128-byte
 // pieces of a row, where fragment-shaped loads from memory would touch a line a
 // lane), and a lane's scale bytes for 256 k in one load.
+// Bound by the load path into LDS and, for long prompts, by the matrix cores (67 % busy at
+// the 2 GHz that the card then runs at): 509 x 28672 x 4096 102 us (1.18 PFLOP/s), 16382
+// rows of 8 experts of 14336 x 4096 1457 us (1.32), 1003 rows of 32 of 2048 x 2048 26.6 us.
 
 // Permutation of a row's 16-byte chunks (XOR).  A 16-byte read is served 16 lanes at
 // a time, lanes 0-3, 12-15, 20-27 and so on: rows 0-3 and 12-15 of one lane quarter
