@@ -387,8 +387,6 @@ __global__ void __launch_bounds__(64 * WV *KG, 2)
             __builtin_amdgcn_sched_barrier(0);
           }
         } else {
-          ahead_x();
-          ahead_w();
 #pragma unroll
           for (int kk = 0; kk < KS / 2; ++kk) {  // 128 k: lane q has block q
             u32x4_t w[NF];
@@ -411,6 +409,10 @@ __global__ void __launch_bounds__(64 * WV *KG, 2)
 #pragma unroll
                 for (int c = 0; c < NF; ++c) acc[c][r] = mfma16(a[c], b, acc[c][r]);
               }
+              // the next stages' loads go out once the matrix cores are fed (256 x 28672 x
+              // 4096 73.6 -> 70.3 us, 2000 x 4096 x 4096 74.5 -> 71)
+              if (kk == 0 && j == 0) ahead_x();
+              if (kk == 0 && j == 1) ahead_w();
             }
           }
         }
@@ -505,12 +507,15 @@ static int launch_tile(Args &a, int out_dtype, hipStream_t s) {
 
 // The kernel for a product.  Up to two rows (four where the columns are too few to
 // give every CU a tile): the row kernel.  Else the largest tile that is not mostly
-// empty and still gives a CU one and a half tiles to overlap, else a smaller one
-// with K shared out inside the workgroup.  Measured (us): M = 256, N = K = 4096:
-// 64 x 128 tiles 27.5, 32 x 64 18.1, 16 x 64 with two K-groups 23; M = 16, N = 6144:
-// 16 x 64 12.1, with two K-groups 10.7, 16 x 32 with two 8.6; M = 8, N = 4096, K =
-// 14336: 16 x 32 with two K-groups 21.2, with four 17.5; M = 509, N = 28672: 128 x 256
-// 111, 64 x 128 148.
+// empty and still gives most CUs one (128 x 256, dense) or a CU one and a half to overlap,
+// else a smaller one with K shared out inside the workgroup.  Grouped, tiles of 128 rows
+// pay from 100 rows an expert on: each expert leaves one that is partly empty.
+// Measured (us): 500 rows of 8 experts of 14336 x 4096: 128 x 256 137, 64 x 128 105; 800:
+// 145, 137; 1000: 156, 168.  Dense, M x N x K: 2000 x 4096 x 4096 (256 tiles of 128 x 256):
+// 66.8, 64 x 128 73.3; 256 x 28672 x 4096 (224): 63.8, 71.6; 1500 x 4096 x 4096 (192): 62.3,
+// 58.0; 256 x 4096 x 4096: 64 x 128 27.5, 32 x 64 18.1, 16 x 64 with two K-groups 23;
+// 16 x 6144 x 4096: 16 x 64 12.1, with two K-groups 10.7, 16 x 32 with two 8.6; 8 x 4096 x
+// 14336: 16 x 32 with two K-groups 21.2, with four 17.5.
 static int launch_product(Args &a, int out_dtype, hipStream_t s) {
   const bool grouped = a.offsets != nullptr;
   const auto tiles = [&](int bm, int bn) {
@@ -525,8 +530,8 @@ static int launch_product(Args &a, int out_dtype, hipStream_t s) {
   if (mean <= 1 && a.R <= 8) return launch_gemv<1>(a, out_dtype, s);
   if (mean <= 2) return launch_gemv<2>(a, out_dtype, s);
   if (mean <= 4 && tiles(16, 64) < 256) return launch_gemv<4>(a, out_dtype, s);
-  constexpr int kFill = 384, kSplit = 192;
-  if (rows > 64 && tiles(128, 256) >= kFill) return launch_tile<8, 4, 4, 1, 2, 1>(a, out_dtype, s);
+  constexpr int kBig = 208, kFill = 384, kSplit = 192;
+  if (rows > (grouped ? 150 : 64) && tiles(128, 256) >= (grouped ? kFill : kBig)) return launch_tile<8, 4, 4, 1, 2, 1>(a, out_dtype, s);
   if (rows > 48) {
     if (tiles(64, 128) >= kFill) return launch_tile<4, 2, 4, 2, 2, 1>(a, out_dtype, s);
     if (tiles(64, 64) >= kFill) return launch_tile<4, 1, 4, 2, 2, 1>(a, out_dtype, s);
