@@ -128,18 +128,20 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
       load_lds16xn<WL, WV * 1024>(ws, waddr + buf * WB + wave * 1024, wo);
     };
     // lane: the four block scales of this wave's columns at n = 64 s + lane; rows that
-    // are not whole words go through registers, a stage ahead
+    // are not whole words go through registers, a stage ahead, from one buffer over the
+    // matrix.  Its last word may hold what follows the matrix: a row past N takes zero
+    // instead, since a byte of 255 there would be NaN, and so 0 x NaN in every sum.
     const uint8_t *sbase = p.scales + first * kb;
     const int so = lane * kb + (k0 >> 5) + wave * 4;
+    const LooseWords loose(sbase, (int64_t)p.N * kb);
     uint32_t snext[2];
     const auto load_scales = [&](int buf, int s) {
-      const int bytes = max(p.N - s * 64, 0) * kb;
       if constexpr (SVEC) {
+        const int bytes = max(p.N - s * 64, 0) * kb;
         load_lds4(buffer_words(sbase + (int64_t)s * 64 * kb, bytes), saddr + buf * 256, so);
       } else {
-        const LooseWords loose(sbase + (int64_t)s * 64 * kb, bytes);
-        snext[0] = loose.fetch(so, 0);
-        snext[1] = loose.fetch(so, 1);
+        snext[0] = loose.fetch(so + s * 64 * kb, 0);
+        snext[1] = loose.fetch(so + s * 64 * kb, 1);
       }
     };
     // The words of 32 n: row n = 32 h + 8 q + i (code_row and code_perm written out)
@@ -185,8 +187,8 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
     constexpr int one = XL + WL + (SVEC ? 1 : 0);
     const auto put_scales = [&](int buf, int s) __attribute__((always_inline)) {
       if constexpr (!SVEC) {
-        const LooseWords loose(sbase + (int64_t)s * 64 * kb, 0);
-        slds[buf * 64 + lane] = loose.word(so, snext[0], snext[1]);
+        const uint32_t w = loose.word(so + s * 64 * kb, snext[0], snext[1]);
+        slds[buf * 64 + lane] = s * 64 + lane < p.N ? w : 0u;
       }
     };
     load_scales(0, s0);

@@ -444,6 +444,44 @@ def test_gradient_of_many_rows(nf4, N, K):
         assert not bool(dX[a:].any())
 
 
+@pytest.mark.parametrize("shift", [1, 2, 3])
+@pytest.mark.parametrize("N", [64, 72, 104])
+@pytest.mark.parametrize("K,counts", [(96, [3, 0, 5]), (256, [20, 40]), (2016, [450, 450]),
+                                      (2048, [900, 0, 900]), (2016, [1300, 1300]),
+                                      (2048, [2100, 2100]), (2048, [10] * 60)],
+                         ids=lambda v: str(v) if isinstance(v, int) else f"{len(v)}x{sum(v)}")
+def test_grouped_with_unaligned_scales_between_nan_bytes(nf4, K, counts, N, shift):
+    """Scales at any byte, all bytes around them 255 and each expert but the first
+    beginning with a NaN row: the tiles of every size, stages that N ends in and K-groups
+    whose share is past N keep to the matrix, and NaN to its row and columns."""
+    E, R = len(counts), sum(counts)
+    codes, aligned = packed((E, N, K), K + N + shift)
+    aligned[1:, 0, :2] = 255
+    flat = torch.full((256 + aligned.numel() + 8192,), 255, dtype=torch.uint8, device=DEV)
+    scales = flat[256 + shift:256 + shift + aligned.numel()].view_as(aligned)
+    scales.copy_(aligned)
+    off = offsets_of(counts)
+    X, dY = normal((R, K), 61, BF), normal((R, N), 62, BF)
+    buf, Y = gpu_guard.alloc((R, N), F32, DEV)
+    nf4.nf4_mx_gemm_grouped(codes, scales, X, off, Y)
+    buf2, dX = gpu_guard.alloc((R, K), F32, DEV)
+    nf4.nf4_mx_gemm_grouped_grad(codes, scales, dY, off, dX)
+    torch.cuda.synchronize()
+    gpu_guard.check(buf)
+    gpu_guard.check(buf2)
+    a = 0
+    for e, c in enumerate(counts):
+        v = ref.values(codes[e], scales[e])
+        first, cols = (1, 64) if e else (0, 0)  # rows of the matrix and columns that are NaN
+        want, mag = ref.product(X[a:a + c], v[first:])
+        ref.close(Y[a:a + c, first:], want, mag, K, f"expert {e}")
+        want, mag = ref.product(dY[a:a + c], v[:, cols:].t())
+        ref.close(dX[a:a + c, cols:], want, mag, N, f"gradient of expert {e}")
+        assert bool(torch.isnan(Y[a:a + c, :first]).all())
+        assert bool(torch.isnan(dX[a:a + c, :cols]).all())
+        a += c
+
+
 def test_rows_and_outputs_beyond_32_bit_offsets(nf4):
     """More than 2^32 bytes of X, of Y, of packed rows and of dX: the last rows."""
     last = 9
