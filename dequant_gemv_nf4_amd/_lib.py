@@ -108,6 +108,34 @@ def _stream(device, stream):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _torch_stream(device, stream):
+    """`stream` (a torch stream or a raw handle) as a torch stream of `device`."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(_stream(device, stream).value, device=device)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream` (None: the current one), from that stream's
+    memory: a block of another stream may still be in use by work queued there, and
+    would be handed out again there while this stream still writes it.  So `stream=`
+    is as a call under torch.cuda.stream(stream): outputs are its own, and inputs made
+    elsewhere have to be ready on it and be kept (Tensor.record_stream) until it has
+    used them."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(device, stream)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _read(status, stream):
+    """The value of a status word that a call on `stream` wrote (waits for it)."""
+    if stream is None:
+        return int(status.item())
+    with torch.cuda.stream(_torch_stream(status.device, stream)):
+        return int(status.item())
+
+
 def _run(func, tensors, args, stream):
     """Call func(*args, stream) of the library on the tensors' device: `stream`, or that
     device's current one.  Small calls take less time than their marshalling, so
@@ -669,24 +697,20 @@ def mx_pack(W, stream=None, check=True):
     if K % MX_BLOCK:
         raise ValueError(f"each block of {MX_BLOCK} along K needs scales of its own: K = {K}")
     dev = W.device
-    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((N, K // MX_BLOCK), dtype=torch.uint8, device=dev)
-    status = torch.empty(1, dtype=torch.int32, device=dev) if check else None
+    codes = _empty((N, K // 2), torch.uint8, dev, stream)
+    scales = _empty((N, K // MX_BLOCK), torch.uint8, dev, stream)
+    status = _empty(1, torch.int32, dev, stream) if check else None
     _run("nf4_mx_pack", (W,), (W.data_ptr(), _DTYPE[W.dtype], N, K, codes.data_ptr(),
                                scales.data_ptr(), _addr(status)), stream)
     if check:
-        ts = stream
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            ts = torch.cuda.ExternalStream(_stream(W.device, stream).value, device=W.device)
-        with torch.cuda.stream(ts):  # None: the current one
-            st = int(status.item())
+        st = _read(status, stream)
         if st:
             raise ValueError(f"nf4_mx_pack flagged blocks: status bits {st:#x}")
     return codes, scales
 
 
 def mx_unpack(codes, scales, dtype=torch.float32, stream=None):
-    W = torch.empty((codes.shape[0], 2 * codes.shape[1]), dtype=dtype, device=codes.device)
+    W = _empty((codes.shape[0], 2 * codes.shape[1]), dtype, codes.device, stream)
     nf4_mx_unpack(codes, scales, W, stream)
     return W
 
@@ -694,25 +718,25 @@ def mx_unpack(codes, scales, dtype=torch.float32, stream=None):
 def mx_gemm(codes, scales, X, out_dtype=torch.float32, stream=None):
     """Y [M][N] = X . dequant(codes, scales)^T for any M (a vector X: Y [N])."""
     shape = (X.shape[0], codes.shape[0]) if X.dim() == 2 else (codes.shape[0],)
-    Y = torch.empty(shape, dtype=out_dtype, device=X.device)
+    Y = _empty(shape, out_dtype, X.device, stream)
     nf4_mx_gemm(codes, scales, X, Y, stream)
     return Y
 
 
 def mx_gemm_packed(codes, scales, xcodes, xscales, out_dtype=torch.float32, stream=None):
-    Y = torch.empty((xcodes.shape[0], codes.shape[0]), dtype=out_dtype, device=codes.device)
+    Y = _empty((xcodes.shape[0], codes.shape[0]), out_dtype, codes.device, stream)
     nf4_mx_gemm_packed(codes, scales, xcodes, xscales, Y, stream)
     return Y
 
 
 def mx_gemm_grouped(codes, scales, X, offsets, out_dtype=torch.float32, stream=None):
-    Y = torch.empty((X.shape[0], codes.shape[1]), dtype=out_dtype, device=X.device)
+    Y = _empty((X.shape[0], codes.shape[1]), out_dtype, X.device, stream)
     nf4_mx_gemm_grouped(codes, scales, X, offsets, Y, stream)
     return Y
 
 
 def mx_gemm_grouped_grad(codes, scales, dY, offsets, out_dtype=torch.float32, stream=None):
-    dX = torch.empty((dY.shape[0], 2 * codes.shape[2]), dtype=out_dtype, device=dY.device)
+    dX = _empty((dY.shape[0], 2 * codes.shape[2]), out_dtype, dY.device, stream)
     nf4_mx_gemm_grouped_grad(codes, scales, dY, offsets, dX, stream)
     return dX
 
@@ -721,9 +745,9 @@ def moe_sort(experts, num_experts, stream=None):
     """(offsets, order, place) of experts int64 [T][topk]; see nf4_moe_sort."""
     _need(experts, "experts", (torch.int64,), (2,))
     dev = experts.device
-    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-    order = torch.empty(experts.numel(), dtype=torch.int32, device=dev)
-    place = torch.empty(experts.shape, dtype=torch.int32, device=dev)
+    offsets = _empty(num_experts + 1, torch.int32, dev, stream)
+    order = _empty(experts.numel(), torch.int32, dev, stream)
+    place = _empty(experts.shape, torch.int32, dev, stream)
     T, topk = experts.shape
     _run("nf4_moe_sort", (experts,), (experts.data_ptr(), T, topk, int(num_experts), offsets.data_ptr(),
                                       order.data_ptr(), place.data_ptr(), None), stream)
@@ -731,20 +755,20 @@ def moe_sort(experts, num_experts, stream=None):
 
 
 def moe_gather(X, place, stream=None):
-    out = torch.empty((place.numel(), X.shape[-1]), dtype=X.dtype, device=X.device)
+    out = _empty((place.numel(), X.shape[-1]), X.dtype, X.device, stream)
     nf4_moe_gather(X, place, out, stream)
     return out
 
 
 def moe_combine(Y, place, weights=None, stream=None):
-    out = torch.empty((place.shape[0], Y.shape[-1]), dtype=Y.dtype, device=Y.device)
+    out = _empty((place.shape[0], Y.shape[-1]), Y.dtype, Y.device, stream)
     nf4_moe_combine(Y, place, weights, out, stream)
     return out
 
 
 def moe_combine_grad(dOut, Y, place, weights, stream=None):
     """(dY, dweights) of moe_combine."""
-    dY = torch.empty_like(Y)
-    dw = torch.empty(place.shape, dtype=torch.float32, device=Y.device)
+    dY = _empty(Y.shape, Y.dtype, Y.device, stream)
+    dw = _empty(place.shape, torch.float32, Y.device, stream)
     nf4_moe_combine_grad(dOut, Y, place, weights, dY, dw, stream)
     return dY, dw

@@ -1,0 +1,111 @@
+"""Calls with `stream=`: the functions that allocate take their outputs' memory from
+the stream they run on, so neither work still queued on the current stream nor later
+allocations there share it while it is written."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def nf4():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    import dequant_gemv_nf4_amd as m
+    m._lib._load()
+    return m
+
+
+@pytest.fixture(scope="module")
+def args(nf4):
+    """Inputs whose outputs have sizes of their own, all above the allocator's small blocks."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    E, N, K, R = 2, 4096, 2048, 1024
+    W = torch.randn((N, K), generator=g, device=DEV)
+    codes, scales = nf4.mx_pack(W)
+    X = torch.randn((R, K), generator=g, device=DEV).to(BF)
+    xc, xs = nf4.mx_pack(X)
+    ids = torch.randint(0, E, (1 << 18, 4), generator=g, device=DEV)
+    route = torch.randint(0, E, (R // 2, 2), generator=g, device=DEV)
+    offsets, _, place = nf4.moe_sort(route, E)
+    w = torch.rand((R // 2, 2), generator=g, device=DEV)
+    out = dict(W=W, codes=codes, scales=scales, stack=torch.stack([codes, codes]),
+               sstack=torch.stack([scales, scales]), X=X, xc=xc, xs=xs, ids=ids, offsets=offsets,
+               place=place, w=w, dY=torch.randn((R, N), generator=g, device=DEV).to(BF))
+    torch.cuda.synchronize()
+    return out
+
+
+CALLS = {
+    "mx_pack": lambda m, a, s: m.mx_pack(a["W"], stream=s, check=False),
+    "mx_unpack": lambda m, a, s: m.mx_unpack(a["codes"], a["scales"], stream=s),
+    "mx_gemm": lambda m, a, s: m.mx_gemm(a["codes"], a["scales"], a["X"], stream=s),
+    "mx_gemm_packed": lambda m, a, s: m.mx_gemm_packed(a["codes"], a["scales"], a["xc"], a["xs"],
+                                                       stream=s),
+    "mx_gemm_grouped": lambda m, a, s: m.mx_gemm_grouped(a["stack"], a["sstack"], a["X"],
+                                                         a["offsets"], stream=s),
+    "mx_gemm_grouped_grad": lambda m, a, s: m.mx_gemm_grouped_grad(
+        a["stack"], a["sstack"], a["dY"], a["offsets"], stream=s),
+    "moe_sort": lambda m, a, s: m.moe_sort(a["ids"], 2, stream=s),
+    "moe_gather": lambda m, a, s: m.moe_gather(a["X"][:512], a["place"], stream=s),
+    "moe_combine": lambda m, a, s: m.moe_combine(a["X"], a["place"], a["w"], stream=s),
+    "moe_combine_grad": lambda m, a, s: m.moe_combine_grad(a["X"][:512], a["X"], a["place"],
+                                                           a["w"], stream=s),
+}
+
+
+def tensors(out):
+    return list(out) if isinstance(out, tuple) else [out]
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_are_the_streams_own(nf4, args, name, raw):
+    main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    want = [t.clone() for t in tensors(CALLS[name](nf4, args, None))]
+    torch.cuda.synchronize()
+    # blocks of the outputs' sizes, freed on the current stream with work queued on them
+    busy = torch.empty((4096, 4096), device=DEV)
+    freed = [torch.empty_like(t) for t in want for _ in range(2)]
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in freed]
+    for _ in range(20):
+        busy = busy @ busy
+    for t in freed:
+        t.fill_(0)
+    del t, freed
+    got = tensors(CALLS[name](nf4, args, stream))
+    for t in got:
+        a, b = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+        assert all(b <= lo or hi <= a for lo, hi in spans)
+    main.wait_stream(side)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    # a result that is dropped is not handed out to the current stream
+    torch.cuda.synchronize()
+    got = tensors(CALLS[name](nf4, args, stream))
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in got]
+    del got, t
+    for t in [torch.empty_like(t) for t in want for _ in range(2)]:
+        a, b = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+        assert all(b <= lo or hi <= a for lo, hi in spans)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_mx_pack_reads_its_status_on_the_stream(nf4, args, raw):
+    """check=True waits for the call's own stream, behind work queued there."""
+    side = torch.cuda.Stream()
+    W = args["W"].clone()
+    W[7, 3] = float("nan")
+    busy = torch.randn((4096, 4096), device=DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            busy = busy @ busy
+    with pytest.raises(ValueError, match="flagged"):
+        nf4.mx_pack(W, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
