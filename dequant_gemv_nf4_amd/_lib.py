@@ -122,7 +122,7 @@ def _empty(shape, dtype, device, stream):
     is as a call under torch.cuda.stream(stream): outputs are its own, and inputs made
     elsewhere have to be ready on it and be kept (Tensor.record_stream) until it has
     used them."""
-    if stream is None or device.type != "cuda":
+    if stream is None or torch.device(device).type != "cuda":
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(_torch_stream(device, stream)):
         return torch.empty(shape, dtype=dtype, device=device)
@@ -318,12 +318,7 @@ def workspace_for(device, nbytes, stream=None):
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         size = max(nbytes, 1 << 16, 2 * ws.numel() if ws is not None else 0)
-        if isinstance(stream, torch.cuda.Stream):
-            ts = stream
-        elif stream is None:
-            ts = torch.cuda.current_stream(device)
-        else:
-            ts = torch.cuda.ExternalStream(handle, device=device)
+        ts = torch.cuda.current_stream(device) if stream is None else _torch_stream(device, stream)
         with torch.cuda.device(device), torch.cuda.stream(ts):
             new = torch.zeros(size, dtype=torch.uint8, device=device)
         if ws is not None:
@@ -459,39 +454,39 @@ def nf4_codebook():
 
 
 # ---- allocation conveniences (torch allocates; the library is then called) ----
-def empty_packed(N, K, device):
-    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=device)
-    scales = torch.empty((N, K // GROUP), dtype=torch.int16, device=device)
+def empty_packed(N, K, device, stream=None):
+    codes = _empty((N, K // 2), torch.uint8, device, stream)
+    scales = _empty((N, K // GROUP), torch.int16, device, stream)
     return codes, scales
 
 
 def pack(W, stream=None, check=True):
     """Allocate and fill (codes, scales) for W; with check=True raise on flagged groups."""
     N, K = W.shape
-    codes, scales = empty_packed(N, K, W.device)
-    status = torch.zeros(1, dtype=torch.int32, device=W.device) if check else None
+    codes, scales = empty_packed(N, K, W.device, stream)
+    status = _empty(1, torch.int32, W.device, stream) if check else None
     nf4_pack(W, codes, scales, status, stream)
     if check:
-        st = int(status.item())
+        st = _read(status, stream)
         if st:
             raise ValueError(f"nf4_pack flagged groups: status bits {st:#x}")
     return codes, scales
 
 
 def unpack(codes, scales, K, stream=None):
-    W = torch.empty((codes.shape[0], K), dtype=torch.float32, device=codes.device)
+    W = _empty((codes.shape[0], K), torch.float32, codes.device, stream)
     nf4_unpack(codes, scales, W, stream)
     return W
 
 
 def gemv(codes, scales, x, stream=None):
-    y = torch.empty(codes.shape[0], dtype=torch.float32, device=x.device)
+    y = _empty(codes.shape[0], torch.float32, x.device, stream)
     nf4_gemv(codes, scales, x, y, stream)
     return y
 
 
 def embed(codes, scales, K, ids, stream=None):
-    out = torch.empty((ids.numel(), K), dtype=torch.bfloat16, device=codes.device)
+    out = _empty((ids.numel(), K), torch.bfloat16, codes.device, stream)
     nf4_embed(codes, scales, K, ids, out, None, stream)
     return out
 
@@ -501,7 +496,7 @@ def gemm(codes, scales, X, stream=None):
     small-batch kernels (with a kept workspace where K splits over workgroups),
     beyond that on the prefill tiles."""
     M = 1 if X.dim() == 1 else X.shape[0]
-    Y = torch.empty((M, codes.shape[0]), dtype=torch.float32, device=X.device)
+    Y = _empty((M, codes.shape[0]), torch.float32, X.device, stream)
     if M <= MAX_M:
         need = smallm_workspace_bytes(codes.shape[0], X.shape[-1], M)
         if need:

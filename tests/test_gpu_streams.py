@@ -36,6 +36,10 @@ def args(nf4):
     out = dict(W=W, codes=codes, scales=scales, stack=torch.stack([codes, codes]),
                sstack=torch.stack([scales, scales]), X=X, xc=xc, xs=xs, ids=ids, offsets=offsets,
                place=place, w=w, dY=torch.randn((R, N), generator=g, device=DEV).to(BF))
+    out["ncodes"], out["nscales"] = nf4.pack(W)
+    out["rows"] = torch.randint(0, N, (2000,), generator=g, device=DEV)
+    out["wide"] = torch.stack([out["ncodes"]] * 80).reshape(80 * N, K // 2)
+    out["wscales"] = torch.stack([out["nscales"]] * 80).reshape(80 * N, K // 64)
     torch.cuda.synchronize()
     return out
 
@@ -55,6 +59,12 @@ CALLS = {
     "moe_combine": lambda m, a, s: m.moe_combine(a["X"], a["place"], a["w"], stream=s),
     "moe_combine_grad": lambda m, a, s: m.moe_combine_grad(a["X"][:512], a["X"], a["place"],
                                                            a["w"], stream=s),
+    "pack": lambda m, a, s: m.pack(a["W"], stream=s, check=False),
+    "unpack": lambda m, a, s: m.unpack(a["ncodes"], a["nscales"], 2048, stream=s),
+    "gemv": lambda m, a, s: m.gemv(a["wide"], a["wscales"], a["X"][0], stream=s),
+    "gemm-small": lambda m, a, s: m.gemm(a["wide"], a["wscales"], a["X"][:8], stream=s),
+    "gemm-prompt": lambda m, a, s: m.gemm(a["ncodes"], a["nscales"], a["X"], stream=s),
+    "embed": lambda m, a, s: m.embed(a["ncodes"], a["nscales"], 2048, a["rows"], stream=s),
 }
 
 
@@ -96,7 +106,8 @@ def test_outputs_are_the_streams_own(nf4, args, name, raw):
 
 
 @pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
-def test_mx_pack_reads_its_status_on_the_stream(nf4, args, raw):
+@pytest.mark.parametrize("name", ["mx_pack", "pack"])
+def test_packing_reads_its_status_on_the_stream(nf4, args, name, raw):
     """check=True waits for the call's own stream, behind work queued there."""
     side = torch.cuda.Stream()
     W = args["W"].clone()
@@ -107,5 +118,5 @@ def test_mx_pack_reads_its_status_on_the_stream(nf4, args, raw):
         for _ in range(20):
             busy = busy @ busy
     with pytest.raises(ValueError, match="flagged"):
-        nf4.mx_pack(W, stream=side.cuda_stream if raw else side)
+        getattr(nf4, name)(W, stream=side.cuda_stream if raw else side)
     torch.cuda.synchronize()
