@@ -736,16 +736,23 @@ def mx_gemm_grouped_grad(codes, scales, dY, offsets, out_dtype=torch.float32, st
     return dX
 
 
-def moe_sort(experts, num_experts, stream=None):
-    """(offsets, order, place) of experts int64 [T][topk]; see nf4_moe_sort."""
+def moe_sort(experts, num_experts, stream=None, check=False):
+    """(offsets, order, place) of experts int64 [T][topk]; see nf4_moe_sort.  An id that is
+    neither -1 nor in [0, num_experts) counts as -1; with check=True it raises (a host
+    synchronisation, so not under capture)."""
     _need(experts, "experts", (torch.int64,), (2,))
     dev = experts.device
     offsets = _empty(num_experts + 1, torch.int32, dev, stream)
     order = _empty(experts.numel(), torch.int32, dev, stream)
     place = _empty(experts.shape, torch.int32, dev, stream)
+    status = _empty(1, torch.int32, dev, stream) if check else None
     T, topk = experts.shape
     _run("nf4_moe_sort", (experts,), (experts.data_ptr(), T, topk, int(num_experts), offsets.data_ptr(),
-                                      order.data_ptr(), place.data_ptr(), None), stream)
+                                      order.data_ptr(), place.data_ptr(), _addr(status)), stream)
+    if check:
+        st = _read(status, stream)
+        if st:
+            raise ValueError(f"nf4_moe_sort flagged expert ids: status bits {st:#x}")
     return offsets, order, place
 
 

@@ -100,6 +100,25 @@ def test_sort_one_expert_no_expert_and_bad_ids(nf4, T):
         check_sort(nf4, e, E)
 
 
+@pytest.mark.parametrize("T", [7, 5000])
+@pytest.mark.parametrize("side", [False, True], ids=["current", "side"])
+def test_sort_refuses_bad_ids_when_asked(nf4, T, side):
+    E = 6
+    stream = torch.cuda.Stream() if side else None
+    e = ids(T, 3, E, 5)
+    good = [t.clone() for t in nf4.moe_sort(e, E)]
+    torch.cuda.synchronize()
+    for a, b in zip(nf4.moe_sort(e, E, stream=stream, check=True), good):
+        assert torch.equal(a, b)
+    for bad in (E, -2, 1 << 40, -(1 << 62)):
+        e[T // 2, 1] = bad
+        torch.cuda.synchronize()
+        with pytest.raises(ValueError, match="expert ids"):
+            nf4.moe_sort(e, E, stream=stream, check=True)
+        offsets, order, place = nf4.moe_sort(e, E)  # not asked: a slot without an expert
+        assert int(place[T // 2, 1]) < 0
+
+
 def test_no_tokens(nf4):
     e = torch.empty((0, 2), dtype=torch.int64, device=DEV)
     offsets, order, place = nf4.moe_sort(e, 4)
