@@ -285,10 +285,16 @@ int nf4_ring_destroy(nf4_ring *ring);
  *  - scales uint8 [N][K/32].
  *  K is a multiple of 32, at most NF4_MAX_K; N * K / 2 < 2^31 (one matrix).
  *  dtype arguments: NF4_F32 or NF4_BF16.
- * The products sum in fp32; the packed values are exact in bf16, so per output
- *   |Y - Y_exact| <= 2^-24 * (K + 8) * sum_k |X[m][k] v(n,k)|,
- * plus half a unit of bf16 where the output is bf16, for finite sums.  NaN and
- * infinities in X or a NaN scale reach the outputs of their row or column only.
+ * The products sum in fp32.  Up to s = 252, the largest that nf4_mx_pack writes, every
+ * value is exact in bf16 and fp32.  Beyond it values reach 2^128 (magnitudes from 4 on
+ * at s = 253, from 2 on at 254): they are infinite in nf4_mx_unpack and in the products
+ * with bf16 rows, and finite in nf4_mx_gemm_packed, which multiplies the codes.
+ * Per output, with T terms (K; N in the gradient), S = sum |x v| over them at most
+ * 2^127, and every v finite as above:
+ *   |Y - Y_exact| <= (T + 8) * (2^-24 * S + 2^-149),
+ * plus half a unit of bf16 (at least 2^-134) where the output is bf16.  (A product is
+ * exact but below 2^-126, where it is rounded to a multiple of 2^-149; none is flushed.)
+ * NaN and infinities in X or a NaN scale reach the outputs of their row or column only.
  * Rules of ownership, streams, errors and determinism are those above.
  */
 #define NF4_MX_BLOCK 32 /* values per scale byte, along K */
@@ -310,8 +316,8 @@ int nf4_mx_pack(const void *W, int dtype, int64_t N, int64_t K, uint8_t *codes, 
                 int32_t *dev_status, void *stream);
 
 /*
- * nf4_mx_unpack -- the values of a packed matrix, W_out [N][K] in fp32 (exact, up
- * to overflow to infinity at s > 252) or bf16 (the same values: they fit it).
+ * nf4_mx_unpack -- the values of a packed matrix, W_out [N][K] in fp32 or bf16, exact
+ * in both (infinite from 2^128 on, as above).
  * Alignment: codes 4 bytes, W_out 16.
  */
 int nf4_mx_unpack(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, void *W_out,

@@ -376,6 +376,79 @@ def test_subnormal_rows(nf4, M):
     ref.close(nf4.mx_gemm_grouped_grad(codes[None], scales[None], dY, off), want, mag, 48)
 
 
+def within(got, want, mag, terms):
+    """(terms + 8) (2^-24 of the magnitudes + 2^-149), and half a unit of bf16."""
+    tol = (terms + 8) * (2.0 ** -24 * mag + 2.0 ** -149)
+    if got.dtype == BF:
+        tol = tol * (1 + 2.0 ** -8) + torch.clamp(2.0 ** -8 * want.abs(), min=2.0 ** -134)
+    err = (got.double() - want).abs()
+    assert bool((err <= tol).all()), f"worst {float((err / tol).max()):.3g} x tolerance"
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("size", [-165, -150, -140, -126, -100])
+@pytest.mark.parametrize("M", [1, 2, 3, 40, 300])
+def test_sums_near_the_smallest_numbers(nf4, M, size, dtype):
+    """Products around 2^size: below 2^-126 they are rounded to multiples of 2^-149, and
+    neither they nor their sums are flushed."""
+    N, K = 264, 160
+    half = size // 2
+    codes, scales = packed((N, K), size % 97, 126 + half, 129 + half)
+    X = normal((M, K), 4).mul(2.0 ** (size - half)).to(BF)
+    dY = normal((M, N), 5).mul(2.0 ** (size - half)).to(BF)
+    v = ref.values(codes, scales)
+    within(nf4.mx_gemm(codes, scales, X, out_dtype=dtype), *ref.product(X, v), K)
+    off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    within(nf4.mx_gemm_grouped(codes[None], scales[None], X, off, out_dtype=dtype),
+           *ref.product(X, v), K)
+    within(nf4.mx_gemm_grouped_grad(codes[None], scales[None], dY, off, out_dtype=dtype),
+           *ref.product(dY, v.t()), N)
+    xc, xs = nf4.mx_pack(X)
+    within(nf4.mx_gemm_packed(codes, scales, xc, xs, out_dtype=dtype),
+           *ref.product(ref.values(xc, xs), v), K)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 40, 300])
+def test_scales_beyond_what_packing_writes(nf4, M):
+    """s = 253 and 254: values of 2^128 and more are infinite with bf16 rows and finite
+    between two packed matrices; up to s = 252 all are finite."""
+    N, K = 264, 160
+    X = normal((M, K), 4).mul(2.0 ** -20).to(BF)
+    X[-1, 66] = 0.0
+    dY = normal((M, N), 5).mul(2.0 ** -20).to(BF)
+    off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    xc, xs = nf4.mx_pack(X)
+    for s in (252, 253, 254):
+        codes, scales = packed((N, K), s, 100, 110)
+        codes &= 0x33  # magnitudes up to 1.5
+        scales[:] = 240
+        scales[5, 2] = s
+        codes[5, 33] = 0x67 if s == 252 else 0x06 if s == 253 else 0x04  # 6, 4; 4; 2
+        v = ref.values(codes, scales)
+        u = ref.values(xc, xs)
+        want, mag = ref.product(u, v)
+        within(nf4.mx_gemm_packed(codes, scales, xc, xs), want, mag, K)
+        big = v.abs() >= 2.0 ** 128
+        assert int(big.sum()) == (0 if s == 252 else 1)
+        v = torch.where(big, torch.sign(v) * float("inf"), v)
+        for Y in (nf4.mx_gemm(codes, scales, X),
+                  nf4.mx_gemm_grouped(codes[None], scales[None], X, off)):
+            inf = big.any(1)
+            want, mag = ref.product(X, v[~inf])
+            within(Y[:, ~inf], want, mag, K)
+            if s > 252:  # the sign of the one infinite product; NaN where x is zero
+                x = X[:, big[5]].reshape(-1).double()
+                want = torch.where(x == 0, float("nan"), torch.sign(x) * float("inf"))
+                assert torch.equal(Y[:, 5].double().nan_to_num(7.0), want.nan_to_num(7.0))
+        dX = nf4.mx_gemm_grouped_grad(codes[None], scales[None], dY, off)
+        inf = big.any(0)
+        want, mag = ref.product(dY, v[:, ~inf].t())
+        within(dX[:, ~inf], want, mag, N)
+        if s > 252:
+            want = torch.sign(dY[:, 5].double()) * float("inf")
+            assert torch.equal(dX[:, inf].reshape(-1).double(), want)
+
+
 @pytest.mark.parametrize("M", [1, 2, 4, 5, 70, 400])
 def test_longest_rows(nf4, M):
     """K = 32768 (sixteen chunks of the row kernel), and a gradient over many rows of
