@@ -41,6 +41,9 @@ struct Args {
 // experts of 4096 x 4096 48.7 us, 5.5 TB/s.
 
 constexpr int kAhead = 4;  // weight rows a wave has in flight
+// Row tiles of one column block that go to one XCD (a group of the grid): a weight row
+// that several of them need comes from memory once.
+constexpr int kRowTiles = 8;
 
 // The sums over the wave of four values a lane, in 10 instructions (44 one at a
 // time): halves, then rows of 16 lanes change places, so each step adds two values'
@@ -469,7 +472,7 @@ static int launch_gemv(Args &a, int out_dtype, hipStream_t s) {
   // 4 waves, 14.8 with 8; 4096 x 4096: 5.8, 5.4
   const int waves = slots * a.N >= 8192 ? 4 : 8;
   const int groups = chunks >= waves ? 1 : waves / chunks;
-  a.grid = make_grid(slots, (a.N + rows - 1) / rows, 8);
+  a.grid = make_grid(slots, (a.N + rows - 1) / rows, kRowTiles);
   const int64_t n = grid_size(a.grid);
   const int threads = 64 * chunks * groups;
   if (n * threads >= (int64_t(1) << 32)) return NF4_ERANGE;
@@ -524,10 +527,19 @@ static int launch_product(Args &a, int out_dtype, hipStream_t s) {
   // rows an expert has on average; popular ones have more
   const int64_t mean = grouped ? (a.R + a.E - 1) / a.E : a.R;
   const int64_t rows = grouped ? mean + mean / 2 : mean;
-  // Grouped, one row an expert: more than one is rare in a few rows, and the tile of one
-  // is faster then (8 rows of 8 experts of 28672 x 4096 57 us, two a tile 62; 60 of 64 of
-  // 4096 x 4096: 63, two a tile 47)
-  if (mean <= 1 && a.R <= 8) return launch_gemv<1>(a, out_dtype, s);
+  // Up to kRowTiles rows, in one group of the grid: an expert's weights come from memory
+  // once even if every row has a tile of its own, and the tiles work side by side.  Beyond
+  // that two groups on two XCDs would read them.  One row a tile against two, us, weights
+  // from memory, experts drawn at random / with falling shares / all rows one expert's:
+  //   28672 x 4096, 8 rows of 8:   61.9 59.6 43.3    64.7 64.5 44.2
+  //                 9 rows of 8:   84.0 81.0 69.5    64.7 63.8 57.2
+  //   4096 x 14336, 8 rows of 64:  38.9 36.7 24.4    41.1 40.8 25.2
+  //                 9 rows of 64:  54.8 53.0 41.3    48.8 44.5 35.0
+  //   2048 x 2048,  8 rows of 8:    6.3  6.1  5.7     6.8  6.7  6.4
+  //                 9 rows of 8:    8.0  7.9  7.5     7.0  6.8  6.3
+  // Fewer rows: between 20 % faster and 8 % slower, but for 5 rows that are all one
+  // expert's (28672 x 4096: 34.2 against 28.0).
+  if (mean <= 1 && a.R <= kRowTiles) return launch_gemv<1>(a, out_dtype, s);
   if (mean <= 2) return launch_gemv<2>(a, out_dtype, s);
   if (mean <= 4 && tiles(16, 64) < 256) return launch_gemv<4>(a, out_dtype, s);
   constexpr int kBig = 208, kFill = 384, kSplit = 192;

@@ -287,6 +287,21 @@ def test_grouped_and_gradient(nf4, counts, tail, N, K):
         assert not bool(Y[a:].any()) and not bool(dX[a:].any())
 
 
+@pytest.mark.parametrize("R", [7, 8, 9, 10])
+@pytest.mark.parametrize("counts", ["spread", "pairs", "one"])
+def test_grouped_around_the_rows_of_one_grid_group(nf4, counts, R):
+    """As many row tiles as share an XCD and one more or less: rows of experts of their
+    own, in pairs, and all of one expert."""
+    E, N, K = 12, 264, 288
+    codes, scales = packed((E, N, K), R)
+    at = {"spread": list(range(R)), "pairs": [2 + i // 2 for i in range(R)], "one": [5] * R}[counts]
+    X = normal((R, K), 41, BF)
+    Y = nf4.mx_gemm_grouped(codes, scales, X, offsets_of([at.count(e) for e in range(E)]))
+    for i, e in enumerate(at):
+        want, mag = ref.product(X[i:i + 1], ref.values(codes[e], scales[e]))
+        ref.close(Y[i:i + 1], want, mag, K, f"row {i}")
+
+
 def test_grouped_without_rows(nf4):
     codes, scales = packed((3, 32, 64), 1)
     off = torch.zeros(4, dtype=torch.int32, device=DEV)
