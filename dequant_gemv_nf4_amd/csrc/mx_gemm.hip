@@ -508,17 +508,28 @@ static int launch_tile(Args &a, int out_dtype, hipStream_t s) {
   return launch_tile_as<MF, NF, WV, KS, KW, KG, false>(a, out_dtype, s);
 }
 
-// The kernel for a product.  Up to two rows (four where the columns are too few to
-// give every CU a tile): the row kernel.  Else the largest tile that is not mostly
-// empty and still gives most CUs one (128 x 256, dense) or a CU one and a half to overlap,
-// else a smaller one with K shared out inside the workgroup.  Grouped, tiles of 128 rows
-// pay from 100 rows an expert on: each expert leaves one that is partly empty.
-// Measured (us): 500 rows of 8 experts of 14336 x 4096: 128 x 256 137, 64 x 128 105; 800:
-// 145, 137; 1000: 156, 168.  Dense, M x N x K: 2000 x 4096 x 4096 (256 tiles of 128 x 256):
-// 66.8, 64 x 128 73.3; 256 x 28672 x 4096 (224): 63.8, 71.6; 1500 x 4096 x 4096 (192): 62.3,
-// 58.0; 256 x 4096 x 4096: 64 x 128 27.5, 32 x 64 18.1, 16 x 64 with two K-groups 23;
-// 16 x 6144 x 4096: 16 x 64 12.1, with two K-groups 10.7, 16 x 32 with two 8.6; 8 x 4096 x
-// 14336: 16 x 32 with two K-groups 21.2, with four 17.5.
+// The kernel for a product: the largest tile that is not mostly empty and still gives the
+// CUs enough of them, else a smaller one with K shared out inside the workgroup (K-groups).
+// Measured, us, M x N x K or rows of experts of N x K, weights from memory (in brackets:
+// tiles of the kind taken):
+//   taken                    case                               others
+//   row kernel, 2 rows       2 x 4096 x 14336          9.7      16 x 32: 14.7
+//   row kernel, 4 rows       4 x 4096 x 14336         12.9      16 x 32: 15.0
+//                            4 x 6144 x 4096           9.6      16 x 32: 7.2
+//   128 x 256                2000 x 4096 x 4096 (256)   68      64 x 128: 74
+//                            256 x 28672 x 4096 (224)   68      64 x 128: 74
+//   128 x 256, grouped       1000 of 8 of 14336 x 4096 159      64 x 128: 171
+//   64 x 128                 1500 x 4096 x 4096         58      128 x 256 (192): 65
+//                            640 x 4096 x 4096 (320)  34.6      32 x 128: 35.8, 64 x 64: 41.2
+//                            64 x 28672 x 4096 (224)  29.4      32 x 128: 32.6, 64 x 64: 32.8
+//   64 x 128, grouped        800 of 8 of 14336 x 4096  137      128 x 256: 154, 32 x 128: 155
+//   32 x 128, grouped        1003 of 32 of 2048 x 2048  31      64 x 128: 32.7, 32 x 64: 36.8
+//   32 x 64                  256 x 4096 x 4096 (512)  18.4      64 x 128: 23.5, two K-groups: 20.7
+//   32 x 64, two K-groups    100 x 4096 x 4096 (256)  11.7      one: 13.6, 16 x 64: 14.1
+//   16 x 64                  16 x 28672 x 4096 (448)  20.8      two K-groups: 21.1
+//   16 x 64, two K-groups    16 x 10240 x 4096 (160)   9.1      one: 11.1, 16 x 32: 12.6
+//   16 x 32, four K-groups   16 x 8192 x 4096 (256)    8.0      16 x 64, two: 9.0
+//                            8 x 4096 x 14336 (128)   15.8      16 x 64, two: 23.2; two: 19.3
 static int launch_product(Args &a, int out_dtype, hipStream_t s) {
   const bool grouped = a.offsets != nullptr;
   const auto tiles = [&](int bm, int bn) {
@@ -543,19 +554,17 @@ static int launch_product(Args &a, int out_dtype, hipStream_t s) {
   if (mean <= 2) return launch_gemv<2>(a, out_dtype, s);
   if (mean <= 4 && tiles(16, 64) < 256) return launch_gemv<4>(a, out_dtype, s);
   constexpr int kBig = 208, kFill = 384, kSplit = 192;
-  if (rows > (grouped ? 150 : 64) && tiles(128, 256) >= (grouped ? kFill : kBig)) return launch_tile<8, 4, 4, 1, 2, 1>(a, out_dtype, s);
-  if (rows > 48) {
-    if (tiles(64, 128) >= kFill) return launch_tile<4, 2, 4, 2, 2, 1>(a, out_dtype, s);
-    if (tiles(64, 64) >= kFill) return launch_tile<4, 1, 4, 2, 2, 1>(a, out_dtype, s);
-  }
+  // grouped, each expert leaves one that is partly empty
+  if (rows > (grouped ? 150 : 64) && tiles(128, 256) >= (grouped ? kFill : kBig))
+    return launch_tile<8, 4, 4, 1, 2, 1>(a, out_dtype, s);
+  if (rows > 48 && tiles(64, 128) >= kSplit) return launch_tile<4, 2, 4, 2, 2, 1>(a, out_dtype, s);
   if (rows > 16) {
     if (tiles(32, 128) >= kFill) return launch_tile<2, 2, 4, 2, 2, 1>(a, out_dtype, s);
     if (tiles(32, 64) >= kFill) return launch_tile<2, 1, 4, 4, 4, 1>(a, out_dtype, s);
     if (tiles(32, 64) >= kSplit) return launch_tile<2, 1, 4, 4, 4, 2>(a, out_dtype, s);
   }
   if (tiles(16, 64) >= kFill) return launch_tile<1, 1, 4, 4, 4, 1>(a, out_dtype, s);
-  if (tiles(16, 64) >= kSplit) return launch_tile<1, 1, 4, 4, 4, 2>(a, out_dtype, s);
-  if (tiles(16, 32) > 256) return launch_tile<1, 1, 2, 4, 4, 2>(a, out_dtype, s);
+  if (tiles(16, 32) > 256) return launch_tile<1, 1, 4, 4, 4, 2>(a, out_dtype, s);
   return launch_tile<1, 1, 2, 4, 4, 4>(a, out_dtype, s);
 }
 

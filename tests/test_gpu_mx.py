@@ -570,6 +570,23 @@ def test_grouped_with_unaligned_scales_between_nan_bytes(nf4, K, counts, N, shif
         a += c
 
 
+@pytest.mark.parametrize("K", [160, 1152])
+@pytest.mark.parametrize("M,N", [(2, 5001), (4, 5001), (10, 5001), (16, 8200), (10, 9001),
+                                 (10, 25000), (40, 7001), (17, 14001), (40, 28672), (50, 28675),
+                                 (100, 14001), (500, 6300), (300, 20004)])
+def test_every_tile_of_the_product(nf4, M, N, K):
+    """Rows and columns on each side of the sizes at which another tile is taken."""
+    codes, scales = packed((N, K), M + N)
+    X = normal((M, K), 3, BF)
+    want, mag = ref.product(X, ref.values(codes, scales))
+    buf, Y = gpu_guard.alloc((M, N), F32, DEV)
+    nf4.nf4_mx_gemm(codes, scales, X, Y)
+    torch.cuda.synchronize()
+    gpu_guard.check(buf)
+    ref.close(Y, want, mag, K)
+    ref.close(nf4.mx_gemm(codes, scales, X, out_dtype=BF), want, mag, K)
+
+
 def test_rows_and_outputs_beyond_32_bit_offsets(nf4):
     """More than 2^32 bytes of X, of Y, of packed rows and of dX: the last rows."""
     last = 9
