@@ -17,8 +17,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // Each wave owns up to kSortGroups groups of 64 consecutive slots, whose keys it holds in
 // registers from one load.  Up to 64 * kSortGroups slots a wave one workgroup counts,
 // scans and ranks by itself; beyond that three kernels do, a workgroup per chunk.  Bound
-// by latency up to tens of thousands of slots: 5 x 2 slots 2.4 us, 2048 x 2 6.9, 8191 x 4
-// 12.5 in three launches.
+// by latency up to tens of thousands of slots: 5 x 2 slots 2.4 us, 2048 x 2 6.3, 8191 x 4
+// 12 in three launches back to back (kernels of 5.0, 5.1 and 5.7-6.2 when traced apart).
 constexpr int kSortGroups = 8;
 constexpr int kSortMaxE = NF4_MOE_MAX_E;
 // Slots of a chunk (the last one takes what is left, less than two chunks).  More

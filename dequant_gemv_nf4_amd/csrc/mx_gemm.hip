@@ -35,10 +35,10 @@ struct Args {
 // LDS and are added in order.  A tile is up to TR rows; the walk is compiled for
 // one, two and TR of them and chosen by how many there are, so an expert with
 // several rows reads its weights once and one with a single row pays for one.
-// Bound by memory where the matrix is large: M = 1, 57344 x 8192 40 us, 6.2 TB/s of codes
-// and scales; 28672 x 4096 13.7 us (4.6 TB/s); 4096 x 14336 9.3 us (3.4), 4096 x 4096
-// 5.4 us (1.6), where starting and filling the pipeline is most of it.  60 rows of 64
-// experts of 4096 x 4096 48.7 us, 5.5 TB/s.
+// Bound by memory where the matrix is large, else by starting and filling the pipeline.
+// Measured, M = 1, us with weights from memory (TB/s of codes and scales): 57344 x 8192 42.4
+// (5.9), 28672 x 4096 13.3 (4.7), 4096 x 14336 8.5 (3.7), 4096 x 4096 4.8 (1.9).  60 rows of
+// 64 experts of 4096 x 4096: 53 (5.1).
 
 constexpr int kAhead = 4;  // weight rows a wave has in flight
 // Row tiles of one column block that go to one XCD (a group of the grid): a weight row
@@ -168,8 +168,9 @@ __global__ void __launch_bounds__(1024) mx_gemv_kernel(Args p, int chunks, int r
 // pieces of a row, where fragment-shaped loads from memory would touch a line a
 // lane), and a lane's scale bytes for 256 k in one load.
 // Bound by the load path into LDS and, for long prompts, by the matrix cores (67 % busy at
-// the 2 GHz that the card then runs at): 509 x 28672 x 4096 102 us (1.18 PFLOP/s), 16382
-// rows of 8 experts of 14336 x 4096 1457 us (1.32), 1003 rows of 32 of 2048 x 2048 26.6 us.
+// the 2 GHz that the card then runs at).  Measured: 509 x 28672 x 4096 102-107 us (1.12-1.17
+// PFLOP/s), 117 with weights from memory; 16382 rows of 8 experts of 14336 x 4096 1457-1538
+// (1.25-1.32) from one card to the next; 1003 rows of 32 of 2048 x 2048 27, from memory 31.
 
 // Permutation of a row's 16-byte chunks (XOR).  A 16-byte read is served 16 lanes at
 // a time, lanes 0-3, 12-15, 20-27 and so on: rows 0-3 and 12-15 of one lane quarter
@@ -462,10 +463,10 @@ __global__ void __launch_bounds__(64 * WV *KG, 2)
 template <int TR>
 static int launch_gemv(Args &a, int out_dtype, hipStream_t s) {
   const int64_t slots = slots_for(a.R, a.E, a.offsets != nullptr, TR);
-  // Weight rows a workgroup.  Dense 16 (4096 x 14336, M = 1: 9.3 us, 8 rows 9.6, 32 13.4).
-  // Grouped, where tiles that turn out empty start workgroups as well: 128, or 32 where
-  // those would be few (30 rows of 16 experts of 4096 x 4096: 28.3 us, 32 rows 29.7; 8 of 8
-  // of 2048 x 2048: 11.5, 32 rows 6.3).
+  // Weight rows a workgroup.  Dense 16 (4096 x 14336, M = 1: 9.3 us; 8 rows 9.6; 32 13.4).
+  // Grouped, where tiles that turn out empty start workgroups as well: 128 (30 rows of 16
+  // experts of 4096 x 4096: 28.3; 32 rows 29.7), or 32 where those would be few (8 of 8 of
+  // 2048 x 2048: 6.3; 128 rows 11.5).
   const int rows = !a.offsets ? 16 : slots * ((a.N + 127) / 128) >= 640 ? 128 : 32;
   const int chunks = (a.K + 2047) / 2048;
   // 8 waves, or 4 where there are plenty of workgroups: 28672 x 4096, M = 1: 13.7 us with

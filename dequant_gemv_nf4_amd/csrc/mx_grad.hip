@@ -33,10 +33,11 @@ struct GradArgs {
 // columns makes room for the next 32 n's as soon as it is multiplied (before: all of
 // it between the matrix instructions of two blocks; 1000 rows of 8 experts 203 -> 191
 // us, 2000 387 -> 364, 16382 1758 -> 1745), and the next stage's loads go out after its
-// first products (16382 rows 1732 -> 1660 us).  So a wave waits for stage s + 1 in the
+// first products (16382 rows 1732 -> 1660 us, each pair on one card).  So a wave waits for stage s + 1 in the
 // middle of stage s, when all of s is in its registers, and stage s + 3 goes where s was.
 // Bound by the issue of vector instructions beside the matrix instructions, and by the
-// card's clock, which such loads hold near 2 GHz.
+// card's clock, which such loads hold near 2 GHz: 16382 rows of 8 experts of 14336 x 4096
+// 1600-1710 us from one card to the next (1.13-1.20 PFLOP/s).
 
 // dY: chunk of 16 bytes of a 128-byte row, permuted as the rows of the product.
 __device__ __forceinline__ int dy_perm(int row) { return (row >> 1) & 7; }
@@ -291,13 +292,18 @@ static int launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
 }
 
 // The largest tile that is not mostly empty and gives every CU work, with N shared out
-// inside the workgroup where tiles are few.  Measured (us, rows of experts of
-// columns x rows of the matrices N x K): 16382 of 8 of 14336 x 4096: 64 x 512 tiles 1660
-// (1.16 PFLOP/s), 32 x 512 2205; 2000 rows: 64 x 512 332, with two K-groups 365, 32 x 256
-// with two 368; 1000 rows: 64 x 512 216, with two 192; 1003 of 32 of 2048 x 2048: 32 x 512
-// with two groups 26.4, 64 x 512 with two 34.9; 300 of 8 of 14336 x 4096: 32 x 256 with two
-// 105, 32 x 512 with two 137; 100 of 8 of 2048 x 4096: 16 x 256 with two 16.9, with four
-// 17.4; 8 of 8 of 14336 x 4096: with four 69.4, with two 76.4.
+// inside the workgroup (K-groups) where tiles are few.  Measured, us, rows of experts of
+// matrices N x K, weights from memory:
+//   taken                   case                               others
+//   64 x 512                16382 of 8 of 14336 x 4096  1700   32 x 512, two K-groups: 2408
+//                           2000 of 8 of 14336 x 4096    324   two K-groups: 354
+//   64 x 512, two K-groups  1000 of 8 of 14336 x 4096    173   one: 199, 32 x 512, two: 279
+//   32 x 512, two           1003 of 32 of 2048 x 2048   27.9   64 x 512, two: 33.6; 32 x 256, two: 32.9
+//   32 x 256, two           300 of 8 of 14336 x 4096     101   32 x 512, two: 141; 16 x 256, two: 146
+//                           500 of 8 of 14336 x 4096     165   32 x 512, two: 140
+//   16 x 256, two           60 of 64 of 4096 x 4096     74.8   four: 79.9
+//   16 x 256, four          8 of 8 of 14336 x 4096      79.7   two: 83.3
+//                           64 of 1 of 4096 x 4096      25.1   two: 28.0
 static int launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
   const auto tiles = [&](int bm, int bk) {
     return slots_for(a.R, a.E, true, bm) * ((a.K + bk - 1) / bk);

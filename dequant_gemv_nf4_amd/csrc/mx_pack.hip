@@ -27,10 +27,11 @@ __device__ __forceinline__ uint32_t dpp_max_quad(uint32_t v) {
 }
 
 // One thread per 8 consecutive values (one 32-bit word of codes), four threads
-// per block, so loads and stores are whole lines.  Bound by memory: 28672 x 4096 fp32
-// packed and unpacked 177 us, 6.0 TB/s; fp32 is read past the caches, which bf16, an
-// activation that a kernel has just written, is not.  A NaN or infinity anywhere in the block is seen as exponent 255 of
-// the largest magnitude's bits, which is also the scale byte it then gets.
+// per block, so loads and stores are whole lines.  Bound by memory.  fp32, weights, is read
+// past the caches; bf16, an activation that a kernel has just written, is not.  A NaN or
+// infinity anywhere in the block is seen as exponent 255 of the largest magnitude's bits,
+// which is also the scale byte it then gets.  Measured, 28672 x 4096 fp32: 97 us, 5.5 TB/s;
+// 4096 x 4096 bf16: 13 us, 9.5 where it is still in the caches.
 template <typename T>
 __global__ void __launch_bounds__(256) mx_pack_kernel(const T *__restrict__ W, int64_t nwords,
                                                       uint32_t *__restrict__ codes,
@@ -79,8 +80,9 @@ __global__ void __launch_bounds__(256) mx_pack_kernel(const T *__restrict__ W, i
 
 __global__ void mx_clear_status_kernel(int32_t *status) { *status = 0; }
 
-// One thread per word of codes -> 8 values (time: with the packing above); the conversion multiplies by the
-// block's power of two (255: NaN).
+// One thread per word of codes -> 8 values; the conversion multiplies by the block's
+// power of two (255: NaN).  Bound by memory: 28672 x 4096 to fp32 95-104 us, 5.1-5.6 TB/s,
+// to bf16 55 us, 5.4 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(256) mx_unpack_kernel(const uint32_t *__restrict__ codes,
                                                         const uint8_t *__restrict__ scales,

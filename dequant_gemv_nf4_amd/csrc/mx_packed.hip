@@ -37,9 +37,9 @@ __device__ __forceinline__ f32x4_t mfma_scaled(u32x4_t a, uint32_t sa, u32x4_t b
 // loaded straight into LDS, NB stages in rotation, one barrier a stage (whole 128-byte
 // pieces: 64-byte ones and a stage more in flight took 8 % longer).  Scales come
 // the same way, 16 bytes (512 k) a row.  Bound by the loads of both operands and, where
-// the output is large, by writing it after the last stage: 4096 x 28672 x 4096 318 us
-// (3.0 PFLOP/s, the matrix cores 34 % busy; 75-85 us are the 470 MB of Y), 37 x 6144 x 4096
-// 6.8 us.
+// the output is large, by writing it after the last stage.  Measured: 4096 x 28672 x 4096
+// 318-335 us (2.9-3.0 PFLOP/s, the matrix cores 34 % busy; 75-85 us are the 470 MB of Y),
+// 37 x 6144 x 4096 6.9 us.
 
 // Permutation (XOR) of the 16-byte chunks of a row of 64 KS bytes: the rows that LDS
 // serves together in a fragment read (0-3 and 12-15 of one lane quarter with 4-11
@@ -258,12 +258,18 @@ static int launch_tile(PackedArgs &a, int out_dtype, hipStream_t s) {
 }
 
 // The largest tile that is not mostly empty and leaves few CUs without one, else a
-// small one with K shared out inside the workgroup.  Measured (us), M x N x K: 4096 x 28672 x
-// 4096: 256 x 256 tiles 314, 128 x 128 354; 2048 x 4096 x 14336: 128 x 128 79 (512
-// tiles), 256 x 256 111 (128); 512 x 4096 x 4096: 64 x 128 13.7, 128 x 128 18.1; 256 x
-// 4096 x 4096: 64 x 64 with two K-groups 9.4, with one 10.0; 37 x 6144 x 4096: 32 x 64
-// with two 7.4, 64 x 64 with two 8.5; 16 x 4096 x 14336: 16 x 64 with two 13.2, with
-// one 15.8; 1 x 28672 x 4096: with two 16.4, with one 14.5.
+// small one with K shared out inside the workgroup (K-groups).  Measured, us, M x N x K,
+// weights from memory (in brackets: tiles of the kind taken):
+//   taken                    case                               others
+//   256 x 256                4096 x 28672 x 4096 (1792)  335    128 x 128: 371
+//                            4096 x 4096 x 4096 (256)     52    128 x 128: 60
+//   128 x 128                2048 x 4096 x 14336 (512)    87    256 x 256 (128): 119, 64 x 128: 116
+//   64 x 128                 512 x 4096 x 4096 (256)    14.3    128 x 128: 18.7
+//                            64 x 28672 x 4096 (224)    18.7    64 x 64, two K-groups: 22.0
+//   64 x 64, two K-groups    256 x 4096 x 4096 (256)     9.8    64 x 128: 13.1, 32 x 64, two: 13.2
+//   32 x 64, two             37 x 6144 x 4096 (192)      7.6    64 x 64, two: 8.6; 16 x 64: 8.5
+//   16 x 64                  1 x 28672 x 4096 (448)     14.0    two K-groups: 16.7
+//   16 x 64, two             16 x 4096 x 14336 (64)     13.4    one: 19.3; 32 x 64, two: 15.3
 static int launch_packed(PackedArgs &a, int out_dtype, hipStream_t s) {
   const auto tiles = [&](int bm, int bn) {
     return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);

@@ -1,5 +1,5 @@
-// nf4_check.h -- host-side argument checks and the output conversion shared by
-// the MXFP4 and routing entry points (internal to libnf4).
+// nf4_check.h -- host-side argument checks shared by the MXFP4 and routing entry
+// points (internal to libnf4).
 #pragma once
 
 #include <hip/hip_runtime.h>
