@@ -112,7 +112,10 @@ def _torch_stream(device, stream):
     """`stream` (a torch stream or a raw handle) as a torch stream of `device`."""
     if isinstance(stream, torch.cuda.Stream):
         return stream
-    return torch.cuda.ExternalStream(_stream(device, stream).value, device=device)
+    handle = _stream(device, stream).value
+    if not handle:  # a null handle makes torch take a stream of its pool
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
 
 
 def _empty(shape, dtype, device, stream):

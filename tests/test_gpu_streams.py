@@ -120,3 +120,50 @@ def test_packing_reads_its_status_on_the_stream(nf4, args, name, raw):
     with pytest.raises(ValueError, match="flagged"):
         getattr(nf4, name)(W, stream=side.cuda_stream if raw else side)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("null", ["handle", "stream"])
+@pytest.mark.parametrize("name", CALLS)
+def test_the_default_stream_by_its_null_handle(nf4, args, name, null):
+    """Another stream is current: the call runs on the default one, behind work queued
+    there, and takes its memory."""
+    default, side = torch.cuda.default_stream(), torch.cuda.Stream()
+    stream = default if null == "stream" else default.cuda_stream
+    assert default.cuda_stream == 0
+    want = [t.clone() for t in tensors(CALLS[name](nf4, args, None))]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = tensors(CALLS[name](nf4, args, stream))
+    # freed on the default stream, its blocks serve the next such call there
+    spans = [t.data_ptr() for t in got]
+    side.wait_stream(default)
+    with torch.cuda.stream(side):
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    side.synchronize()
+    del got
+    again = tensors(CALLS[name](nf4, args, None))
+    assert sorted(t.data_ptr() for t in again) == sorted(spans)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", ["mx_pack", "pack", "moe_sort"])
+def test_status_on_the_null_handle(nf4, args, name):
+    W, ids = args["W"].clone(), args["ids"].clone()
+    W[7, 3] = float("nan")
+    ids[9, 1] = 5
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with pytest.raises(ValueError, match="flagged"):
+            if name == "moe_sort":
+                nf4.moe_sort(ids, 2, stream=0, check=True)
+            else:
+                getattr(nf4, name)(W, stream=0)
+
+
+def test_workspace_of_the_null_handle(nf4):
+    default = torch.cuda.default_stream()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        ws = nf4.workspace_for(DEV, 1 << 20, 0)
+        assert nf4.workspace_for(DEV, 1 << 20, default) is ws
+    default.synchronize()
+    assert not bool(ws.any())
