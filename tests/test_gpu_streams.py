@@ -167,3 +167,34 @@ def test_workspace_of_the_null_handle(nf4):
         assert nf4.workspace_for(DEV, 1 << 20, default) is ws
     default.synchronize()
     assert not bool(ws.any())
+
+
+@pytest.mark.parametrize("fork", [False, True], ids=["same", "forked"])
+def test_captured_with_a_stream_argument(nf4, args, fork):
+    """Calls on the capturing stream by its argument, or on one that forks from it and
+    joins again; every replay against the eager call, with eager work in between."""
+    X = args["X"].clone()
+
+    def step(s):
+        xc, xs = nf4.mx_pack(X, stream=s, check=False)
+        rows = nf4.moe_gather(X[:512], args["place"], stream=s)
+        return (nf4.mx_gemm(args["codes"], args["scales"], X, stream=s),
+                nf4.mx_gemm_packed(args["codes"], args["scales"], xc, xs, stream=s),
+                nf4.mx_gemm_grouped(args["stack"], args["sstack"], rows, args["offsets"], stream=s))
+    step(None)
+    torch.cuda.synchronize()
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        if fork:
+            other.wait_stream(main)
+        out = step(other if fork else main)
+        if fork:
+            main.wait_stream(other)
+    for i in range(3):
+        X.copy_(torch.randn(X.shape, device=DEV).to(BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, step(None)))
+        torch.cuda.synchronize()
