@@ -162,9 +162,11 @@ def test_status_on_the_null_handle(nf4, args, name):
 
 def test_workspace_of_the_null_handle(nf4):
     default = torch.cuda.default_stream()
+    kept = nf4.workspace_for(DEV, 1 << 16, default)  # other calls may have used this one
     with torch.cuda.stream(torch.cuda.Stream()):
-        ws = nf4.workspace_for(DEV, 1 << 20, 0)
-        assert nf4.workspace_for(DEV, 1 << 20, default) is ws
+        assert nf4.workspace_for(DEV, 1 << 16, 0) is kept
+        ws = nf4.workspace_for(DEV, kept.numel() + 1, 0)
+        assert ws is not kept and nf4.workspace_for(DEV, kept.numel() + 1, default) is ws
     default.synchronize()
     assert not bool(ws.any())
 
