@@ -44,6 +44,11 @@ from ._lib import (  # noqa: F401
     MOE_BAD_ID,
     MOE_MAX_E,
     MX_BLOCK,
+    mx_linear,
+    mx_linear_grad,
+    mx_linear_grad_workspace_bytes,
+    nf4_mx_linear,
+    nf4_mx_linear_grad,
     moe_combine,
     moe_combine_grad,
     moe_gather,

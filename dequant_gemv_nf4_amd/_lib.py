@@ -76,6 +76,12 @@ def _load():
     L.nf4_moe_gather.argtypes = [vp, ci, vp, i64, i64, i64, vp, vp]
     L.nf4_moe_combine.argtypes = [vp, ci, vp, vp, i64, i64, i64, vp, vp]
     L.nf4_moe_combine_grad.argtypes = [vp, vp, ci, vp, vp, i64, i64, i64, vp, vp, vp]
+    L.nf4_mx_linear.argtypes = [vp, vp, i64, i64, vp, i64, vp, ci, ci, vp, vp, ci, vp, vp]
+    L.nf4_mx_linear_grad.argtypes = [vp, vp, i64, i64, vp, vp, ci, i64, vp, vp, vp, ci, vp, i64, vp]
+    L.nf4_mx_linear_grad_workspace_bytes.argtypes = [i64, i64, i64]
+    L.nf4_mx_linear_grad_workspace_bytes.restype = i64
+    for f in (L.nf4_mx_linear, L.nf4_mx_linear_grad):
+        f.restype = ci
     for f in (L.nf4_mx_pack, L.nf4_mx_unpack, L.nf4_mx_gemm, L.nf4_mx_gemm_packed,
               L.nf4_mx_gemm_grouped, L.nf4_mx_gemm_grouped_grad, L.nf4_moe_sort,
               L.nf4_moe_gather, L.nf4_moe_combine, L.nf4_moe_combine_grad):
@@ -777,3 +783,111 @@ def moe_combine_grad(dOut, Y, place, weights, stream=None):
     dw = _empty(place.shape, torch.float32, Y.device, stream)
     nf4_moe_combine_grad(dOut, Y, place, weights, dY, dw, stream)
     return dY, dw
+
+
+# ---- fused forms of the MXFP4 products ----
+ACTS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5, "geglu": 6}
+GATED_ACTS = ("swiglu", "geglu")
+
+
+def _act(act, N):
+    """(the library's number of `act`, columns that it makes of N)."""
+    if act not in ACTS:
+        raise ValueError(f"act is {act!r}, expected one of {tuple(ACTS)}")
+    if act not in GATED_ACTS:
+        return ACTS[act], N
+    if N % 2:
+        raise ValueError(f"{act} gates one half of the rows with the other: N = {N} is odd")
+    return ACTS[act], N // 2
+
+
+def _like(t, name, shape, dtypes):
+    _need(t, name, dtypes)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, has {tuple(t.shape)}")
+
+
+def nf4_mx_linear(codes, scales, X, Y, bias=None, act=None, residual=None, Z=None, stream=None):
+    """Y [M][N] ([M][N/2] for a gated act; fp32 or bf16) = act(X . dequant(codes, scales)^T +
+    bias) + residual; Z bf16 [M][N], if given, receives what the activation is taken of."""
+    N, K = _mx_matrix(codes, scales)
+    number, cols = _act(act, N)
+    _need(X, "X", _BF16, (1, 2))
+    if X.shape[-1] != K:
+        raise ValueError(f"X has {X.shape[-1]} columns, the matrix K = {K}")
+    lead = tuple(X.shape[:-1])
+    _like(Y, "Y", lead + (cols,), _FLOATS)
+    if bias is not None:
+        _like(bias, "bias", (N,), _FLOATS)
+    if residual is not None:
+        _like(residual, "residual", lead + (cols,), (Y.dtype,))
+    if Z is not None:
+        _like(Z, "Z", lead + (N,), _BF16)
+    _run("nf4_mx_linear", (X, codes, scales, Y, bias, residual, Z),
+         (codes.data_ptr(), scales.data_ptr(), N, K, X.data_ptr(), lead[0] if lead else 1,
+          _addr(bias), 0 if bias is None else _DTYPE[bias.dtype], number, _addr(residual),
+          Y.data_ptr(), _DTYPE[Y.dtype], _addr(Z)), stream)
+
+
+def mx_linear_grad_workspace_bytes(N, K, M):
+    """Bytes of workspace nf4_mx_linear_grad needs for (N, K, M); 0 = none."""
+    n = _load().nf4_mx_linear_grad_workspace_bytes(int(N), int(K), int(M))
+    if n < 0:
+        raise ValueError(f"invalid shape N={N} K={K} M={M}")
+    return int(n)
+
+
+def nf4_mx_linear_grad(codes, scales, dY, Z, act, dX, dZ=None, dbias=None, workspace=None, stream=None):
+    """dX [M][K] (fp32 or bf16), dZ bf16 [M][N] and dbias fp32 [N] of nf4_mx_linear from dY
+    bf16 [M][N] ([M][N/2] gated) and the Z that it kept; N % 8 == 0.  Z and dZ may be None
+    without an activation.  workspace: uint8, mx_linear_grad_workspace_bytes(N, K, M)."""
+    N, K = _mx_matrix(codes, scales)
+    number, cols = _act(act, N)
+    _need(dY, "dY", _BF16, (1, 2))
+    lead = tuple(dY.shape[:-1])
+    _like(dY, "dY", lead + (cols,), _BF16)
+    _like(dX, "dX", lead + (K,), _FLOATS)
+    if Z is not None or act is not None:
+        _like(Z, "Z", lead + (N,), _BF16)
+    if dZ is not None or act is not None:
+        _like(dZ, "dZ", lead + (N,), _BF16)
+    if dbias is not None:
+        _like(dbias, "dbias", (N,), _F32)
+    if workspace is not None:
+        _need(workspace, "workspace", _U8)
+    _run("nf4_mx_linear_grad", (dY, codes, scales, Z, dX, dZ, dbias, workspace),
+         (codes.data_ptr(), scales.data_ptr(), N, K, dY.data_ptr(), _addr(Z), number,
+          lead[0] if lead else 1, _addr(dZ), _addr(dbias), dX.data_ptr(), _DTYPE[dX.dtype],
+          _addr(workspace), 0 if workspace is None else workspace.numel()), stream)
+
+
+def mx_linear(codes, scales, X, bias=None, act=None, residual=None, out_dtype=torch.bfloat16,
+              keep_z=False, stream=None):
+    """act(X . dequant(codes, scales)^T + bias) + residual for any number of rows; with keep_z
+    (that, Z) for mx_linear_grad.  act: None, "relu", "silu", "gelu", "gelu_tanh", or "swiglu"
+    and "geglu", where the matrix's first half of rows gates its second."""
+    _need(codes, "codes", _U8, (2,))
+    _need(X, "X", _BF16, (1, 2))
+    N = codes.shape[0]
+    lead = tuple(X.shape[:-1])
+    Y = _empty(lead + (_act(act, N)[1],), out_dtype, X.device, stream)
+    Z = _empty(lead + (N,), torch.bfloat16, X.device, stream) if keep_z else None
+    nf4_mx_linear(codes, scales, X, Y, bias, act, residual, Z, stream)
+    return (Y, Z) if keep_z else Y
+
+
+def mx_linear_grad(codes, scales, dY, Z=None, act=None, out_dtype=torch.bfloat16, bias_grad=False,
+                   stream=None):
+    """(dX, dZ, dbias) of mx_linear; dbias is None unless bias_grad, dZ is dY itself without an
+    activation.  The residual's gradient is dY."""
+    _need(codes, "codes", _U8, (2,))
+    _need(dY, "dY", _BF16, (1, 2))
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    lead = tuple(dY.shape[:-1])
+    dX = _empty(lead + (K,), out_dtype, dY.device, stream)
+    dZ = None if act is None else _empty(lead + (N,), torch.bfloat16, dY.device, stream)
+    dbias = _empty((N,), torch.float32, dY.device, stream) if bias_grad else None
+    need = _load().nf4_mx_linear_grad_workspace_bytes(N, K, lead[0] if lead else 1)
+    ws = _empty(need, torch.uint8, dY.device, stream) if need > 0 else None
+    nf4_mx_linear_grad(codes, scales, dY, Z, act, dX, dZ, dbias, ws, stream)
+    return dX, dY if act is None else dZ, dbias

@@ -8,8 +8,8 @@
 // fragments of 8 MFMAs (16x16x32): MFMA j has the columns k0 + 8 i + j, i = 0 .. 15.
 // D: lane l holds row l % 16 and columns k0 + 8 (4 (l / 16) + r) + j, so the eight
 // tiles of a lane are 8 consecutive outputs.
-#include "mx_device.h"
-#include "nf4_check.h"
+#include "mx_act.h"
+#include "mx_grad.h"
 
 namespace nf4 {
 namespace mx {
@@ -18,11 +18,17 @@ struct GradArgs {
   const uint8_t *codes;
   const uint8_t *scales;
   const uint16_t *dY;
-  const int32_t *offsets;
+  const int32_t *offsets;  // null: dense
   void *dX;
   int64_t R;
   int E, N, K;
   Grid grid;
+  // partial sums (PART): rows of dY are ld values apart, zero from column N up to the next
+  // multiple of 64; split i of the n's goes to dX + i R K in fp32, added to what is there times
+  // rescale[row] if that is given.
+  int64_t ld;
+  int splits;
+  const float *rescale;
 };
 
 // A workgroup owns 16 MF rows x 128 WV columns; its waves form KG groups of WV that
@@ -63,7 +69,7 @@ __device__ __forceinline__ uint32_t decode2(uint32_t w, float scale, int j) {
   }
 }
 
-template <int MF, int WV, int KG, bool SVEC, typename OUT>
+template <int MF, int WV, int KG, bool SVEC, typename OUT, bool PART>
 __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
   constexpr int BM = 16 * MF, NX = 3;
   constexpr int XB = BM * 128, WB = 64 * 64 * WV;
@@ -74,7 +80,13 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
   __shared__ __attribute__((aligned(256))) uint32_t sc[KG][WV][NX][64];
   int slot, block;
   if (!grid_item(p.grid, &slot, &block)) return;
-  const RowTile t = find_tile(p.offsets, p.E, p.R, slot, BM);
+  int split = 0;
+  if constexpr (PART) {
+    split = block % p.splits;
+    block /= p.splits;
+  }
+  const int64_t ld = PART ? p.ld : p.N;
+  const RowTile t = find_tile(PART ? nullptr : p.offsets, p.E, p.R, slot, BM);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -90,7 +102,8 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
   if (t.e >= 0) {
     const int kb = p.K >> 5, kc = p.K >> 1;
     const int64_t first = (int64_t)t.e * p.N;
-    const int stages = (p.N + 63) >> 6, per = (stages + KG - 1) / KG;
+    const int groups = PART ? KG * p.splits : KG;
+    const int stages = (p.N + 63) >> 6, per = (stages + groups - 1) / groups;
     uint8_t *const xlds = shared[kg];
     uint8_t *const wlds = shared[kg] + NX * XB;
     uint32_t *const slds = sc[kg][wave][0];
@@ -99,7 +112,7 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
       const int idx = (i * WV + wave) * 64 + lane, row = idx >> 3;
-      xo[i] = row * p.N * 2 + ((idx & 7) ^ dy_perm(row)) * 16;
+      xo[i] = row * (int)ld * 2 + ((idx & 7) ^ dy_perm(row)) * 16;
     }
 #pragma unroll
     for (int i = 0; i < WL; ++i) {
@@ -107,15 +120,15 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
       const int n = code_row<WV>(idx / (4 * WV)), ch = idx % (4 * WV);
       wo[i] = n * kc + (k0 >> 1) + (ch ^ code_perm<WV>(n) * 4) * 16;
     }
-    const int xbytes = t.rows * p.N * 2;
-    const uint8_t *xbase = reinterpret_cast<const uint8_t *>(p.dY + (int64_t)t.row0 * p.N);
+    const int xbytes = t.rows * (int)ld * 2;
+    const uint8_t *xbase = reinterpret_cast<const uint8_t *>(p.dY + (int64_t)t.row0 * ld);
     const uint8_t *wbase = p.codes + first * kc;
     // Past N the codes are outside their buffer and dY's chunks are masked; columns
     // past K read another row's codes, their outputs are not stored.
     const auto load_stage = [&](int buf, int s) {
       const int adv = s * 128;
       const u32x4_t rs = buffer_words(xbase + adv, max(xbytes - adv, 0));
-      const int left = (p.N >> 3) - s * 8;
+      const int left = ((PART ? p.N + 7 : p.N) >> 3) - s * 8;
       int o[XL];
 #pragma unroll
       for (int i = 0; i < XL; ++i) {
@@ -184,7 +197,7 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
         more(j);
       }
     };
-    const int s0 = kg * per;
+    const int s0 = (split * KG + kg) * per;
     constexpr int one = XL + WL + (SVEC ? 1 : 0);
     const auto put_scales = [&](int buf, int s) __attribute__((always_inline)) {
       if constexpr (!SVEC) {
@@ -245,6 +258,7 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
           acc[j][r] += part[((g * WV + wave) * 8 * MF + j * MF + r) * 64 + lane];
   }
   OUT *X = reinterpret_cast<OUT *>(p.dX);
+  if constexpr (PART) X += (int64_t)split * p.R * p.K;
 #pragma unroll
   for (int r = 0; r < MF; ++r) {
     const int m = r * 16 + l16;
@@ -257,7 +271,17 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = acc[j][r][i];
-      if constexpr (sizeof(OUT) == 4) {
+      if constexpr (PART) {
+        f32x4_t lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+        f32x4_t *at = reinterpret_cast<f32x4_t *>(row + k);
+        if (p.rescale) {
+          const float f = p.rescale[t.row0 + m];
+          lo += at[0] * f;
+          hi += at[1] * f;
+        }
+        at[0] = lo;
+        at[1] = hi;
+      } else if constexpr (sizeof(OUT) == 4) {
         *reinterpret_cast<f32x4_t *>(row + k) = f32x4_t{v[0], v[1], v[2], v[3]};
         *reinterpret_cast<f32x4_t *>(row + k + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
       } else {
@@ -272,15 +296,17 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
 
 template <int MF, int WV, int KG, bool SVEC>
 static int launch_grad_as(GradArgs &a, int out_dtype, hipStream_t s) {
-  a.grid = make_grid(slots_for(a.R, a.E, true, 16 * MF), (a.K + 128 * WV - 1) / (128 * WV), 8);
+  const int64_t blocks = (a.K + 128 * WV - 1) / (128 * WV);
+  a.grid = make_grid(slots_for(a.R, a.E, a.offsets != nullptr, 16 * MF), blocks * a.splits, 8);
   const int64_t n = grid_size(a.grid);
   if (n * 64 * WV * KG >= (int64_t(1) << 32)) return NF4_ERANGE;
-  if (out_dtype == NF4_F32)
-    hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, float>), dim3((unsigned)n),
-                       dim3(64 * WV * KG), 0, s, a);
+  const dim3 grid((unsigned)n), threads(64 * WV * KG);
+  if (a.ld)
+    hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, float, true>), grid, threads, 0, s, a);
+  else if (out_dtype == NF4_F32)
+    hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, float, false>), grid, threads, 0, s, a);
   else
-    hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, uint16_t>), dim3((unsigned)n),
-                       dim3(64 * WV * KG), 0, s, a);
+    hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, uint16_t, false>), grid, threads, 0, s, a);
   return launch_status(hipGetLastError());
 }
 
@@ -306,7 +332,7 @@ static int launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
 //                           64 of 1 of 4096 x 4096      25.1   two: 28.0
 static int launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
   const auto tiles = [&](int bm, int bk) {
-    return slots_for(a.R, a.E, true, bm) * ((a.K + bk - 1) / bk);
+    return slots_for(a.R, a.E, a.offsets != nullptr, bm) * ((a.K + bk - 1) / bk);
   };
   const int64_t mean = (a.R + a.E - 1) / a.E, rows = mean + mean / 2;
   if (rows > 48) {
@@ -319,6 +345,124 @@ static int launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
   }
   if (tiles(16, 256) >= 384) return launch_grad<1, 2, 2>(a, out_dtype, s);
   return launch_grad<1, 2, 4>(a, out_dtype, s);
+}
+
+// ------------------------------------------------- sums shared out over workgroups ----
+// A dense gradient has few tiles where rows are few, so the n are shared out: parts of the
+// sum in fp32, added in order by whoever takes them.
+struct DensePlan {
+  int mf, wv, kg, splits;
+};
+static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
+  const auto tiles = [&](int bm, int bk) { return (M + bm - 1) / bm * ((K + bk - 1) / bk); };
+  DensePlan d;
+  if (M > 32)
+    d = {4, 4, tiles(64, 512) >= 256 ? 1 : 2, 0};
+  else if (M > 16)
+    d = {2, 4, 2, 0};
+  else
+    d = {1, 2, 4, 0};
+  const int64_t n = tiles(16 * d.mf, 128 * d.wv);
+  // at least four stages of 64 n a group, and no more workgroups than two a CU
+  const int64_t most = (N + 256 * d.kg - 1) / (256 * d.kg), want = 512 / (n < 512 ? n : 512);
+  d.splits = (int)(want < most ? want : most);
+  if (d.splits < 1) d.splits = 1;
+  return d;
+}
+
+int grad_splits(int64_t M, int64_t N, int64_t K) { return plan_dense(M, N, K).splits; }
+
+int launch_grad_parts(const GradParts &g, hipStream_t s) {
+  const DensePlan d = plan_dense(g.M, g.plan_N, g.K);
+  GradArgs a{g.codes, g.scales, g.dY, nullptr, g.parts, g.M, 1, (int)g.N, (int)g.K, {}, g.ld, d.splits, g.rescale};
+  if (d.mf == 4 && d.kg == 1) return launch_grad<4, 4, 1>(a, NF4_F32, s);
+  if (d.mf == 4) return launch_grad<4, 4, 2>(a, NF4_F32, s);
+  if (d.mf == 2) return launch_grad<2, 4, 2>(a, NF4_F32, s);
+  return launch_grad<1, 2, 4>(a, NF4_F32, s);
+}
+
+// out = the parts' sum, in order
+template <typename OUT>
+__global__ void __launch_bounds__(256)
+    mx_parts_kernel(const float *__restrict__ parts, int splits, int64_t size, OUT *__restrict__ out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= size) return;
+  f32x4_t v = *reinterpret_cast<const f32x4_t *>(parts + i);
+  for (int k = 1; k < splits; ++k) v += *reinterpret_cast<const f32x4_t *>(parts + k * size + i);
+  store4<OUT>(out + i, 0, 4, v, true);
+}
+
+// ------------------------------------------------------- in front of the sums ----
+// dZ = dY f'(Z) (gated: dY z_u f'(z_g) and dY f(z_g)) in bf16, and its column sums from the
+// unrounded values.  A thread has four columns (of both halves, gated) and every
+// `blockDim.y`-th row of its workgroup's, so that with `bias` a workgroup has whole columns
+// and the sums are added in one order.
+template <int LANES, bool GATED>
+__global__ void __launch_bounds__(1024)
+    mx_act_grad_kernel(const uint16_t *__restrict__ dY, const uint16_t *__restrict__ Z, int64_t M, int N,
+                       int act, int64_t rows_wg, uint16_t *__restrict__ dZ, float *__restrict__ dbias) {
+  constexpr int W = GATED ? 8 : 4;
+  __shared__ float part[1024 * W];
+  const int cols = GATED ? N >> 1 : N;
+  const int c = threadIdx.x % LANES, y = threadIdx.x / LANES, ny = 1024 / LANES;
+  const int n = (blockIdx.x * LANES + c) * 4;
+  const int64_t m0 = (int64_t)blockIdx.y * rows_wg, m1 = m0 + rows_wg < M ? m0 + rows_wg : M;
+  float sum[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) sum[i] = 0.f;
+  if (n < cols) {
+    const auto get = [](const uint16_t *p) __attribute__((always_inline)) {
+      const u32x2_t w = *reinterpret_cast<const u32x2_t *>(p);
+      return f32x4_t{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+    };
+#pragma unroll 2
+    for (int64_t m = m0 + y; m < m1; m += ny) {
+      const f32x4_t d = get(dY + m * cols + n);
+      f32x4_t z = {0.f, 0.f, 0.f, 0.f}, u = z;
+      if (Z) z = get(Z + m * N + n);
+      if constexpr (GATED) u = get(Z + m * N + cols + n);
+      f32x4_t g = act_slopes(act, z) * d;
+      if constexpr (GATED) {
+        g *= u;
+        u = act_values(act, z) * d;
+      }
+      if (dZ) {
+        store4<uint16_t>(dZ + m * N, n, cols, g, true);
+        if constexpr (GATED) store4<uint16_t>(dZ + m * N, cols + n, N, u, true);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum[i] += g[i];
+        if constexpr (GATED) sum[4 + i] += u[i];
+      }
+    }
+  }
+  if (!dbias) return;
+#pragma unroll
+  for (int i = 0; i < W; ++i) part[(y * LANES + c) * W + i] = sum[i];
+  __syncthreads();
+  for (int k = threadIdx.x; k < LANES * W; k += 1024) {
+    float v = 0.f;
+    for (int r = 0; r < ny; ++r) v += part[r * LANES * W + k];
+    const int at = (blockIdx.x * LANES + k / W) * 4 + k % 4;
+    if (at < cols) dbias[k % W >= 4 ? cols + at : at] = v;
+  }
+}
+
+static int launch_act_grad(const uint16_t *dY, const uint16_t *Z, int64_t M, int64_t N, int act, uint16_t *dZ,
+                           float *dbias, hipStream_t s) {
+  const bool gated = is_gated(act);
+  const int64_t cols = gated ? N / 2 : N;
+  // without a bias the rows are shared out as well
+  const int64_t rows = dbias ? M : 64;
+  const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)((M + rows - 1) / rows));
+  if (gated)
+    hipLaunchKernelGGL((mx_act_grad_kernel<16, true>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ,
+                       dbias);
+  else
+    hipLaunchKernelGGL((mx_act_grad_kernel<16, false>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ,
+                       dbias);
+  return launch_status(hipGetLastError());
 }
 
 }  // namespace mx
@@ -340,8 +484,56 @@ int nf4_mx_gemm_grouped_grad(const uint8_t *codes, const uint8_t *scales, int64_
     return NF4_EALIGN;
   if (int r = nf4::device_status()) return r;
   if (R == 0) return NF4_OK;
-  nf4::mx::GradArgs a{codes, scales, dY, offsets, dX, R, (int)E, (int)N, (int)K, {}};
+  nf4::mx::GradArgs a{codes, scales, dY, offsets, dX, R, (int)E, (int)N, (int)K, {}, 0, 1, nullptr};
   return nf4::mx::launch_rows_grad(a, out_dtype, (hipStream_t)stream);
+}
+
+int64_t nf4_mx_linear_grad_workspace_bytes(int64_t N, int64_t K, int64_t M) {
+  if (nf4::check_mx_shape(N, K) || N % 8 != 0 || N > (int64_t(1) << 23) || M < 1 || M > (int64_t(1) << 21))
+    return -1;
+  const int64_t n = nf4::mx::grad_splits(M, N, K);
+  return n > 1 ? n * M * K * 4 : 0;
+}
+
+int nf4_mx_linear_grad(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, const uint16_t *dY,
+                       const uint16_t *Z, int act, int64_t M, uint16_t *dZ, float *dbias, void *dX,
+                       int out_dtype, void *workspace, int64_t workspace_bytes, void *stream) {
+  using namespace nf4::mx;
+  const bool plain = act == NF4_ACT_NONE;
+  if (!codes || !scales || !dY || !dX || !nf4::known_dtype(out_dtype) || !known_act(act) ||
+      (!plain && (!Z || !dZ)))
+    return NF4_EINVAL;
+  if (int r = nf4::check_mx_shape(N, K)) return r;
+  if (N % 8 != 0) return NF4_EINVAL;
+  // so that every launch below holds its tiles
+  if (M < 1 || M > (int64_t(1) << 21) || N > (int64_t(1) << 23)) return NF4_ERANGE;
+  if (!nf4::aligned_to(codes, 16) || !nf4::aligned_to(dY, 16) || !nf4::aligned_to(Z, 16) ||
+      !nf4::aligned_to(dZ, 16) || !nf4::aligned_to(dX, 16) || !nf4::aligned_to(dbias, 4) ||
+      !nf4::aligned_to(workspace, 256))
+    return NF4_EALIGN;
+  const int64_t need = nf4_mx_linear_grad_workspace_bytes(N, K, M);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return NF4_ERANGE;
+  if (int r = nf4::device_status()) return r;
+  hipStream_t s = (hipStream_t)stream;
+  if (!plain || dZ || dbias)
+    if (int r = launch_act_grad(dY, plain ? nullptr : Z, M, N, act, dZ, dbias, s)) return r;
+  const uint16_t *d = plain ? dY : dZ;
+  if (need == 0) {
+    GradArgs a{codes, scales, d, nullptr, dX, M, 1, (int)N, (int)K, {}, 0, 1, nullptr};
+    return launch_rows_grad(a, out_dtype, s);
+  }
+  float *parts = static_cast<float *>(workspace);
+  if (int r = launch_grad_parts({codes, scales, N, K, N, d, N, M, parts, nullptr}, s)) return r;
+  const int splits = grad_splits(M, N, K);
+  const int64_t size = M * K;
+  const unsigned blocks = (unsigned)((size / 4 + 255) / 256);
+  if (out_dtype == NF4_F32)
+    hipLaunchKernelGGL((mx_parts_kernel<float>), dim3(blocks), dim3(256), 0, s, parts, splits, size,
+                       static_cast<float *>(dX));
+  else
+    hipLaunchKernelGGL((mx_parts_kernel<uint16_t>), dim3(blocks), dim3(256), 0, s, parts, splits, size,
+                       static_cast<uint16_t *>(dX));
+  return nf4::launch_status(hipGetLastError());
 }
 
 }  // extern "C"

@@ -423,6 +423,59 @@ int nf4_mx_gemm_grouped_grad(const uint8_t *codes, const uint8_t *scales, int64_
                              int64_t K, const uint16_t *dY, const int32_t *offsets, int64_t R,
                              void *dX, int out_dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Fused forms of the MXFP4 products.  act arguments: an nf4_act; f(z) is
+ *   relu max(z, 0), silu z / (1 + exp(-z)), gelu z P(z) with P the normal distribution
+ *   function, gelu_tanh z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2.
+ * The gated ones take the matrix's rows 0 .. N/2 - 1 as the gate of rows N/2 .. N - 1:
+ * swiglu silu(z_i) z_(N/2 + i), geglu gelu_tanh(z_i) z_(N/2 + i).
+ */
+enum nf4_act {
+  NF4_ACT_NONE = 0,
+  NF4_ACT_RELU = 1,
+  NF4_ACT_SILU = 2,
+  NF4_ACT_GELU = 3,
+  NF4_ACT_GELU_TANH = 4,
+  NF4_ACT_SWIGLU = 5,
+  NF4_ACT_GEGLU = 6
+};
+
+/*
+ * nf4_mx_linear -- z[m][n] = sum_k X[m][k] v(n,k) + bias[n], Y = f(z) + residual, X bf16
+ * [M][K], any M >= 1.  Y [M][N] ([M][N/2] gated, N even) fp32 or bf16, rounded once.
+ *  - bias fp32 or bf16 [N], residual of Y's shape and type, Z bf16 [M][N]: each may be
+ *    NULL.  Z receives z, rounded once, which nf4_mx_linear_grad takes.  residual may be Y
+ *    itself (each element is read before it is written, by the same thread).
+ * z is within the products' bound (plus 2^-23 |z| for the bias); f is within 2^-20 of its
+ * value, the normal numbers' range given.
+ * Alignment: codes, X, Y, residual and Z 16 bytes, bias that of its type.  Errors as
+ * nf4_mx_gemm; NF4_EINVAL for an unknown act or dtype and for a gated act with odd N.
+ */
+int nf4_mx_linear(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, const uint16_t *X,
+                  int64_t M, const void *bias, int bias_dtype, int act, const void *residual, void *Y,
+                  int out_dtype, uint16_t *Z, void *stream);
+
+/*
+ * nf4_mx_linear_grad -- the gradient of nf4_mx_linear (the packed matrix is frozen), from
+ * dY bf16 [M][N] ([M][N/2] gated) and the z it kept:
+ *   dZ = dY f'(Z) (gated: dY z_u f'(z_g) | dY f(z_g)), bf16 [M][N], rounded once;
+ *   dbias[n] = sum_m dZ[m][n] before that rounding, fp32 [N], NULL if not wanted;
+ *   dX[m][k] = sum_n dZ[m][n] v(n,k), fp32 or bf16 [M][K], from the rounded dZ.
+ * The residual's gradient is dY.  Without activation (act NF4_ACT_NONE) Z is not read and
+ * dZ, a copy of dY, may be NULL.
+ * relu'(0) = 0.  N is a multiple of 8 (NF4_EINVAL) and at most 2^23, M at most 2^21.
+ *  - workspace: device memory, 256-byte aligned, of at least
+ *    nf4_mx_linear_grad_workspace_bytes(N, K, M) bytes (0: may be NULL), with anything in
+ *    it; the sums over n of calls of few rows are shared out over workgroups and meet there.
+ *    Calls that share one must not run at the same time.
+ * Alignment: codes, dY, Z, dZ and dX 16 bytes.  Errors: NF4_ERANGE for a missing or short
+ * workspace, otherwise as nf4_mx_linear.
+ */
+int64_t nf4_mx_linear_grad_workspace_bytes(int64_t N, int64_t K, int64_t M);
+int nf4_mx_linear_grad(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, const uint16_t *dY,
+                       const uint16_t *Z, int act, int64_t M, uint16_t *dZ, float *dbias, void *dX,
+                       int out_dtype, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* The 16 NF4 levels L[0..15] (fp32) this library decodes with.  Host only. */
 void nf4_codebook(float out[16]);
 

@@ -1,0 +1,291 @@
+"""Fused forms of the MXFP4 products on the GPU against 64-bit definitions: the product
+with bias, activation and residual and its gradient, the head's cross entropy, and the
+expert layer for a few tokens.
+
+Tolerances.  Sums of T products are off by at most (T + 8) 2^-24 of the sum of their
+magnitudes; an activation by 2^-20 |z|, its slope by 2^-20, and |f'| <= 1.13; rounding to
+bf16 by 2^-8 of the value, to fp32 by 2^-24."""
+import math
+
+import pytest
+import torch
+
+import dequant_gemv_nf4_amd as nf4
+from gpu_guard import alloc, check
+from mx_reference import values
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+GATED = ("swiglu", "geglu")
+ACTS = (None, "relu", "silu", "gelu", "gelu_tanh", "swiglu", "geglu")
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def matrix(n, k, seed, sigma=0.05, lead=()):
+    """Random packed bytes: every code, scales around sigma."""
+    g = gen(seed)
+    codes = torch.randint(0, 256, (*lead, n, k // 2), dtype=torch.uint8, device=DEV, generator=g)
+    mid = 127 + round(math.log2(sigma))
+    scales = torch.randint(mid - 2, mid + 2, (*lead, n, k // 32), device=DEV, generator=g)
+    return codes, scales.to(torch.uint8)
+
+
+def rand(shape, seed, dtype=BF, scale=1.0):
+    return (scale * torch.randn(shape, device=DEV, generator=gen(seed))).to(dtype)
+
+
+def f64(act, z):
+    """(f(z), f'(z)) in float64."""
+    if act is None:
+        return z, torch.ones_like(z)
+    if act == "relu":
+        return z.clamp(min=0), (z > 0).double()
+    if act in ("silu", "swiglu"):
+        s = torch.sigmoid(z)
+        return z * s, s + z * s * (1 - s)
+    if act == "gelu":
+        c = 0.5 * torch.erfc(-z * math.sqrt(0.5))
+        return z * c, c + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    a = 2 * math.sqrt(2 / math.pi)
+    s = torch.sigmoid(a * (z + 0.044715 * z ** 3))
+    return z * s, s + z * s * (1 - s) * a * (1 + 3 * 0.044715 * z * z)
+
+
+def inside(got, want, tol, what):
+    err = (got.double() - want).abs()
+    bad = ~(err <= tol)
+    assert not bool(bad.any()), (f"{what}: {int(bad.sum())} of {bad.numel()} outside, worst "
+                                 f"{float((err / tol).nan_to_num(nan=1e9).max()):.3g} x tolerance")
+
+
+def linear_reference(codes, scales, x, bias, act, residual, dtype):
+    """(y, tolerance, z, tolerance of z)."""
+    v = values(codes, scales)
+    k = v.shape[1]
+    z = x.double() @ v.t().contiguous()
+    dz = (k + 8) * 2.0 ** -24 * (x.double().abs() @ v.abs().t().contiguous()) + 1e-30
+    if bias is not None:
+        z = z + bias.double()
+        dz = dz + 2.0 ** -23 * (z.abs() + bias.double().abs())
+    if act in GATED:
+        a, b = z.chunk(2, dim=-1)
+        da, db = dz.chunk(2, dim=-1)
+        f = f64(act, a)[0]
+        df = 1.13 * da + 2.0 ** -20 * (a.abs() + da)
+        y, tol = f * b, df * (b.abs() + db) + f.abs() * db + 2.0 ** -23 * (f * b).abs()
+    else:
+        y = f64(act, z)[0]
+        tol = 1.13 * dz + (0 if act in (None, "relu") else 2.0 ** -20) * (z.abs() + dz)
+    if residual is not None:
+        y = y + residual.double()
+        tol = tol + 2.0 ** -23 * (y.abs() + residual.double().abs())
+    half = HALF[dtype]
+    return y, tol * (1 + half) + half * y.abs() + 1e-30, z, dz * (1 + HALF[BF]) + HALF[BF] * z.abs()
+
+
+def run_linear(m, n, k, act, bias=None, residual=False, dtype=BF, keep=False, seed=0, vector=False):
+    codes, scales = matrix(n, k, seed + 1)
+    cols = n // 2 if act in GATED else n
+    x = rand((k,) if vector else (m, k), seed + 2)
+    b = None if bias is None else rand((n,), seed + 3, bias)
+    lead = () if vector else (m,)
+    r = rand((*lead, cols), seed + 4, dtype) if residual else None
+    ybuf, y = alloc((*lead, cols), dtype, DEV)
+    zbuf, z = alloc((*lead, n), BF, DEV) if keep else (None, None)
+    nf4.nf4_mx_linear(codes, scales, x, y, b, act, r, z)
+    want, tol, zw, ztol = linear_reference(codes, scales, x, b, act, r, dtype)
+    inside(y, want, tol, f"Y {m}x{n}x{k} {act}")
+    check(ybuf, "Y")
+    if keep:
+        inside(z, zw, ztol, "Z")
+        check(zbuf, "Z")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m", [1, 2, 3, 17, 40, 70])
+def test_linear_acts(m, act):
+    run_linear(m, 272, 160, act, bias=F32, residual=True, keep=True, seed=m)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bias", [None, BF, F32])
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+def test_linear_operands(act, bias, dtype):
+    for residual in (False, True):
+        run_linear(5, 96, 64, act, bias, residual, dtype, keep=residual, seed=7)
+
+
+# columns that are no multiple of a vector, of a tile, of anything
+@pytest.mark.parametrize("n", [1, 2, 3, 17, 30, 66, 129, 250])
+@pytest.mark.parametrize("m", [1, 4, 9, 33])
+def test_linear_odd_columns(m, n):
+    run_linear(m, n, 96, "silu", bias=F32, residual=True, keep=True, seed=n)
+    if n % 2 == 0:
+        run_linear(m, n, 96, "swiglu", bias=BF, residual=True, dtype=F32, keep=True, seed=n)
+
+
+# each kernel: one, two, four rows; tiles of 16 x 32 up to 128 x 256; scales at odd strides
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (2, 4096, 2080), (4, 2048, 4096), (8, 4096, 4096),
+                                   (16, 10240, 512), (16, 28672, 256), (33, 24576, 256),
+                                   (100, 6144, 512), (40, 26624, 288), (300, 13824, 256),
+                                   (300, 13824, 96), (520, 14336, 256), (520, 14336, 160)])
+@pytest.mark.parametrize("act", ["swiglu", "gelu_tanh"])
+def test_linear_kernels(m, n, k, act):
+    run_linear(m, n, k, act, bias=F32, residual=True, keep=m % 2 == 0, seed=k + m)
+
+
+def test_linear_vector_and_in_place():
+    run_linear(1, 64, 64, "relu", residual=True, vector=True)
+    codes, scales = matrix(96, 64, 1)
+    x, r = rand((6, 64), 2), rand((6, 96), 3)
+    want = nf4.mx_linear(codes, scales, x, act="silu", residual=r)
+    nf4.nf4_mx_linear(codes, scales, x, r, act="silu", residual=r)
+    assert torch.equal(r, want)
+
+
+def test_linear_is_the_product():
+    """Without bias, activation and residual the sums are nf4_mx_gemm's, bit for bit."""
+    for m in (1, 3, 20, 300):
+        codes, scales = matrix(1024, 512, m)
+        x = rand((m, 512), m)
+        for dtype in (BF, F32):
+            assert torch.equal(nf4.mx_linear(codes, scales, x, out_dtype=dtype),
+                               nf4.mx_gemm(codes, scales, x, out_dtype=dtype))
+
+
+def test_linear_large_values():
+    """Activations where exp overflows and where nothing is left of the small side."""
+    codes = torch.full((32, 16), 0x22, dtype=torch.uint8, device=DEV)  # every value 1
+    scales = torch.full((32, 1), 127, dtype=torch.uint8, device=DEV)
+    x = torch.zeros((6, 32), dtype=BF, device=DEV)
+    x[:, 0] = torch.tensor([-1e30, -200.0, -20.0, 20.0, 200.0, 1e30], device=DEV).to(BF)
+    for act in ACTS[1:5]:
+        y = nf4.mx_linear(codes, scales, x, act=act, out_dtype=F32)
+        want = f64(act, x[:, :1].double()).__getitem__(0).expand(6, 32)
+        inside(y, want, 2.0 ** -20 * x[:, :1].double().abs(), act)
+    x[:, 0] = torch.tensor([float("inf"), float("nan"), 1, 2, 3, 4], device=DEV).to(BF)
+    for act in ACTS[1:5]:
+        y = nf4.mx_linear(codes, scales, x, act=act, out_dtype=F32)
+        assert torch.isinf(y[0]).all() and torch.isnan(y[1]).all() and torch.isfinite(y[2:]).all()
+
+
+def grad_reference(codes, scales, dy, z, act):
+    """(dz, tolerance, db, tolerance)."""
+    z, dy = z.double(), dy.double()
+    if act in GATED:
+        a, b = z.chunk(2, dim=-1)
+        f, df = f64(act, a)
+        dz = torch.cat([dy * b * df, dy * f], dim=-1)
+        off = torch.cat([2.0 ** -20 * (dy * b).abs(), 2.0 ** -20 * (dy * a).abs()], dim=-1)
+    else:
+        dz = dy * f64(act, z)[1]
+        off = 2.0 ** -20 * dy.abs()
+    off = off + 2.0 ** -22 * dz.abs()
+    m = dz.reshape(-1, dz.shape[-1]).shape[0]
+    db = dz.reshape(m, -1).sum(0)
+    dbtol = off.reshape(m, -1).sum(0) + (m + 8) * 2.0 ** -24 * dz.abs().reshape(m, -1).sum(0)
+    return dz, off + HALF[BF] * dz.abs() + 1e-30, db, dbtol + 1e-30
+
+
+def run_grad(m, n, k, act, bias, dtype=BF, seed=0):
+    codes, scales = matrix(n, k, seed + 1)
+    cols = n // 2 if act in GATED else n
+    z, dy = rand((m, n), seed + 2, scale=2.0), rand((m, cols), seed + 3)
+    dxbuf, dx = alloc((m, k), dtype, DEV)
+    dzbuf, dz = alloc((m, n), BF, DEV)
+    dbbuf, db = alloc((n,), F32, DEV) if bias else (None, None)
+    need = nf4.mx_linear_grad_workspace_bytes(n, k, m)
+    wsbuf, ws = alloc((need,), torch.uint8, DEV) if need else (None, None)
+    nf4.nf4_mx_linear_grad(codes, scales, dy, z, act, dx, dz, db, ws)
+    want, tol, dbw, dbtol = grad_reference(codes, scales, dy, z, act)
+    inside(dz, want, tol, f"dZ {m}x{n}x{k} {act}")
+    if bias:
+        inside(db, dbw, dbtol, "dbias")
+        check(dbbuf, "dbias")
+    v = values(codes, scales)
+    mag = (n + 40) * 2.0 ** -24 * (dz.double().abs() @ v.abs())   # 40: the parts' sums
+    want = dz.double() @ v
+    inside(dx, want, mag * (1 + HALF[dtype]) + HALF[dtype] * want.abs() + 1e-30, "dX")
+    for buf in (dxbuf, dzbuf) + ((wsbuf,) if need else ()):
+        check(buf, "gradient")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m", [1, 5, 17, 40, 130])
+def test_grad_acts(m, act):
+    run_grad(m, 272, 160, act, True, seed=m)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 8, 32), (2, 16, 64), (1, 4096, 4096), (20, 8192, 96), (77, 13824, 640),
+                                   (64, 1000, 4096), (700, 504, 1056), (2100, 64, 4096), (50, 1032, 32),
+                                   (33, 4104, 8192)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_grad_shapes(m, n, k, dtype):
+    run_grad(m, n, k, "swiglu" if n % 16 == 0 else "silu", m % 2 == 0, dtype, seed=n)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_grad_by_differences(act):
+    """The gradient agrees with central differences of the 64-bit forward."""
+    m, n, k = 3, 32, 64
+    codes, scales = matrix(n, k, 5)
+    x, b = rand((m, k), 6), rand((n,), 7, F32)
+    y, z = nf4.mx_linear(codes, scales, x, bias=b, act=act, out_dtype=F32, keep_z=True)
+    dy = rand(y.shape, 8)
+    dx, _, db = nf4.mx_linear_grad(codes, scales, dy, z, act, out_dtype=F32, bias_grad=True)
+
+    def total(x, b):
+        v = values(codes, scales)
+        z = x @ v.t().contiguous() + b
+        if act in GATED:
+            p, q = z.chunk(2, dim=-1)
+            return float((f64(act, p)[0] * q * dy.double()).sum())
+        return float((f64(act, z)[0] * dy.double()).sum())
+
+    h = 1e-5
+    x64, b64 = x.double(), b.double()
+    # z and dZ are rounded to bf16 in between: 2^-7 of the gradient's terms, whose size the
+    # rows' norms bound
+    v = values(codes, scales)
+    size = float(dy.double().abs().sum(1).max() * (z.double().abs().max() + 1.13) * 1.6)
+    for i, j in ((0, 0), (1, 17), (2, 63)):
+        if act == "relu" and float((x64[i] @ v.t()).add(b64).abs().min()) < 1e-3:
+            continue
+        e = torch.zeros_like(x64)
+        e[i, j] = h
+        want = (total(x64 + e, b64) - total(x64 - e, b64)) / (2 * h)
+        assert abs(float(dx[i, j]) - want) <= 2.0 ** -7 * size * float(v[:, j].abs().max()), (act, i, j)
+    for j in (0, 15, 31):
+        e = torch.zeros_like(b64)
+        e[j] = h
+        want = (total(x64, b64 + e) - total(x64, b64 - e)) / (2 * h)
+        assert abs(float(db[j]) - want) <= 2.0 ** -7 * size * m, (act, j)
+
+
+def test_grad_without_activation():
+    codes, scales = matrix(64, 96, 1)
+    dy = rand((9, 64), 2)
+    dx, dz, db = nf4.mx_linear_grad(codes, scales, dy, out_dtype=F32, bias_grad=True)
+    assert dz is dy
+    off = torch.tensor([0, 9], dtype=torch.int32, device=DEV)
+    same = nf4.mx_gemm_grouped_grad(codes[None], scales[None], dy, off)
+    tol = 72 * 2.0 ** -23 * (dy.double().abs() @ values(codes, scales).abs())
+    inside(dx, same.double(), tol, "dX")
+    inside(db, dy.double().sum(0), 17 * 2.0 ** -24 * dy.double().abs().sum(0), "dbias")
+
+
+def test_slopes_at_large_values():
+    codes, scales = matrix(32, 32, 1)
+    z = torch.tensor([-3e38, -1e20, -88.0, -30.0, -6.0, 0.0, 5.0, 8.0, 30.0, 88.0, 1e20, 3e38],
+                     device=DEV).to(BF)
+    z = z.repeat(3)[:32].reshape(1, 32).contiguous()
+    dy = torch.ones_like(z)
+    for act in ACTS[1:5]:
+        dz = nf4.mx_linear_grad(codes, scales, dy, z, act)[1]
+        want = f64(act, z.double().clamp(-1e4, 1e4))[1]
+        inside(dz, want, 2.0 ** -20 + HALF[BF] * want.abs(), act)
