@@ -18,6 +18,7 @@ EMBED_BAD_ID = 1
 MX_BLOCK = 32
 MOE_MAX_E = 512
 MOE_BAD_ID = 1
+LOSS_BAD_TARGET = 1
 
 _STATUS = {0: "NF4_OK", -1: "NF4_EINVAL", -2: "NF4_EALIGN", -3: "NF4_ERANGE",
            -4: "NF4_EDEVICE", -5: "NF4_ELAUNCH"}
@@ -80,7 +81,10 @@ def _load():
     L.nf4_mx_linear_grad.argtypes = [vp, vp, i64, i64, vp, vp, ci, i64, vp, vp, vp, ci, vp, i64, vp]
     L.nf4_mx_linear_grad_workspace_bytes.argtypes = [i64, i64, i64]
     L.nf4_mx_linear_grad_workspace_bytes.restype = i64
-    for f in (L.nf4_mx_linear, L.nf4_mx_linear_grad):
+    L.nf4_mx_cross_entropy.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, ci, vp, i64, vp, vp]
+    L.nf4_mx_cross_entropy_workspace_bytes.argtypes = [i64, i64, i64, ci]
+    L.nf4_mx_cross_entropy_workspace_bytes.restype = i64
+    for f in (L.nf4_mx_linear, L.nf4_mx_linear_grad, L.nf4_mx_cross_entropy):
         f.restype = ci
     for f in (L.nf4_mx_pack, L.nf4_mx_unpack, L.nf4_mx_gemm, L.nf4_mx_gemm_packed,
               L.nf4_mx_gemm_grouped, L.nf4_mx_gemm_grouped_grad, L.nf4_moe_sort,
@@ -891,3 +895,61 @@ def mx_linear_grad(codes, scales, dY, Z=None, act=None, out_dtype=torch.bfloat16
     ws = _empty(need, torch.uint8, dY.device, stream) if need > 0 else None
     nf4_mx_linear_grad(codes, scales, dY, Z, act, dX, dZ, dbias, ws, stream)
     return dX, dY if act is None else dZ, dbias
+
+
+def mx_cross_entropy_workspace_bytes(N, K, M, grad=False):
+    """Bytes of workspace nf4_mx_cross_entropy needs for (N, K, M), with or without gradient."""
+    n = _load().nf4_mx_cross_entropy_workspace_bytes(int(N), int(K), int(M), int(grad))
+    if n < 0:
+        raise ValueError(f"invalid shape N={N} K={K} M={M}")
+    return int(n)
+
+
+def nf4_mx_cross_entropy(codes, scales, X, targets, loss, lse, dloss=None, dX=None, workspace=None,
+                         dev_status=None, stream=None):
+    """loss and lse fp32 [M] of the logits X . dequant(codes, scales)^T (X bf16 [M][K]) at
+    targets int64 [M], negative ones ignored; with dloss fp32 [M] the gradient dX [M][K]
+    (fp32 or bf16).  workspace: uint8, mx_cross_entropy_workspace_bytes(N, K, M, dX is given)."""
+    N, K = _mx_matrix(codes, scales)
+    _need(X, "X", _BF16, (2,))
+    M = X.shape[0]
+    if X.shape[1] != K:
+        raise ValueError(f"X has {X.shape[1]} columns, the matrix K = {K}")
+    _like(targets, "targets", (M,), (torch.int64,))
+    _like(loss, "loss", (M,), _F32)
+    _like(lse, "lse", (M,), _F32)
+    if (dX is None) != (dloss is None):
+        raise ValueError("dX and dloss are given together")
+    if dX is not None:
+        _like(dX, "dX", (M, K), _FLOATS)
+        _like(dloss, "dloss", (M,), _F32)
+    if workspace is not None:
+        _need(workspace, "workspace", _U8)
+    if dev_status is not None:
+        _need(dev_status, "dev_status", _I32)
+    _run("nf4_mx_cross_entropy", (X, codes, scales, targets, loss, lse, dloss, dX, workspace, dev_status),
+         (codes.data_ptr(), scales.data_ptr(), N, K, X.data_ptr(), targets.data_ptr(), M,
+          loss.data_ptr(), lse.data_ptr(), _addr(dloss), _addr(dX), 0 if dX is None else _DTYPE[dX.dtype],
+          _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(dev_status)), stream)
+
+
+def mx_cross_entropy(codes, scales, X, targets, dloss=None, out_dtype=torch.bfloat16, stream=None,
+                     check=False):
+    """(loss, lse) of each row, or with the losses' gradients dloss (loss, lse, dX).  A target
+    below 0 is ignored, and so is one of N or more; with check=True the latter raises (a host
+    synchronisation, so not under capture)."""
+    N, K = _mx_matrix(codes, scales)
+    _need(X, "X", _BF16, (2,))
+    M, dev = X.shape[0], X.device
+    need = _load().nf4_mx_cross_entropy_workspace_bytes(N, K, M, int(dloss is not None))
+    loss = _empty((M,), torch.float32, dev, stream)
+    lse = _empty((M,), torch.float32, dev, stream)
+    dX = None if dloss is None else _empty((M, K), out_dtype, dev, stream)
+    ws = _empty(max(need, 0), torch.uint8, dev, stream)
+    status = _empty(1, torch.int32, dev, stream) if check else None
+    nf4_mx_cross_entropy(codes, scales, X, targets, loss, lse, dloss, dX, ws, status, stream)
+    if check:
+        st = _read(status, stream)
+        if st:
+            raise ValueError(f"nf4_mx_cross_entropy flagged targets: status bits {st:#x}")
+    return (loss, lse) if dX is None else (loss, lse, dX)

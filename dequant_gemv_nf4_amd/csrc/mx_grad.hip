@@ -373,7 +373,7 @@ static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
 int grad_splits(int64_t M, int64_t N, int64_t K) { return plan_dense(M, N, K).splits; }
 
 int launch_grad_parts(const GradParts &g, hipStream_t s) {
-  const DensePlan d = plan_dense(g.M, g.plan_N, g.K);
+  const DensePlan d = plan_dense(g.plan_M, g.plan_N, g.K);
   GradArgs a{g.codes, g.scales, g.dY, nullptr, g.parts, g.M, 1, (int)g.N, (int)g.K, {}, g.ld, d.splits, g.rescale};
   if (d.mf == 4 && d.kg == 1) return launch_grad<4, 4, 1>(a, NF4_F32, s);
   if (d.mf == 4) return launch_grad<4, 4, 2>(a, NF4_F32, s);
@@ -523,7 +523,7 @@ int nf4_mx_linear_grad(const uint8_t *codes, const uint8_t *scales, int64_t N, i
     return launch_rows_grad(a, out_dtype, s);
   }
   float *parts = static_cast<float *>(workspace);
-  if (int r = launch_grad_parts({codes, scales, N, K, N, d, N, M, parts, nullptr}, s)) return r;
+  if (int r = launch_grad_parts({codes, scales, N, K, M, N, d, N, M, parts, nullptr}, s)) return r;
   const int splits = grad_splits(M, N, K);
   const int64_t size = M * K;
   const unsigned blocks = (unsigned)((size / 4 + 255) / 256);

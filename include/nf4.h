@@ -476,6 +476,38 @@ int nf4_mx_linear_grad(const uint8_t *codes, const uint8_t *scales, int64_t N, i
                        const uint16_t *Z, int act, int64_t M, uint16_t *dZ, float *dbias, void *dX,
                        int out_dtype, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* bit OR-ed into *dev_status by nf4_mx_cross_entropy */
+#define NF4_LOSS_BAD_TARGET 1 /* a target of N or more: its row is ignored */
+
+/*
+ * nf4_mx_cross_entropy -- softmax cross entropy of the logits l[m][n] = sum_k X[m][k]
+ * v(n,k), which are never kept: (codes, scales) [N][K] is the head, N the vocabulary, X
+ * bf16 [M][K], targets int64 [M].
+ *   lse[m] = log sum_n exp l[m][n];  loss[m] = lse[m] - l[m][targets[m]]     (fp32)
+ *   dX[m][k] = dloss[m] * (sum_n exp(l[m][n] - lse[m]) v(n,k) - v(targets[m],k))
+ * dX [M][K] fp32 or bf16 is the gradient for the losses' gradients dloss, fp32 [M] (the head
+ * is frozen); both are given or both NULL.  A row whose target is negative is ignored: loss 0,
+ * a zero row of dX, its lse as for the others.  So is one whose target is N or more, which is
+ * flagged in *dev_status (device int32, may be NULL; if given, the call first clears it).
+ * A row with a NaN or infinite logit has a lse that is not finite, and (if not ignored) a loss
+ * and a row of dX that are not.
+ *  - workspace: device memory, 256-byte aligned, of at least
+ *    nf4_mx_cross_entropy_workspace_bytes(N, K, M, dX != NULL) bytes, with anything in it:
+ *    up to 2^28 bytes, and with dX 4 K bytes a row of up to 4096 rows (more for few rows,
+ *    whose sums are shared out over workgroups).  Calls that share one must not run at the
+ *    same time.  The function returns -1 for sizes that the call refuses.
+ * The sums over k are the products'; exp is within 2^-20 of its value (|l| at most 64, in
+ * proportion beyond), sums of it are fp32, and the gradient takes exp(l - lse) in bf16, each
+ * rounded once.
+ * Alignment: codes, X and dX 16 bytes, targets 8.  Errors: NF4_ERANGE for M < 1, M >= 2^26,
+ * N > 2^23 or a missing or short workspace, otherwise as nf4_mx_gemm.
+ */
+int64_t nf4_mx_cross_entropy_workspace_bytes(int64_t N, int64_t K, int64_t M, int grad);
+int nf4_mx_cross_entropy(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, const uint16_t *X,
+                         const int64_t *targets, int64_t M, float *loss, float *lse, const float *dloss, void *dX,
+                         int out_dtype, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
+                         void *stream);
+
 /* The 16 NF4 levels L[0..15] (fp32) this library decodes with.  Host only. */
 void nf4_codebook(float out[16]);
 

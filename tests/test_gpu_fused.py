@@ -289,3 +289,167 @@ def test_slopes_at_large_values():
         dz = nf4.mx_linear_grad(codes, scales, dy, z, act)[1]
         want = f64(act, z.double().clamp(-1e4, 1e4))[1]
         inside(dz, want, 2.0 ** -20 + HALF[BF] * want.abs(), act)
+
+
+# ------------------------------------------------------------ cross entropy ----
+def loss_reference(codes, scales, x, targets, dloss):
+    """(loss, tolerance, lse, tolerance, dX, tolerance) in float64."""
+    v = values(codes, scales)
+    n, k = v.shape
+    l = x.double() @ v.t().contiguous()
+    dl = ((k + 8) * 2.0 ** -24 * (x.double().abs() @ v.abs().t().contiguous())).amax(1)
+    lse = torch.logsumexp(l, dim=1)
+    top = l.abs().amax(1)
+    # exp 2^-20 a 64 of |l|; sums of it in fp32: 16 terms a lane, then strips a thread, threads,
+    # pieces, each in turn or as a tree, fewer than 128 steps
+    e = 2.0 ** -20 * (1 + top / 64) + 2.0 ** -17
+    lsetol = dl + e + 2.0 ** -22 * lse.abs()
+    kept = (targets >= 0) & (targets < n)
+    at = torch.where(kept, targets, 0).unsqueeze(1)
+    lt = l.gather(1, at).squeeze(1)
+    loss = torch.where(kept, lse - lt, 0.0)
+    losstol = torch.where(kept, lsetol + dl + 2.0 ** -23 * (lse.abs() + lt.abs()), 0.0)
+    if dloss is None:
+        return loss, losstol, lse, lsetol
+    p = torch.exp(l - lse.unsqueeze(1))
+    g = torch.where(kept, dloss.double(), 0.0).unsqueeze(1)
+    mag = p @ v.abs()
+    off = mag * (2.0 ** -8 + 2 * (dl + e).unsqueeze(1) + (n + 40) * 2.0 ** -24)
+    row = v[at.squeeze(1)]
+    dx = (p @ v - row) * g
+    off = (off + 2.0 ** -22 * (mag + row.abs())) * g.abs()
+    return loss, losstol, lse, lsetol, dx, off
+
+
+def run_loss(m, n, k, grad, dtype=BF, seed=0, scale=1.0, sigma=0.05, ignored=True):
+    codes, scales = matrix(n, k, seed + 1, sigma)
+    x = rand((m, k), seed + 2, scale=scale)
+    targets = torch.randint(0, n, (m,), device=DEV, generator=gen(seed + 3))
+    if ignored:
+        targets[::5] = -100
+        targets[3::7] = -1
+    dloss = rand((m,), seed + 4, F32) if grad else None
+    need = nf4.mx_cross_entropy_workspace_bytes(n, k, m, grad)
+    wsbuf, ws = alloc((need,), torch.uint8, DEV)
+    lbuf, loss = alloc((m,), F32, DEV)
+    ebuf, lse = alloc((m,), F32, DEV)
+    dbuf, dx = alloc((m, k), dtype, DEV) if grad else (None, None)
+    nf4.nf4_mx_cross_entropy(codes, scales, x, targets, loss, lse, dloss, dx, ws)
+    want = loss_reference(codes, scales, x, targets, dloss)
+    what = f"{m}x{n}x{k}"
+    inside(lse, want[2], want[3], "lse " + what)
+    inside(loss, want[0], want[1], "loss " + what)
+    if grad:
+        tol = want[5] * (1 + HALF[dtype]) + HALF[dtype] * want[4].abs() + 1e-36
+        inside(dx, want[4], torch.where((targets < 0).unsqueeze(1), 0.0, tol), "dX " + what)
+        check(dbuf, "dX")
+    for buf in (wsbuf, lbuf, ebuf):
+        check(buf, "cross entropy")
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("n", [1, 2, 8, 17, 100, 257, 1031])
+@pytest.mark.parametrize("m", [1, 5, 17, 40, 100])
+def test_loss_small(m, n, grad):
+    run_loss(m, n, 96, grad, seed=n, dtype=F32 if n % 2 else BF)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 32000, 4096), (5, 32000, 512), (16, 128256, 128), (33, 50257, 160),
+                                   (70, 50257, 96), (300, 32001, 256), (2100, 40003, 64), (4200, 301, 32),
+                                   (4100, 17000, 32), (130, 700, 8192)])
+@pytest.mark.parametrize("grad", [False, True])
+def test_loss_shapes(m, n, k, grad):
+    run_loss(m, n, k, grad, seed=k, dtype=BF if m % 2 else F32)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-3, 30.0, 1000.0])
+def test_loss_ranges(scale):
+    """Logits that are all zero, nearly equal, and hundreds or ten thousands apart."""
+    run_loss(37, 3000, 128, True, seed=3, scale=scale, dtype=F32)
+
+
+def test_loss_rising_maximum():
+    """Every strip beats the ones before by far, so all but the last count for nothing; and
+    the other way round; over several pieces."""
+    m, n, k = 2100, 36000, 32
+    codes = torch.zeros((n, 16), dtype=torch.uint8, device=DEV)
+    codes[:, 0] = 2                                     # value 1 at k = 0
+    step = torch.arange(n, device=DEV) * 24 // n        # powers of two 2^0 .. 2^23
+    for order in (step, step.flip(0)):
+        scales = (110 + order).to(torch.uint8).reshape(n, 1)
+        x = torch.zeros((m, k), dtype=BF, device=DEV)
+        x[:, 0] = torch.linspace(-64, 64, m, device=DEV).to(BF)
+        targets = torch.arange(m, device=DEV) * 17 % n
+        dloss = torch.ones(m, device=DEV)
+        loss, lse, dx = nf4.mx_cross_entropy(codes, scales, x, targets, dloss, out_dtype=F32)
+        want = loss_reference(codes, scales, x, targets, dloss)
+        inside(lse, want[2], want[3], "lse")
+        inside(loss, want[0], want[1], "loss")
+        inside(dx, want[4], want[5] + 1e-36, "dX")
+
+
+def test_loss_not_finite():
+    codes, scales = matrix(5000, 64, 1)
+    x = rand((8, 64), 2)
+    x[1, 3], x[2, 5] = float("nan"), float("inf")
+    x[3] = float("nan")
+    targets = torch.tensor([1, 2, 3, -1, 4, 5, -7, 6], device=DEV)
+    loss, lse, dx = nf4.mx_cross_entropy(codes, scales, x, targets, torch.ones(8, device=DEV))
+    assert not torch.isfinite(lse[1:4]).any() and not torch.isfinite(loss[1:3]).any()
+    assert not torch.isfinite(dx[1:3]).any()
+    assert loss[3] == 0 and (dx[3] == 0).all() and (dx[6] == 0).all() and torch.isfinite(lse[6])
+    rest = [0, 4, 5, 7]
+    alone = nf4.mx_cross_entropy(codes, scales, x[rest].contiguous(), targets[rest], torch.ones(4, device=DEV))
+    want = loss_reference(codes, scales, x[rest], targets[rest], torch.ones(4, device=DEV))
+    inside(loss[rest], want[0], want[1], "loss")
+    inside(alone[0], want[0], want[1], "loss")
+    inside(dx[rest], want[4], want[5] * 1.01 + 2.0 ** -8 * want[4].abs(), "dX")
+
+
+def test_loss_bad_targets():
+    codes, scales = matrix(100, 64, 1)
+    x = rand((6, 64), 2)
+    targets = torch.tensor([0, 99, 100, -1, 1 << 40, -(1 << 40)], device=DEV)
+    ones = torch.ones(6, device=DEV)
+    with pytest.raises(ValueError, match="flagged targets"):
+        nf4.mx_cross_entropy(codes, scales, x, targets, check=True)
+    loss, lse, dx = nf4.mx_cross_entropy(codes, scales, x, targets, ones)
+    assert (loss[2:] == 0).all() and (dx[2:] == 0).all() and (loss[:2] != 0).all()
+    nf4.mx_cross_entropy(codes, scales, x, targets.clamp(max=99), ones, check=True)
+    status = torch.full((1,), 77, dtype=torch.int32, device=DEV)
+    ws = torch.empty(nf4.mx_cross_entropy_workspace_bytes(100, 64, 6), dtype=torch.uint8, device=DEV)
+    nf4.nf4_mx_cross_entropy(codes, scales, x, targets, loss, lse, workspace=ws, dev_status=status)
+    assert int(status) == nf4.LOSS_BAD_TARGET
+
+
+def test_loss_by_differences():
+    m, n, k = 4, 500, 64
+    codes, scales = matrix(n, k, 1)
+    x = rand((m, k), 2)
+    targets = torch.tensor([3, 499, -100, 250], device=DEV)
+    dloss = rand((m,), 3, F32)
+    dx = nf4.mx_cross_entropy(codes, scales, x, targets, dloss, out_dtype=F32)[2]
+    v = values(codes, scales)
+
+    def total(x):
+        l = x @ v.t().contiguous()
+        t = targets.clamp(min=0).unsqueeze(1)
+        one = torch.logsumexp(l, 1) - l.gather(1, t).squeeze(1)
+        return float((torch.where(targets >= 0, one, 0.0) * dloss.double()).sum())
+
+    for i, j in ((0, 0), (1, 63), (2, 5), (3, 31)):
+        e = torch.zeros((m, k), dtype=torch.float64, device=DEV)
+        e[i, j] = 1e-5
+        want = (total(x.double() + e) - total(x.double() - e)) / 2e-5
+        # bf16 values: 2^-8 of the mean of |v|; the difference itself: 1e-9
+        assert abs(float(dx[i, j]) - want) <= 2.0 ** -7 * float(v[:, j].abs().max() * dloss[i].abs()) + 1e-9
+
+
+def test_loss_same_bits():
+    """Twice the same, and the losses with and without gradient agree within their bounds."""
+    codes, scales = matrix(32000, 256, 1)
+    x = rand((65, 256), 2)
+    targets = torch.randint(0, 32000, (65,), device=DEV)
+    a = nf4.mx_cross_entropy(codes, scales, x, targets, torch.ones(65, device=DEV))
+    b = nf4.mx_cross_entropy(codes, scales, x, targets, torch.ones(65, device=DEV))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
