@@ -19,6 +19,7 @@ MX_BLOCK = 32
 MOE_MAX_E = 512
 MOE_BAD_ID = 1
 LOSS_BAD_TARGET = 1
+MOE_MLP_MAX_T = 64
 
 _STATUS = {0: "NF4_OK", -1: "NF4_EINVAL", -2: "NF4_EALIGN", -3: "NF4_ERANGE",
            -4: "NF4_EDEVICE", -5: "NF4_ELAUNCH"}
@@ -84,7 +85,10 @@ def _load():
     L.nf4_mx_cross_entropy.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, ci, vp, i64, vp, vp]
     L.nf4_mx_cross_entropy_workspace_bytes.argtypes = [i64, i64, i64, ci]
     L.nf4_mx_cross_entropy_workspace_bytes.restype = i64
-    for f in (L.nf4_mx_linear, L.nf4_mx_linear_grad, L.nf4_mx_cross_entropy):
+    L.nf4_moe_mlp.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, i64, i64, ci, vp, vp, ci, vp, i64, vp]
+    L.nf4_moe_mlp_workspace_bytes.argtypes = [i64, i64, i64, ci, i64, i64]
+    L.nf4_moe_mlp_workspace_bytes.restype = i64
+    for f in (L.nf4_mx_linear, L.nf4_mx_linear_grad, L.nf4_mx_cross_entropy, L.nf4_moe_mlp):
         f.restype = ci
     for f in (L.nf4_mx_pack, L.nf4_mx_unpack, L.nf4_mx_gemm, L.nf4_mx_gemm_packed,
               L.nf4_mx_gemm_grouped, L.nf4_mx_gemm_grouped_grad, L.nf4_moe_sort,
@@ -953,3 +957,65 @@ def mx_cross_entropy(codes, scales, X, targets, dloss=None, out_dtype=torch.bflo
         if st:
             raise ValueError(f"nf4_mx_cross_entropy flagged targets: status bits {st:#x}")
     return (loss, lse) if dX is None else (loss, lse, dX)
+
+
+def _mlp_shape(codes1, scales1, codes2, scales2, act):
+    """(E, H, I) of an expert layer's matrices."""
+    E, N1, H = _mx_matrix(codes1, scales1, ndim=3)
+    E2, H2, I = _mx_matrix(codes2, scales2, ndim=3)
+    cols = _act(act, N1)[1]
+    if (E2, H2, I) != (E, H, cols):
+        raise ValueError(f"codes1 {tuple(codes1.shape)} with act {act!r} needs codes2 of [E={E}][H={H}]"
+                         f"[I/2={cols // 2}], got {tuple(codes2.shape)}")
+    return E, H, I
+
+
+def moe_mlp_workspace_bytes(E, H, I, T, topk, act="swiglu"):
+    """Bytes of workspace nf4_moe_mlp needs."""
+    n = _load().nf4_moe_mlp_workspace_bytes(int(E), int(H), int(I), _act(act, 2)[0], int(T), int(topk))
+    if n < 0:
+        raise ValueError(f"invalid sizes E={E} H={H} I={I} T={T} topk={topk}")
+    return int(n)
+
+
+def nf4_moe_mlp(codes1, scales1, codes2, scales2, X, experts, weights, out, act="swiglu", residual=None,
+                workspace=None, stream=None):
+    """out [T][H] (fp32 or bf16) = sum_j weights[t][j] W2[e] act(W1[e] X[t]) + residual[t] with e =
+    experts[t][j] (int64; none outside [0, E)), X bf16 [T][H], at most MOE_MLP_MAX_T tokens; W1
+    packed [E][2 I][H] ([E][I][H] for an act that does not gate), W2 packed [E][H][I].
+    workspace: uint8, moe_mlp_workspace_bytes(E, H, I, T, topk, act)."""
+    E, H, I = _mlp_shape(codes1, scales1, codes2, scales2, act)
+    _need(X, "X", _BF16, (2,))
+    T = X.shape[0]
+    if X.shape[1] != H:
+        raise ValueError(f"X has {X.shape[1]} columns, the matrices H = {H}")
+    _need(experts, "experts", (torch.int64,), (2,))
+    if experts.shape[0] != T:
+        raise ValueError(f"experts must be [T={T}][topk], has {tuple(experts.shape)}")
+    _like(weights, "weights", experts.shape, _F32)
+    _like(out, "out", (T, H), _FLOATS)
+    if residual is not None:
+        _like(residual, "residual", (T, H), (out.dtype,))
+    if workspace is not None:
+        _need(workspace, "workspace", _U8)
+    _run("nf4_moe_mlp", (X, codes1, scales1, codes2, scales2, experts, weights, residual, out, workspace),
+         (codes1.data_ptr(), scales1.data_ptr(), codes2.data_ptr(), scales2.data_ptr(), E, H, I,
+          X.data_ptr(), experts.data_ptr(), weights.data_ptr(), T, experts.shape[1], ACTS[act],
+          _addr(residual), out.data_ptr(), _DTYPE[out.dtype], _addr(workspace),
+          0 if workspace is None else workspace.numel()), stream)
+
+
+def moe_mlp(codes1, scales1, codes2, scales2, X, experts, weights, act="swiglu", residual=None,
+            out_dtype=torch.bfloat16, stream=None):
+    """A whole layer of experts for up to MOE_MLP_MAX_T tokens; see nf4_moe_mlp."""
+    E, H, I = _mlp_shape(codes1, scales1, codes2, scales2, act)
+    _need(X, "X", _BF16, (2,))
+    _need(experts, "experts", (torch.int64,), (2,))
+    if X.shape[0] > MOE_MLP_MAX_T:
+        raise ValueError(f"moe_mlp takes up to {MOE_MLP_MAX_T} tokens, got {X.shape[0]}; sort the tokens "
+                         "(moe_sort) and use the grouped products")
+    out = _empty((X.shape[0], H), out_dtype, X.device, stream)
+    need = _load().nf4_moe_mlp_workspace_bytes(E, H, I, ACTS[act], X.shape[0], experts.shape[1])
+    ws = _empty(max(need, 0), torch.uint8, X.device, stream)
+    nf4_moe_mlp(codes1, scales1, codes2, scales2, X, experts, weights, out, act, residual, ws, stream)
+    return out

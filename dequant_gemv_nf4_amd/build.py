@@ -20,7 +20,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnf4.so")
 SOURCES = ["api.hip", "pack.hip", "gemv.hip", "gemm_mfma.hip", "gemm_prefill.hip", "embed.hip",
-           "ring.hip", "mx_pack.hip", "mx_gemm.hip", "mx_packed.hip", "mx_grad.hip", "moe.hip", "mx_linear.hip", "mx_loss.hip"]
+           "ring.hip", "mx_pack.hip", "mx_gemm.hip", "mx_packed.hip", "mx_grad.hip", "moe.hip", "mx_linear.hip", "mx_loss.hip",
+           "moe_mlp.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # what the library is built from (the hash the benchmark line reports)
 HASHED = ["include/nf4.h"] + ["dequant_gemv_nf4_amd/csrc/" + f for f in
@@ -29,7 +30,7 @@ HASHED = ["include/nf4.h"] + ["dequant_gemv_nf4_amd/csrc/" + f for f in
                                "embed.hip", "ring.hip", "nf4_check.h", "mx_device.h",
                                "mx_pack.hip", "mx_gemm.hip", "mx_packed.hip", "mx_grad.hip",
                                "moe.hip", "mx_product.h", "mx_act.h", "mx_grad.h",
-                               "mx_linear.hip", "mx_loss.hip")]
+                               "mx_linear.hip", "mx_loss.hip", "moe_mlp.hip")]
 BUILD_INFO = os.path.join(HERE, "build_info.json")
 
 

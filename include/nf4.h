@@ -508,6 +508,33 @@ int nf4_mx_cross_entropy(const uint8_t *codes, const uint8_t *scales, int64_t N,
                          int out_dtype, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
                          void *stream);
 
+/*
+ * nf4_moe_mlp -- a whole layer of experts for up to NF4_MOE_MLP_MAX_T tokens:
+ *   out[t] = sum_j weights[t][j] W2[e] f(W1[e] X[t]) + residual[t],  e = experts[t][j]
+ * with W1 the packed matrices (codes1, scales1) [E][N1][H], N1 = I or, gated, 2 I (gate rows
+ * first), and W2 (codes2, scales2) [E][H][I].  X bf16 [T][H], experts int64 [T][topk], weights
+ * fp32 [T][topk], residual (may be NULL) and out [T][H] of one type, fp32 or bf16.
+ *  - A slot whose id is outside [0, E) has no part; a token without any gets its residual, or
+ *    zero.  An expert that a token names twice counts once with the sum of both weights.
+ *  - f(W1 x) times its weight is rounded to bf16 between the products; the sums are fp32, out
+ *    is rounded once.  residual may be out itself.
+ *  - workspace: device memory, 256-byte aligned, of at least nf4_moe_mlp_workspace_bytes(..)
+ *    bytes (-1 for sizes that the call refuses), with anything in it.  Calls that share one
+ *    must not run at the same time.
+ * For more tokens: nf4_moe_sort, nf4_moe_gather, nf4_mx_gemm_grouped and nf4_moe_combine.
+ * T = 0 is valid.  H and I are multiples of 32, N1 * H / 2 and H * I / 2 below 2^31, E and
+ * topk at most NF4_MOE_MAX_E.
+ * Alignment: codes1, codes2, X, residual and out 16 bytes, experts 8.  Errors: NF4_EINVAL for a
+ * null pointer, unknown act or dtype, sizes below 1; NF4_ERANGE for those beyond the limits and
+ * for a missing or short workspace.
+ */
+#define NF4_MOE_MLP_MAX_T 64 /* most tokens of nf4_moe_mlp */
+int64_t nf4_moe_mlp_workspace_bytes(int64_t E, int64_t H, int64_t I, int act, int64_t T, int64_t topk);
+int nf4_moe_mlp(const uint8_t *codes1, const uint8_t *scales1, const uint8_t *codes2, const uint8_t *scales2,
+                int64_t E, int64_t H, int64_t I, const uint16_t *X, const int64_t *experts, const float *weights,
+                int64_t T, int64_t topk, int act, const void *residual, void *out, int out_dtype, void *workspace,
+                int64_t workspace_bytes, void *stream);
+
 /* The 16 NF4 levels L[0..15] (fp32) this library decodes with.  Host only. */
 void nf4_codebook(float out[16]);
 

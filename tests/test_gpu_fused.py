@@ -453,3 +453,126 @@ def test_loss_same_bits():
     a = nf4.mx_cross_entropy(codes, scales, x, targets, torch.ones(65, device=DEV))
     b = nf4.mx_cross_entropy(codes, scales, x, targets, torch.ones(65, device=DEV))
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+# -------------------------------------------------- expert layer for few tokens ----
+def moe_reference(m1, m2, x, experts, weights, act, residual, dtype):
+    """(out, tolerance) in float64."""
+    num, t = m1[0].shape[0], x.shape[0]
+    out = torch.zeros((t, m2[0].shape[1]), dtype=torch.float64, device=DEV)
+    tol = torch.zeros_like(out)
+    share = torch.zeros((t, num), dtype=torch.float64, device=DEV)
+    kept = (experts >= 0) & (experts < num)
+    share.scatter_add_(1, torch.where(kept, experts, 0), torch.where(kept, weights.double(), 0.0))
+    size = torch.zeros_like(share)
+    size.scatter_add_(1, torch.where(kept, experts, 0), torch.where(kept, weights.double().abs(), 0.0))
+    used = torch.zeros_like(share, dtype=torch.bool)
+    used.scatter_(1, torch.where(kept, experts, 0), kept) if experts.numel() else None
+    for e in range(num):
+        tok = torch.nonzero((torch.where(kept, experts, -1) == e).any(1)).squeeze(1)
+        if not tok.numel():
+            continue
+        a, atol, _, _ = linear_reference(m1[0][e], m1[1][e], x[tok], None, act, None, F32)
+        w, wsize = share[tok, e].unsqueeze(1), size[tok, e].unsqueeze(1)
+        a, atol = a * w, atol * w.abs() + 2.0 ** -21 * a.abs() * wsize
+        atol = atol + 2.0 ** -8 * (a.abs() + atol)                 # rounded to bf16
+        v = values(m2[0][e], m2[1][e])
+        out.index_add_(0, tok, a @ v.t().contiguous())
+        off = atol + (v.shape[1] + 8) * 2.0 ** -24 * (a.abs() + atol)
+        tol.index_add_(0, tok, off @ v.abs().t().contiguous())
+    # the sums of a token's experts, and of the waves, in fp32
+    tol = tol + (experts.shape[1] + 24) * 2.0 ** -24 * (out.abs() + tol)
+    if residual is not None:
+        out = out + residual.double()
+        tol = tol + 2.0 ** -23 * (out.abs() + residual.double().abs())
+    return out, tol * (1 + HALF[dtype]) + HALF[dtype] * out.abs() + 1e-30
+
+
+def run_moe(t, k, e, h, i, act="swiglu", residual=False, dtype=BF, seed=0, experts=None):
+    m1 = matrix(2 * i if act in GATED else i, h, seed + 1, lead=(e,))
+    m2 = matrix(h, i, seed + 2, lead=(e,))
+    x = rand((t, h), seed + 3)
+    if experts is None:
+        experts = torch.rand((t, e), device=DEV, generator=gen(seed + 4)).argsort(1)[:, :k].contiguous()
+    weights = rand(experts.shape, seed + 5, F32)
+    r = rand((t, h), seed + 6, dtype) if residual else None
+    obuf, out = alloc((t, h), dtype, DEV)
+    need = nf4.moe_mlp_workspace_bytes(e, h, i, t, experts.shape[1], act)
+    wbuf, ws = alloc((need,), torch.uint8, DEV)
+    nf4.nf4_moe_mlp(*m1, *m2, x, experts, weights, out, act, r, ws)
+    want, tol = moe_reference(m1, m2, x, experts, weights, act, r, dtype)
+    inside(out, want, tol, f"experts {t}x{k} of {e}, {h} x {i} {act}")
+    check(obuf, "out")
+    check(wbuf, "workspace")
+    return m1, m2, x, experts, weights, out
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("t,k,e", [(1, 1, 1), (1, 2, 8), (5, 2, 8), (17, 2, 3), (40, 3, 8), (64, 4, 16)])
+def test_moe_acts(t, k, e, act):
+    run_moe(t, k, e, 96, 64, act, residual=t % 2 == 0, seed=t)
+
+
+@pytest.mark.parametrize("t,k,e,h,i", [(1, 8, 128, 2048, 768), (19, 8, 128, 256, 96), (64, 2, 128, 512, 160),
+                                       (64, 1, 512, 32, 32), (64, 8, 8, 1024, 32), (64, 2, 8, 512, 4096),
+                                       (2, 2, 4, 32, 14336), (3, 4, 6, 8192, 32), (33, 2, 16, 544, 1056),
+                                       (64, 512, 512, 32, 32), (16, 16, 16, 160, 224), (1, 1, 2, 4096, 8224),
+                                       (48, 40, 64, 64, 32)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_moe_shapes(t, k, e, h, i, dtype):
+    run_moe(t, k, e, h, i, residual=dtype == F32, dtype=dtype, seed=h)
+
+
+@pytest.mark.parametrize("t,e", [(4, 8), (64, 8), (64, 64)])
+def test_moe_routing(t, e):
+    """All tokens on one expert, a token on one expert twice, slots and tokens without one."""
+    one = torch.full((t, 2), e - 1, device=DEV)
+    run_moe(t, 2, e, 64, 96, experts=one, seed=1)
+    twice = torch.randint(0, e, (t, 1), device=DEV, generator=gen(2)).expand(t, 3).contiguous()
+    twice[:, 1] = (twice[:, 1] + 1) % e
+    run_moe(t, 3, e, 64, 96, experts=twice, residual=True, seed=2)
+    some = torch.randint(-1, e + 1, (t, 4), device=DEV, generator=gen(3))
+    some[0], some[t - 1, 1:] = -1, torch.tensor([1 << 40, -(1 << 40), e], device=DEV)
+    for residual in (False, True):
+        run_moe(t, 4, e, 64, 96, experts=some, residual=residual, seed=3)
+    none = torch.full((t, 2), -1, device=DEV)
+    out = run_moe(t, 2, e, 64, 96, experts=none, seed=4)[-1]
+    assert (out == 0).all()
+
+
+def test_moe_is_the_layer_of_its_parts():
+    """The layer as sort, gather, products, activation and combine give it."""
+    t, k, e, h, i = 24, 2, 8, 256, 512
+    m1, m2, x, experts, weights, out = run_moe(t, k, e, h, i, dtype=F32)
+    offsets, _, place = nf4.moe_sort(experts, e)
+    z = nf4.mx_gemm_grouped(*m1, nf4.moe_gather(x, place), offsets)
+    gate, up = z.chunk(2, dim=1)
+    a = (torch.nn.functional.silu(gate) * up).to(BF)
+    y = nf4.moe_combine(nf4.mx_gemm_grouped(*m2, a, offsets), place, weights)
+    want, tol = moe_reference(m1, m2, x, experts, weights, "swiglu", None, F32)
+    inside(y, want, tol, "parts")
+    inside(out, want, tol, "whole")
+
+
+def test_moe_infinite_expert_stays_with_its_tokens():
+    t, k, e, h, i = 6, 2, 8, 64, 64
+    for n in (6, 64):
+        m1, m2 = matrix(2 * i, h, 1, lead=(e,)), matrix(h, i, 2, lead=(e,))
+        m1[1][3, 5, 0] = 255                                   # a NaN row of expert 3
+        x = rand((n, h), 3)
+        x[2, 7] = float("inf")
+        experts = torch.tensor([[0, 1], [2, 3], [4, 5], [6, 7], [3, 0], [1, 2]], device=DEV)
+        experts = experts.repeat(11, 1)[:n].contiguous()
+        x[8:] = x[8:].clamp(-3, 3)
+        weights = torch.ones((n, 2), device=DEV)
+        out = nf4.moe_mlp(*m1, *m2, x, experts, weights)
+        bad = (experts == 3).any(1)
+        bad[2] = True
+        assert torch.equal(torch.isnan(out).any(1), bad)
+
+
+def test_moe_no_tokens():
+    m1, m2 = matrix(64, 32, 1, lead=(4,)), matrix(32, 32, 2, lead=(4,))
+    out = nf4.moe_mlp(*m1, *m2, torch.empty((0, 32), dtype=BF, device=DEV),
+                      torch.empty((0, 2), dtype=torch.int64, device=DEV), torch.empty((0, 2), device=DEV))
+    assert out.shape == (0, 32)
