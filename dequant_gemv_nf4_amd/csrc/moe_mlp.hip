@@ -41,14 +41,18 @@ __device__ __forceinline__ void make_masks(const Routing &r, Masks &m) {
   __syncthreads();
 }
 
-// Inclusive prefix over the wave.
+// Inclusive prefix over the wave: within rows of 16 lanes, then the rows' last lanes are
+// passed on (row_bcast 15 and 31).
 __device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_up(v, d, 64);
-    if (lane >= d) v += o;
-  }
+#define NF4_ADD_DPP(ctrl, rows) \
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false)
+  NF4_ADD_DPP(0x111, 0xf);
+  NF4_ADD_DPP(0x112, 0xf);
+  NF4_ADD_DPP(0x114, 0xf);
+  NF4_ADD_DPP(0x118, 0xf);
+  NF4_ADD_DPP(0x142, 0xa);
+  NF4_ADD_DPP(0x143, 0xc);
+#undef NF4_ADD_DPP
   return v;
 }
 
@@ -89,13 +93,16 @@ __device__ __forceinline__ RowTile find_rows(const Routing &r, const Masks &mask
 // The weight of a token's row of expert e.
 __device__ __forceinline__ float row_weight(const Routing &r, int token, int e) {
   float w = 0.f;
-  for (int j = 0; j < r.topk; ++j)
-    if (r.experts[token * r.topk + j] == e) w += r.weights[token * r.topk + j];
+#pragma unroll 4
+  for (int j = 0; j < r.topk; ++j) {  // both loaded, so that no load waits for another
+    const float v = r.weights[token * r.topk + j];
+    w += r.experts[token * r.topk + j] == e ? v : 0.f;
+  }
   return w;
 }
 
+// A tile's rows, for as long as it takes.
 struct TileState {
-  Masks masks;
   int tokens[kTokens];
   float weight[kTokens];
 };
@@ -103,14 +110,18 @@ __device__ __forceinline__ TileState &tile_state() {
   __shared__ TileState s;
   return s;
 }
+// A tile of the longer products; the masks are done with before the stages come to their place.
+__device__ __forceinline__ RowTile tile_rows(const Routing &r, int slot, int bm, void *lds) {
+  Masks &masks = *static_cast<Masks *>(lds);
+  make_masks(r, masks);
+  return find_rows(r, masks, slot, bm, tile_state().tokens);
+}
 
 // Rows of X by the tokens of a tile.
 struct TokenRows {
   Routing r;
-  __device__ __forceinline__ RowTile find(const Args &, int slot, int bm) const {
-    TileState &s = tile_state();
-    make_masks(r, s.masks);
-    return find_rows(r, s.masks, slot, bm, s.tokens);
+  __device__ __forceinline__ RowTile find(const Args &, int slot, int bm, void *lds) const {
+    return tile_rows(r, slot, bm, lds);
   }
   __device__ __forceinline__ int64_t base(const RowTile &) const { return 0; }
   __device__ __forceinline__ int whole(const Args &, const RowTile &) const { return r.T; }
@@ -122,10 +133,8 @@ struct TokenRows {
 // Rows as the first kernel wrote them.
 struct PairRows {
   Routing r;
-  __device__ __forceinline__ RowTile find(const Args &, int slot, int bm) const {
-    TileState &s = tile_state();
-    make_masks(r, s.masks);
-    return find_rows(r, s.masks, slot, bm, s.tokens);
+  __device__ __forceinline__ RowTile find(const Args &, int slot, int bm, void *lds) const {
+    return tile_rows(r, slot, bm, lds);
   }
   __device__ __forceinline__ int64_t base(const RowTile &t) const { return t.row0; }
   __device__ __forceinline__ int whole(const Args &, const RowTile &t) const { return t.rows; }
@@ -218,15 +227,18 @@ struct RangeLoads {
   }
 };
 
-// The range of up to 16 rows of X: row offsets are the lane's (l16).
-__device__ __forceinline__ void load_range(u32x4_t (&x)[4][4], __amdgpu_buffer_rsrc_t xrs, int row_bytes, int K, int k0) {
+// The range of up to 16 rows of X: row offsets are the lane's (l16); lanes without a row (not
+// `in`) take zeros.  No branch here or in the products: behind one the compiler could not
+// count the loads in flight and would wait for all of them.
+__device__ __forceinline__ void load_range(u32x4_t (&x)[4][4], __amdgpu_buffer_rsrc_t xrs, bool in, int row_bytes,
+                                           int K, int k0) {
   const int q = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int k = k0 + 128 * s + 32 * q;
+    const int at = in && k < K ? row_bytes + k * 2 : kOutside;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      x[s][j] = __builtin_amdgcn_raw_buffer_load_b128(xrs, k < K ? row_bytes + k * 2 + j * 16 : kOutside, 0, 0);
+    for (int j = 0; j < 4; ++j) x[s][j] = __builtin_amdgcn_raw_buffer_load_b128(xrs, at + j * 16, 0, 0);
   }
 }
 
@@ -235,90 +247,143 @@ __device__ __forceinline__ f32x4_t multiply(const RangeLoads<SVEC, PAIRS> &w, co
                                             int K, int k0) {
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    if (k0 + 128 * s < K) {  // uniform
-      const float sc = w.scale(s, K, k0);
+    const float sc = w.scale(s, K, k0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc = mfma16(decode8(w.cw[s][j], sc), x[s][j], acc);
-    }
+    for (int j = 0; j < 4; ++j) acc = mfma16(decode8(w.cw[s][j], sc), x[s][j], acc);
   }
   return acc;
 }
 
-// First product: a workgroup owns 16 G weight rows (columns) of a tile; its waves share out
-// the ranges of K.
+// First product.  The work is the items (tile of rows, block of 16 G weight rows), in this
+// order, dealt out in runs of equal length: as many workgroups as the CUs hold, each with
+// one run, so that nothing depends on how the tokens chose.  In a tile the workgroup's
+// waves have a range of K each (several in turn, if K is longer than the waves' ranges),
+// whose rows of X stay in registers while the weights pass by; the next block is always
+// under way; the waves' sums meet in LDS once a block, in the two halves of `part` in turn.
+struct UpArgs {
+  Args p;
+  Routing r;
+  int blocks, act;
+  uint32_t *counters;  // of the second product, set to zero here
+  int ncounters;
+};
+
+// Tiles of all experts.
+__device__ __forceinline__ int count_tiles(const Routing &r, const Masks &masks) {
+  int n = 0;
+  for (int base = 0; base < r.E; base += 64) {
+    const int e = base + (threadIdx.x & 63);
+    const int rows = e < r.E ? __popcll(mask_of(masks, e)) : 0;
+    n += __builtin_amdgcn_readlane((int)wave_prefix((uint32_t)(rows + 15) >> 4), 63);
+  }
+  return n;
+}
+
 template <int G, bool SVEC, bool PAIRS>
 __global__ void __launch_bounds__(512)
-    moe_up_kernel(Args p, int blocks, Routing r, int act) {
-  extern __shared__ float part[];  // [wave][row][16 G]
-  const int slot = blockIdx.x / blocks, n0 = (blockIdx.x - slot * blocks) * 16 * G;
-  const TokenRows rows{r};
-  const RowTile t = rows.find(p, slot, 16);
-  if (t.rows <= 0) return;
+    moe_up_kernel(UpArgs a) {
+  extern __shared__ float part[];  // [2][wave][row][16 G]
+  __shared__ Masks masks;
+  const Args &p = a.p;
+  const Routing &r = a.r;
   TileState &st = tile_state();
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int cols = min(16 * G, p.N - n0);
   const int kb = p.K >> 5, kc = p.K >> 1;
-  const int64_t first = (int64_t)t.e * p.N + (PAIRS ? n0 >> 1 : n0);
-  const int wrows = PAIRS ? (p.N + cols) >> 1 : cols;
-  const uint8_t *const cbase = p.codes + first * kc, *const sbase = p.scales + first * kb;
-  const __amdgpu_buffer_rsrc_t xrs = buffer(p.X, (int64_t)r.T * p.K * 2);
-  const int xrow = (l16 < t.rows ? st.tokens[l16] : r.T) * p.K * 2;
-  if ((int)threadIdx.x < t.rows) st.weight[threadIdx.x] = row_weight(r, st.tokens[threadIdx.x], t.e);
-  f32x4_t acc[G];
+  make_masks(r, masks);
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.ncounters; i += gridDim.x * blockDim.x)
+    a.counters[i] = 0u;
+  const int64_t items = (int64_t)count_tiles(r, masks) * a.blocks;
+  const int64_t lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
+  const int passes = (p.K + waves * kRange - 1) / (waves * kRange);
+  const ActRows<PAIRS> out{r, a.act};
+  float *half = part;
+  int first = threadIdx.x;  // of a block's outputs: another wave has them each time
+  for (int64_t at = lo; at < hi;) {
+    const int tile = (int)(at / a.blocks), b0 = (int)(at - (int64_t)tile * a.blocks);
+    const int b1 = (int)(hi - at < a.blocks - b0 ? b0 + (hi - at) : a.blocks);
+    at += b1 - b0;
+    __syncthreads();  // the last tile's state has been read
+    const RowTile t = find_rows(r, masks, tile, 16, st.tokens);
+    const uint8_t *const ce = p.codes + (int64_t)t.e * p.N * kc, *const se = p.scales + (int64_t)t.e * p.N * kb;
+    const __amdgpu_buffer_rsrc_t xrs = buffer(p.X, (int64_t)r.T * p.K * 2);
+    const int xrow = (l16 < t.rows ? st.tokens[l16] : 0) * p.K * 2;
+    const int kfirst = wave * kRange;
+    RangeLoads<SVEC, PAIRS> w[G];
+    const auto load = [&](RangeLoads<SVEC, PAIRS> &to, int b, int g, int k0) __attribute__((always_inline)) {
+      const int n0 = b * 16 * G, cols = b < b1 ? min(16 * G, p.N - n0) : 0;  // past the run the buffers are empty
+      const int col = PAIRS ? n0 >> 1 : n0, wrows = PAIRS && cols > 0 ? (p.N + cols) >> 1 : cols;
+      to.load(ce + (int64_t)col * kc, se + (int64_t)col * kb, wrows, g * 16, p.N, p.K, k0);
+    };
 #pragma unroll
-  for (int g = 0; g < G; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = wave * kRange; k0 < p.K; k0 += waves * kRange) {
-    RangeLoads<SVEC, PAIRS> w[2];
+    for (int g = 0; g < G; ++g) load(w[g], b0, g, kfirst);
     u32x4_t x[4][4];
-    w[0].load(cbase, sbase, wrows, 0, p.N, p.K, k0);
-    load_range(x, xrs, xrow, p.K, k0);
+    load_range(x, xrs, l16 < t.rows, xrow, p.K, kfirst);
+    if ((int)threadIdx.x < t.rows) st.weight[threadIdx.x] = row_weight(r, st.tokens[threadIdx.x], t.e);
+    for (int b = b0; b < b1; ++b) {
+      const int n0 = b * 16 * G;
+      f32x4_t acc[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      if (g + 1 < G) w[(g + 1) & 1].load(cbase, sbase, wrows, (g + 1) * 16, p.N, p.K, k0);
-      acc[g] = multiply(w[g & 1], x, acc[g], p.K, k0);
-    }
-  }
+      for (int g = 0; g < G; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int pass = 0; pass < passes; ++pass) {
+        const int k0 = kfirst + pass * waves * kRange;
+        const bool last = pass + 1 == passes;
+        const int k1 = last ? kfirst : k0 + waves * kRange;
 #pragma unroll
-  for (int g = 0; g < G; ++g)
-    if (l16 < t.rows) *reinterpret_cast<f32x4_t *>(part + (wave * 16 + l16) * (16 * G) + g * 16 + q * 4) = acc[g];
-  __syncthreads();
-  const ActRows<PAIRS> out{r, act};
-  constexpr int W = PAIRS ? 8 : 4, quads = 16 * G / W;
-  for (int i = threadIdx.x; i < t.rows * quads; i += blockDim.x) {
-    const int m = i / quads, c = i % quads * W;
-    if (n0 + c >= p.N) continue;
-    f32x4_t a = {0.f, 0.f, 0.f, 0.f}, b = a;
-    for (int k = 0; k < waves; ++k) {
-      const float *s = part + (k * 16 + m) * (16 * G) + c;
-      a += *reinterpret_cast<const f32x4_t *>(s);
-      if constexpr (PAIRS) b += *reinterpret_cast<const f32x4_t *>(s + 4);
+        for (int g = 0; g < G; ++g) {
+          acc[g] = multiply(w[g], x, acc[g], p.K, k0);
+          load(w[g], last ? b + 1 : b, g, k1);
+          __builtin_amdgcn_sched_barrier(0);  // else the loads are moved to where they are needed
+        }
+        if (passes > 1) load_range(x, xrs, l16 < t.rows, xrow, p.K, k1);
+      }
+      if (l16 < t.rows) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          *reinterpret_cast<f32x4_t *>(half + (wave * 16 + l16) * (16 * G) + g * 16 + q * 4) = acc[g];
+      }
+      __syncthreads();
+      constexpr int W = PAIRS ? 8 : 4, quads = 16 * G / W;
+      for (int i = first; i < t.rows * quads; i += blockDim.x) {
+        const int m = i / quads, c = i % quads * W;
+        if (n0 + c >= p.N) continue;
+        f32x4_t u = {0.f, 0.f, 0.f, 0.f}, v = u;
+        for (int k = 0; k < waves; ++k) {
+          const float *s = half + (k * 16 + m) * (16 * G) + c;
+          u += *reinterpret_cast<const f32x4_t *>(s);
+          if constexpr (PAIRS) v += *reinterpret_cast<const f32x4_t *>(s + 4);
+        }
+        if constexpr (PAIRS)
+          out.put(p, t, m, (n0 + c) >> 1, f32x4_t{u[0], u[2], v[0], v[2]}, f32x4_t{u[1], u[3], v[1], v[3]});
+        else
+          out.put(p, t, m, n0 + c, u, u);
+      }
+      half = half == part ? part + waves * 16 * 16 * G : part;
+      first = first < 64 ? first + blockDim.x - 64 : first - 64;
     }
-    if constexpr (PAIRS)
-      out.put(p, t, m, (n0 + c) >> 1, f32x4_t{a[0], a[2], b[0], b[2]}, f32x4_t{a[1], a[3], b[1], b[3]});
-    else
-      out.put(p, t, m, n0 + c, a, a);
   }
 }
 
-// Second product and the sum over a token's experts: a workgroup owns 16 columns of the
-// output for all tokens; its waves share out the ranges of all experts' I and add, each
-// for itself and in one order, into sums of its own in LDS.
+// Second product and the sum over a token's experts: a workgroup owns 16 G columns of the
+// output for all tokens (G groups of 16, for which a range of the rows is loaded once).  A unit is a range of an expert's I; the units go in turn to the
+// waves of the `splits` workgroups that share the columns, and a wave adds its units, in
+// order, into sums of its own in LDS.
 struct ActiveExperts {
   Masks masks;
   uint16_t expert[NF4_MOE_MAX_E];
   uint16_t row0[NF4_MOE_MAX_E];
   int count;
 };
-template <bool SVEC, typename OUT>
+template <int G, bool SVEC, typename OUT>
 __global__ void __launch_bounds__(512)
-    moe_down_kernel(Args p, Routing r, const void *residual) {
-  extern __shared__ float sums[];  // [wave][token][16]
+    moe_down_kernel(Args p, int splits, Routing r, const void *residual, float *parts, uint32_t *counters) {
+  constexpr int kCols = 16 * G, kQuads = kCols / 4;
+  extern __shared__ float sums[];  // [wave][token][kCols]
   __shared__ ActiveExperts act;
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int n0 = blockIdx.x * 16, cols = min(16, p.N - n0);
-  for (int i = threadIdx.x; i < waves * r.T * 16; i += blockDim.x) sums[i] = 0.f;
+  const int block = blockIdx.x / splits, split = blockIdx.x - block * splits;
+  const int n0 = block * kCols, cols = min(kCols, p.N - n0);
   make_masks(r, act.masks);
   if (wave == 0) {
     uint32_t before = 0;
@@ -336,45 +401,86 @@ __global__ void __launch_bounds__(512)
     }
     if (lane == 0) act.count = (int)(before >> 16);
   }
+  for (int i = threadIdx.x; i < waves * r.T * (kCols / 4); i += blockDim.x)
+    reinterpret_cast<f32x4_t *>(sums)[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
   const int kb = p.K >> 5, kc = p.K >> 1;
-  const int ranges = (p.K + kRange - 1) / kRange, units = act.count * ranges;
-  float *const own = sums + wave * r.T * 16;
-  const auto start = [&](RangeLoads<SVEC, false> &w, int u) __attribute__((always_inline)) {
-    const int i = u / ranges, k0 = (u - i * ranges) * kRange;
-    const int64_t first = (int64_t)act.expert[u < units ? i : 0] * p.N + n0;
-    w.load(p.codes + first * kc, p.scales + first * kb, u < units ? cols : 0, 0, p.N, p.K, k0);
+  // read from LDS, but the same for the wave: buffers have to be in scalar registers
+  const auto uniform = [](int v) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(v); };
+  const int ranges = (p.K + kRange - 1) / kRange, units = uniform(act.count) * ranges, step = waves * splits;
+  float *const own = sums + wave * r.T * kCols;
+  struct Unit {  // past the last one `rows` and `cols` are 0, and its buffers empty
+    int e, row0, rows, cols, k0;
+    uint64_t mask;
   };
-  RangeLoads<SVEC, false> w;
-  if (units > 0) start(w, wave);
-  for (int u = wave; u < units; u += waves) {
-    const int i = u / ranges, k0 = (u - i * ranges) * kRange;
-    const uint64_t mask = mask_of(act.masks, act.expert[i]);
-    const int n = __popcll(mask), rank = __popcll(mask & ((uint64_t(1) << lane) - 1));
-    RangeLoads<SVEC, false> now = w;
-    start(w, u + waves);
-    for (int m0 = 0; m0 < n; m0 += 16) {
-      const int rows = min(16, n - m0);
-      const __amdgpu_buffer_rsrc_t xrs = buffer(p.X + (int64_t)(act.row0[i] + m0) * p.K, (int64_t)rows * p.K * 2);
-      u32x4_t x[4][4];
-      load_range(x, xrs, l16 * p.K * 2, p.K, k0);
-      // the token of row l16: lanes are tokens, and send theirs to their row
-      const bool mine = (mask >> lane & 1) && rank >= m0 && rank < m0 + 16;
-      const int token = __builtin_amdgcn_ds_permute(mine ? (rank - m0) * 4 : 63 * 4, lane);
-      const int tok = __shfl(token, l16, 64);
-      const f32x4_t v = multiply(now, x, f32x4_t{0.f, 0.f, 0.f, 0.f}, p.K, k0);
-      if (l16 < rows) {
+  const auto unit = [&](int u) __attribute__((always_inline)) {
+    const bool ok = u < units;
+    const int i = ok ? u / ranges : 0;
+    Unit v{uniform(act.expert[i]), uniform(act.row0[i]), 0, ok ? cols : 0, ok ? (u - i * ranges) * kRange : 0, 0};
+    const uint64_t m = (uint64_t)(uint32_t)uniform(act.masks.of[2 * v.e + 1]) << 32 | (uint32_t)uniform(act.masks.of[2 * v.e]);
+    v.mask = ok ? m : 0;
+    v.rows = __popcll(v.mask);
+    return v;
+  };
+  const auto load_x = [&](u32x4_t (&x)[4][4], const Unit &v, int m0) __attribute__((always_inline)) {
+    const int rows = max(min(16, v.rows - m0), 0);
+    load_range(x, buffer(p.X + (int64_t)(v.row0 + m0) * p.K, (int64_t)rows * p.K * 2), l16 < rows, l16 * p.K * 2, p.K,
+               v.k0);
+  };
+  const auto load_w = [&](RangeLoads<SVEC, false> &w, const Unit &v, int g) __attribute__((always_inline)) {
+    const int64_t first = (int64_t)v.e * p.N + n0;
+    w.load(p.codes + first * kc, p.scales + first * kb, v.cols, g * 16, p.N, p.K, v.k0);
+  };
+  // Row l16's token: lanes are tokens, and send theirs to their row.
+  const auto token = [&](const Unit &v, int m0) __attribute__((always_inline)) {
+    const int rank = (int)__popcll(v.mask & ((uint64_t(1) << lane) - 1)) - m0;
+    const bool mine = (v.mask >> lane & 1) && rank >= 0 && rank < 16;
+    return __shfl(__builtin_amdgcn_ds_permute(mine ? rank * 4 : 63 * 4, lane), l16, 64);
+  };
+  const auto add = [&](const Unit &v, int m0, int tok, int g, f32x4_t s) __attribute__((always_inline)) {
+    if (m0 + l16 < v.rows) *reinterpret_cast<f32x4_t *>(own + tok * kCols + g * 16 + q * 4) += s;
+  };
+  RangeLoads<SVEC, false> w[G > 1 ? 2 : 1];
+  u32x4_t x[2][4][4];
+  const auto turn = [&](u32x4_t (&now)[4][4], u32x4_t (&next)[4][4], const Unit &v, const Unit &after)
+                        __attribute__((always_inline)) {
+    const int tok = token(v, 0);
+    load_x(next, after, 0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) own[tok * 16 + q * 4 + c] += v[c];
+    for (int g = 0; g < G; ++g) {
+      RangeLoads<SVEC, false> one;
+      RangeLoads<SVEC, false> &use = G > 1 ? w[g & 1] : one;
+      if constexpr (G == 1) one = w[0];
+      if (g + 1 < G)
+        load_w(w[(g + 1) & 1], v, g + 1);
+      else
+        load_w(w[0], after, 0);
+      __builtin_amdgcn_sched_barrier(0);  // else the loads are moved to where they are needed
+      add(v, 0, tok, g, multiply(use, now, f32x4_t{0.f, 0.f, 0.f, 0.f}, p.K, v.k0));
+    }
+    for (int m0 = 16; m0 < v.rows; m0 += 16) {  // more rows than a tile: the weights once more
+      const int more = token(v, m0);
+      load_x(now, v, m0);
+#pragma unroll 1
+      for (int g = 0; g < G; ++g) {
+        RangeLoads<SVEC, false> again;
+        load_w(again, v, g);
+        add(v, m0, more, g, multiply(again, now, f32x4_t{0.f, 0.f, 0.f, 0.f}, p.K, v.k0));
       }
     }
+  };
+  const int u0 = split * waves + wave;
+  Unit a = unit(u0);
+  load_w(w[0], a, 0);
+  load_x(x[0], a, 0);
+  for (int u = u0; u < units; u += 2 * step) {
+    const Unit b = unit(u + step);
+    turn(x[0], x[1], a, b);
+    a = unit(u + 2 * step);
+    turn(x[1], x[0], b, a);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < r.T * 4; i += blockDim.x) {
-    const int t = i >> 2, c = (i & 3) * 4;
-    if (n0 + c >= p.N) continue;
-    f32x4_t v = *reinterpret_cast<const f32x4_t *>(sums + t * 16 + c);
-    for (int k = 1; k < waves; ++k) v += *reinterpret_cast<const f32x4_t *>(sums + (k * r.T + t) * 16 + c);
+  const auto put = [&](int t, int c, f32x4_t v) __attribute__((always_inline)) {
     const int64_t at = (int64_t)t * p.N;
     if (residual) {
       const OUT *s = reinterpret_cast<const OUT *>(residual) + at + n0 + c;
@@ -386,6 +492,42 @@ __global__ void __launch_bounds__(512)
       }
     }
     store4<OUT>(reinterpret_cast<OUT *>(p.Y) + at, n0 + c, p.N, v, true);
+  };
+  float *const all = parts + (int64_t)block * splits * r.T * kCols;
+  for (int i = threadIdx.x; i < r.T * kQuads; i += blockDim.x) {
+    const int t = i / kQuads, c = i % kQuads * 4;
+    f32x4_t v = *reinterpret_cast<const f32x4_t *>(sums + t * kCols + c);
+    for (int k = 1; k < waves; ++k) v += *reinterpret_cast<const f32x4_t *>(sums + (k * r.T + t) * kCols + c);
+    if (splits == 1) {
+      if (n0 + c < p.N) put(t, c, v);
+      continue;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)  // agent-scope: performed where every XCD sees them
+      __hip_atomic_store(all + (split * r.T + t) * kCols + c + k, v[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (splits == 1) return;
+  // The last of the columns' workgroups to come here adds all parts, in order.  Each
+  // thread waits until its stores are performed (vmcnt), the barrier puts that before the
+  // count, and only the workgroup that saw the last count reads, with loads that go where
+  // the stores went.
+  __shared__ int last;
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(counters + block, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+           (uint32_t)(splits - 1);
+  __syncthreads();
+  if (!last) return;
+  for (int i = threadIdx.x; i < r.T * kQuads; i += blockDim.x) {
+    const int t = i / kQuads, c = i % kQuads * 4;
+    if (n0 + c >= p.N) continue;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] += __hip_atomic_load(all + (s * r.T + t) * kCols + c + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    put(t, c, v);
   }
 }
 
@@ -440,41 +582,91 @@ struct MlpArgs {
   const void *residual;
   void *out;
   int out_dtype;
-  uint16_t *rows;  // [pairs][I]
-  float *sums;     // [pairs][H], in the tiled form
+  uint16_t *rows;      // [pairs][I]
+  float *sums;         // [pairs][H] in the tiled form, else the second product's parts
+  uint32_t *counters;  // of the column blocks that are shared out
   int64_t pairs;
 };
 
-// Whether the rows of an expert are few (16 a tile) or the tiles of the longer products are used.
-static bool few_rows(int64_t T, int64_t topk, int64_t E) { return T * topk <= 4 * E || T <= 16; }
+// Whether the rows of an expert are few (16 a tile) or the tiles of the longer products are
+// used; at most 2^13 pairs either way (16 x 512, or eight an expert).
+// Both, us, 4096 x 14336 of 8 experts, two a token: 24 tokens 167 and 175, 32 172 and 182, 64
+// 289 and 229; 2048 x 768 of 64, eight a token: 64 tokens 59 and 59.
+static bool few_rows(int64_t T, int64_t topk, int64_t E) { return T * topk <= 8 * E || T <= 16; }
+
+// the tiles that there can be
+static int64_t tiles_of(int64_t pairs, int64_t E) { return slots_for(pairs, E, true, 16); }
 
 template <bool PAIRS>
-static int launch_up_few(const MlpArgs &a, hipStream_t s) {
-  constexpr int G = 4;
-  const Args p{a.codes1, a.scales1, a.X, nullptr, a.rows, a.pairs, a.E, a.N1, a.H, {}};
-  const int64_t slots = slots_for(a.pairs, a.E, true, 16), blocks = (a.N1 + 16 * G - 1) / (16 * G);
+static int launch_up_few(const MlpArgs &a, int ncounters, hipStream_t s) {
   const int ranges = (a.H + kRange - 1) / kRange, waves = ranges < 8 ? ranges : 8;
-  if (slots * blocks * waves * 64 >= (int64_t(1) << 32)) return NF4_ERANGE;
-  const dim3 grid((unsigned)(slots * blocks)), threads(64 * waves);
-  const size_t lds = (size_t)waves * 16 * 16 * G * 4;
-  if (a.H % 128 == 0 && aligned_to(a.scales1, 4))
-    hipLaunchKernelGGL((moe_up_kernel<G, true, PAIRS>), grid, threads, lds, s, p, (int)blocks, a.r, a.act);
+  const int hold = 256 * (8 / waves);
+  const int64_t tiles = tiles_of(a.pairs, a.E);
+  // blocks of one group where four to a block would leave CUs without one
+  const int g = tiles * ((a.N1 + 63) / 64) >= hold ? 4 : 1, blocks = (a.N1 + 16 * g - 1) / (16 * g);
+  const dim3 grid((unsigned)(tiles * blocks < hold ? tiles * blocks : hold)), threads(64 * waves);
+  const size_t lds = (size_t)waves * 16 * 16 * g * 4 * 2;
+  const UpArgs u{{a.codes1, a.scales1, a.X, nullptr, a.rows, a.pairs, a.E, a.N1, a.H, {}}, a.r, blocks, a.act,
+                 a.counters, ncounters};
+  const bool svec = a.H % 128 == 0 && aligned_to(a.scales1, 4);
+  if (g == 4 && svec)
+    hipLaunchKernelGGL((moe_up_kernel<4, true, PAIRS>), grid, threads, lds, s, u);
+  else if (g == 4)
+    hipLaunchKernelGGL((moe_up_kernel<4, false, PAIRS>), grid, threads, lds, s, u);
+  else if (svec)
+    hipLaunchKernelGGL((moe_up_kernel<1, true, PAIRS>), grid, threads, lds, s, u);
   else
-    hipLaunchKernelGGL((moe_up_kernel<G, false, PAIRS>), grid, threads, lds, s, p, (int)blocks, a.r, a.act);
+    hipLaunchKernelGGL((moe_up_kernel<1, false, PAIRS>), grid, threads, lds, s, u);
   return launch_status(hipGetLastError());
 }
 
-template <typename OUT>
-static int launch_down_few(const MlpArgs &a, hipStream_t s) {
+// How the second product is dealt out: groups of 16 columns a workgroup, and workgroups that
+// share a column block's units, as many as make one a CU.
+struct DownPlan {
+  int g, blocks, splits;
+};
+static DownPlan down_plan(int64_t H, int64_t I, int64_t tiles) {
+  DownPlan d;
+  const int64_t units = tiles * ((I + kRange - 1) / kRange);
+  const auto splits = [&](int g) {
+    const int64_t b = (H + 16 * g - 1) / (16 * g), most = (units + 7) / 8;
+    const int64_t n = b >= 192 ? 1 : 256 / b;
+    return n < most ? n : most;
+  };
+  // G = 4 from where every wave of the chip has a unit and a half, us against G = 1: 2 experts
+  // of 4096 x 14336 (56 units) 21.3, 24.0; of 4096 x 4096 (16) 14.9, 9.1; 8 of 128 of 2048 x
+  // 768 (16) 14.8, 9.8, about 90 of them 29, 32
+  const int64_t b4 = (H + 63) / 64;
+  d.g = 2 * units * (b4 < 256 ? b4 : 256) >= 3 * 8 * 256 ? 4 : 1;
+  d.blocks = (int)((H + 16 * d.g - 1) / (16 * d.g));
+  d.splits = (int)splits(d.g);
+  return d;
+}
+
+template <int G, typename OUT>
+static int launch_down_as(const MlpArgs &a, const DownPlan &d, hipStream_t s) {
   const Args p{a.codes2, a.scales2, a.rows, nullptr, a.out, a.pairs, a.E, a.H, a.I, {}};
   const int waves = 8;
-  const dim3 grid((unsigned)((a.H + 15) / 16)), threads(64 * waves);
-  const size_t lds = (size_t)waves * a.r.T * 16 * 4;
+  const dim3 grid((unsigned)(d.blocks * d.splits)), threads(64 * waves);
+  const size_t lds = (size_t)waves * a.r.T * 16 * G * 4;
   if (a.I % 128 == 0 && aligned_to(a.scales2, 4))
-    hipLaunchKernelGGL((moe_down_kernel<true, OUT>), grid, threads, lds, s, p, a.r, a.residual);
+    hipLaunchKernelGGL((moe_down_kernel<G, true, OUT>), grid, threads, lds, s, p, d.splits, a.r, a.residual, a.sums,
+                       a.counters);
   else
-    hipLaunchKernelGGL((moe_down_kernel<false, OUT>), grid, threads, lds, s, p, a.r, a.residual);
+    hipLaunchKernelGGL((moe_down_kernel<G, false, OUT>), grid, threads, lds, s, p, d.splits, a.r, a.residual, a.sums,
+                       a.counters);
   return launch_status(hipGetLastError());
+}
+template <typename OUT>
+static int launch_down_few(const MlpArgs &a, const DownPlan &d, hipStream_t s) {
+  return d.g == 4 ? launch_down_as<4, OUT>(a, d, s) : launch_down_as<1, OUT>(a, d, s);
+}
+
+static int launch_few(const MlpArgs &a, hipStream_t s) {
+  const DownPlan d = down_plan(a.H, a.I, tiles_of(a.pairs, a.E));
+  const int n = d.splits > 1 ? d.blocks : 0;
+  if (int r = is_gated(a.act) ? launch_up_few<true>(a, n, s) : launch_up_few<false>(a, n, s)) return r;
+  return a.out_dtype == NF4_F32 ? launch_down_few<float>(a, d, s) : launch_down_few<uint16_t>(a, d, s);
 }
 
 template <class ROWS, class EPI, bool F32, bool B16>
@@ -488,10 +680,7 @@ static int launch_tiles(Product<ROWS, EPI, F32, B16> p) {
 }
 
 static int launch_mlp(const MlpArgs &a, hipStream_t s) {
-  if (few_rows(a.r.T, a.r.topk, a.E)) {
-    if (int r = is_gated(a.act) ? launch_up_few<true>(a, s) : launch_up_few<false>(a, s)) return r;
-    return a.out_dtype == NF4_F32 ? launch_down_few<float>(a, s) : launch_down_few<uint16_t>(a, s);
-  }
+  if (few_rows(a.r.T, a.r.topk, a.E)) return launch_few(a, s);
   const Args up{a.codes1, a.scales1, a.X, nullptr, a.rows, a.pairs, a.E, a.N1, a.H, {}};
   int r;
   if (is_gated(a.act))
@@ -513,7 +702,24 @@ static int launch_mlp(const MlpArgs &a, hipStream_t s) {
 
 // pairs (token, expert) at most, and where the second part of the workspace starts
 static int64_t pair_count(int64_t T, int64_t topk, int64_t E) { return T * (topk < E ? topk : E); }
-static int64_t rows_bytes(int64_t pairs, int64_t I) { return (pairs * I * 2 + 255) / 256 * 256; }
+static int64_t whole(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+// what of the workspace is whose
+struct MlpPlan {
+  int64_t pairs, sums, counters, bytes;
+};
+static MlpPlan mlp_plan(int64_t E, int64_t H, int64_t I, int64_t T, int64_t topk) {
+  MlpPlan d;
+  d.pairs = pair_count(T, topk, E);
+  d.sums = whole(d.pairs * I * 2);
+  if (!few_rows(T, topk, E)) {
+    d.counters = d.bytes = d.sums + whole(d.pairs * H * 4);
+    return d;
+  }
+  const DownPlan s = down_plan(H, I, tiles_of(d.pairs, E));
+  d.counters = d.sums + (s.splits > 1 ? whole((int64_t)s.blocks * s.splits * T * 16 * s.g * 4) : 0);
+  d.bytes = d.counters + (s.splits > 1 ? whole((int64_t)s.blocks * 4) : 0);
+  return d;
+}
 
 static int check_mlp(int64_t E, int64_t H, int64_t I, int act, int64_t T, int64_t topk) {
   if (E < 1 || T < 0 || topk < 1 || !known_act(act)) return NF4_EINVAL;
@@ -532,8 +738,7 @@ extern "C" {
 int64_t nf4_moe_mlp_workspace_bytes(int64_t E, int64_t H, int64_t I, int act, int64_t T, int64_t topk) {
   using namespace nf4::mx;
   if (check_mlp(E, H, I, act, T, topk)) return -1;
-  const int64_t pairs = pair_count(T, topk, E);
-  return rows_bytes(pairs, I) + (few_rows(T, topk, E) ? 0 : pairs * H * 4);
+  return T == 0 ? 0 : mlp_plan(E, H, I, T, topk).bytes;
 }
 
 int nf4_moe_mlp(const uint8_t *codes1, const uint8_t *scales1, const uint8_t *codes2, const uint8_t *scales2,
@@ -553,11 +758,12 @@ int nf4_moe_mlp(const uint8_t *codes1, const uint8_t *scales1, const uint8_t *co
     return NF4_ERANGE;
   if (int r = nf4::device_status()) return r;
   if (T == 0) return NF4_OK;
-  const int64_t pairs = pair_count(T, topk, E);
+  const MlpPlan d = mlp_plan(E, H, I, T, topk);
   uint8_t *const ws = static_cast<uint8_t *>(workspace);
   const MlpArgs a{codes1, scales1, codes2, scales2, (int)E, (int)H, (int)I, (int)(is_gated(act) ? 2 * I : I), X,
                   {experts, weights, (int)T, (int)topk, (int)E}, act, residual, out, out_dtype,
-                  reinterpret_cast<uint16_t *>(ws), reinterpret_cast<float *>(ws + rows_bytes(pairs, I)), pairs};
+                  reinterpret_cast<uint16_t *>(ws), reinterpret_cast<float *>(ws + d.sums),
+                  reinterpret_cast<uint32_t *>(ws + d.counters), d.pairs};
   return launch_mlp(a, (hipStream_t)stream);
 }
 

@@ -30,13 +30,14 @@ struct Args {
 };
 
 // What a kernel takes its rows from and does with its sums is compiled in:
-//   ROWS  which rows a workgroup has (find; uniform over the workgroup) and where row m
+//   ROWS  which rows a workgroup has (find; uniform over the workgroup, with LDS that is free
+//         until it returns) and where row m
 //         of them lies in X (place, a row of `base`), `whole` rows of which there are;
 //   EPI   kPairs: weight rows of the two halves of the matrix alternate (0, N/2, 1, N/2 +
 //         1, ..), so that a gate and what it gates meet in one lane; kPlain: the sums are
 //         the outputs.  Else rows_out (row kernel) and tile_out (tiles) take them.
 struct SortedRows {
-  __device__ __forceinline__ RowTile find(const Args &p, int slot, int bm) const {
+  __device__ __forceinline__ RowTile find(const Args &p, int slot, int bm, void *) const {
     return find_tile(p.offsets, p.E, p.R, slot, bm);
   }
   __device__ __forceinline__ int64_t base(const RowTile &t) const { return t.row0; }
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(1024)
   extern __shared__ float part1[];  // [chunk][row of the workgroup][TR]
   int slot, block;
   if (!grid_item(p.grid, &slot, &block)) return;
-  const RowTile t = rows.find(p, slot, TR);
+  const RowTile t = rows.find(p, slot, TR, part1);
   if (t.rows <= 0) return;
   const int n0 = block * rows_wg;
   const int cols = min(rows_wg, p.N - n0);
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(64 * WV *KG, 2)
       shared[KG][NX * XB + NW * WB + (SL ? NS * SB * WV : 0)];
   int slot, block;
   if (!grid_item(p.grid, &slot, &block)) return;
-  const RowTile t = rows.find(p, slot, BM);
+  const RowTile t = rows.find(p, slot, BM, &shared[0][0]);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
