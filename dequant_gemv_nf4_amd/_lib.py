@@ -811,30 +811,58 @@ def _act(act, N):
 
 def _like(t, name, shape, dtypes):
     _need(t, name, dtypes)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, has {tuple(t.shape)}")
+
+
+# The conveniences below check what the caller gave and allocate the rest in the right
+# shape, so each operator's call is in one function, without a second round of checks: for
+# one token they take longer than the kernel.
+def _linear_sizes(codes, scales, X, bias, act, residual, out_dtype):
+    """(N, K, number of the act, leading sizes, columns of Y)."""
+    N, K = _mx_matrix(codes, scales)
+    number, cols = _act(act, N)
+    _need(X, "X", _BF16, (1, 2))
+    *lead, width = X.shape
+    if width != K:
+        raise ValueError(f"X has {width} columns, the matrix K = {K}")
+    if bias is not None:
+        _like(bias, "bias", (N,), _FLOATS)
+    if residual is not None:
+        _like(residual, "residual", (*lead, cols), (out_dtype,))
+    return N, K, number, lead, cols
+
+
+def _linear(codes, scales, N, K, X, lead, bias, number, residual, Y, Z, stream):
+    _run("nf4_mx_linear", (X, codes, scales, Y, bias, residual, Z),
+         (codes.data_ptr(), scales.data_ptr(), N, K, X.data_ptr(), lead[0] if lead else 1,
+          _addr(bias), 0 if bias is None else _DTYPE[bias.dtype], number, _addr(residual),
+          Y.data_ptr(), _DTYPE[Y.dtype], _addr(Z)), stream)
 
 
 def nf4_mx_linear(codes, scales, X, Y, bias=None, act=None, residual=None, Z=None, stream=None):
     """Y [M][N] ([M][N/2] for a gated act; fp32 or bf16) = act(X . dequant(codes, scales)^T +
     bias) + residual; Z bf16 [M][N], if given, receives what the activation is taken of."""
-    N, K = _mx_matrix(codes, scales)
-    number, cols = _act(act, N)
-    _need(X, "X", _BF16, (1, 2))
-    if X.shape[-1] != K:
-        raise ValueError(f"X has {X.shape[-1]} columns, the matrix K = {K}")
-    lead = tuple(X.shape[:-1])
-    _like(Y, "Y", lead + (cols,), _FLOATS)
-    if bias is not None:
-        _like(bias, "bias", (N,), _FLOATS)
-    if residual is not None:
-        _like(residual, "residual", lead + (cols,), (Y.dtype,))
+    _need(Y, "Y", _FLOATS)
+    N, K, number, lead, cols = _linear_sizes(codes, scales, X, bias, act, residual, Y.dtype)
+    _like(Y, "Y", (*lead, cols), _FLOATS)
     if Z is not None:
-        _like(Z, "Z", lead + (N,), _BF16)
-    _run("nf4_mx_linear", (X, codes, scales, Y, bias, residual, Z),
-         (codes.data_ptr(), scales.data_ptr(), N, K, X.data_ptr(), lead[0] if lead else 1,
-          _addr(bias), 0 if bias is None else _DTYPE[bias.dtype], number, _addr(residual),
-          Y.data_ptr(), _DTYPE[Y.dtype], _addr(Z)), stream)
+        _like(Z, "Z", (*lead, N), _BF16)
+    _linear(codes, scales, N, K, X, lead, bias, number, residual, Y, Z, stream)
+
+
+def mx_linear(codes, scales, X, bias=None, act=None, residual=None, out_dtype=torch.bfloat16,
+              keep_z=False, stream=None):
+    """act(X . dequant(codes, scales)^T + bias) + residual for any number of rows; with keep_z
+    (that, Z) for mx_linear_grad.  act: None, "relu", "silu", "gelu", "gelu_tanh", or "swiglu"
+    and "geglu", where the matrix's first half of rows gates its second."""
+    N, K, number, lead, cols = _linear_sizes(codes, scales, X, bias, act, residual, out_dtype)
+    if out_dtype not in _DTYPE:
+        raise TypeError(f"out_dtype is {out_dtype}, expected one of {_FLOATS}")
+    Y = _empty((*lead, cols), out_dtype, X.device, stream)
+    Z = _empty((*lead, N), torch.bfloat16, X.device, stream) if keep_z else None
+    _linear(codes, scales, N, K, X, lead, bias, number, residual, Y, Z, stream)
+    return (Y, Z) if keep_z else Y
 
 
 def mx_linear_grad_workspace_bytes(N, K, M):
@@ -845,59 +873,54 @@ def mx_linear_grad_workspace_bytes(N, K, M):
     return int(n)
 
 
-def nf4_mx_linear_grad(codes, scales, dY, Z, act, dX, dZ=None, dbias=None, workspace=None, stream=None):
-    """dX [M][K] (fp32 or bf16), dZ bf16 [M][N] and dbias fp32 [N] of nf4_mx_linear from dY
-    bf16 [M][N] ([M][N/2] gated) and the Z that it kept; N % 8 == 0.  Z and dZ may be None
-    without an activation.  workspace: uint8, mx_linear_grad_workspace_bytes(N, K, M)."""
+def _linear_grad_sizes(codes, scales, dY, Z, act):
     N, K = _mx_matrix(codes, scales)
     number, cols = _act(act, N)
     _need(dY, "dY", _BF16, (1, 2))
-    lead = tuple(dY.shape[:-1])
-    _like(dY, "dY", lead + (cols,), _BF16)
-    _like(dX, "dX", lead + (K,), _FLOATS)
+    *lead, width = dY.shape
+    if width != cols:
+        raise ValueError(f"dY has {width} columns, expected {cols}")
     if Z is not None or act is not None:
-        _like(Z, "Z", lead + (N,), _BF16)
-    if dZ is not None or act is not None:
-        _like(dZ, "dZ", lead + (N,), _BF16)
-    if dbias is not None:
-        _like(dbias, "dbias", (N,), _F32)
-    if workspace is not None:
-        _need(workspace, "workspace", _U8)
+        _like(Z, "Z", (*lead, N), _BF16)
+    return N, K, number, lead
+
+
+def _linear_grad(codes, scales, N, K, dY, lead, Z, number, dZ, dbias, dX, workspace, stream):
     _run("nf4_mx_linear_grad", (dY, codes, scales, Z, dX, dZ, dbias, workspace),
          (codes.data_ptr(), scales.data_ptr(), N, K, dY.data_ptr(), _addr(Z), number,
           lead[0] if lead else 1, _addr(dZ), _addr(dbias), dX.data_ptr(), _DTYPE[dX.dtype],
           _addr(workspace), 0 if workspace is None else workspace.numel()), stream)
 
 
-def mx_linear(codes, scales, X, bias=None, act=None, residual=None, out_dtype=torch.bfloat16,
-              keep_z=False, stream=None):
-    """act(X . dequant(codes, scales)^T + bias) + residual for any number of rows; with keep_z
-    (that, Z) for mx_linear_grad.  act: None, "relu", "silu", "gelu", "gelu_tanh", or "swiglu"
-    and "geglu", where the matrix's first half of rows gates its second."""
-    _need(codes, "codes", _U8, (2,))
-    _need(X, "X", _BF16, (1, 2))
-    N = codes.shape[0]
-    lead = tuple(X.shape[:-1])
-    Y = _empty(lead + (_act(act, N)[1],), out_dtype, X.device, stream)
-    Z = _empty(lead + (N,), torch.bfloat16, X.device, stream) if keep_z else None
-    nf4_mx_linear(codes, scales, X, Y, bias, act, residual, Z, stream)
-    return (Y, Z) if keep_z else Y
+def nf4_mx_linear_grad(codes, scales, dY, Z, act, dX, dZ=None, dbias=None, workspace=None, stream=None):
+    """dX [M][K] (fp32 or bf16), dZ bf16 [M][N] and dbias fp32 [N] of nf4_mx_linear from dY
+    bf16 [M][N] ([M][N/2] gated) and the Z that it kept; N % 8 == 0.  Z and dZ may be None
+    without an activation.  workspace: uint8, mx_linear_grad_workspace_bytes(N, K, M)."""
+    N, K, number, lead = _linear_grad_sizes(codes, scales, dY, Z, act)
+    _like(dX, "dX", (*lead, K), _FLOATS)
+    if dZ is not None or act is not None:
+        _like(dZ, "dZ", (*lead, N), _BF16)
+    if dbias is not None:
+        _like(dbias, "dbias", (N,), _F32)
+    if workspace is not None:
+        _need(workspace, "workspace", _U8)
+    _linear_grad(codes, scales, N, K, dY, lead, Z, number, dZ, dbias, dX, workspace, stream)
 
 
 def mx_linear_grad(codes, scales, dY, Z=None, act=None, out_dtype=torch.bfloat16, bias_grad=False,
                    stream=None):
     """(dX, dZ, dbias) of mx_linear; dbias is None unless bias_grad, dZ is dY itself without an
     activation.  The residual's gradient is dY."""
-    _need(codes, "codes", _U8, (2,))
-    _need(dY, "dY", _BF16, (1, 2))
-    N, K = codes.shape[0], 2 * codes.shape[1]
-    lead = tuple(dY.shape[:-1])
-    dX = _empty(lead + (K,), out_dtype, dY.device, stream)
-    dZ = None if act is None else _empty(lead + (N,), torch.bfloat16, dY.device, stream)
-    dbias = _empty((N,), torch.float32, dY.device, stream) if bias_grad else None
+    N, K, number, lead = _linear_grad_sizes(codes, scales, dY, Z, act)
+    if out_dtype not in _DTYPE:
+        raise TypeError(f"out_dtype is {out_dtype}, expected one of {_FLOATS}")
+    dev = dY.device
+    dX = _empty((*lead, K), out_dtype, dev, stream)
+    dZ = None if act is None else _empty((*lead, N), torch.bfloat16, dev, stream)
+    dbias = _empty((N,), torch.float32, dev, stream) if bias_grad else None
     need = _load().nf4_mx_linear_grad_workspace_bytes(N, K, lead[0] if lead else 1)
-    ws = _empty(need, torch.uint8, dY.device, stream) if need > 0 else None
-    nf4_mx_linear_grad(codes, scales, dY, Z, act, dX, dZ, dbias, ws, stream)
+    ws = _empty((need,), torch.uint8, dev, stream) if need > 0 else None
+    _linear_grad(codes, scales, N, K, dY, lead, Z, number, dZ, dbias, dX, ws, stream)
     return dX, dY if act is None else dZ, dbias
 
 
@@ -909,32 +932,42 @@ def mx_cross_entropy_workspace_bytes(N, K, M, grad=False):
     return int(n)
 
 
+def _loss_sizes(codes, scales, X, targets, dloss):
+    N, K = _mx_matrix(codes, scales)
+    _need(X, "X", _BF16, (2,))
+    M, width = X.shape
+    if width != K:
+        raise ValueError(f"X has {width} columns, the matrix K = {K}")
+    _like(targets, "targets", (M,), (torch.int64,))
+    if dloss is not None:
+        _like(dloss, "dloss", (M,), _F32)
+    return N, K, M
+
+
+def _loss(codes, scales, N, K, X, targets, M, loss, lse, dloss, dX, workspace, dev_status, stream):
+    _run("nf4_mx_cross_entropy", (X, codes, scales, targets, loss, lse, dloss, dX, workspace, dev_status),
+         (codes.data_ptr(), scales.data_ptr(), N, K, X.data_ptr(), targets.data_ptr(), M,
+          loss.data_ptr(), lse.data_ptr(), _addr(dloss), _addr(dX), 0 if dX is None else _DTYPE[dX.dtype],
+          _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(dev_status)), stream)
+
+
 def nf4_mx_cross_entropy(codes, scales, X, targets, loss, lse, dloss=None, dX=None, workspace=None,
                          dev_status=None, stream=None):
     """loss and lse fp32 [M] of the logits X . dequant(codes, scales)^T (X bf16 [M][K]) at
     targets int64 [M], negative ones ignored; with dloss fp32 [M] the gradient dX [M][K]
     (fp32 or bf16).  workspace: uint8, mx_cross_entropy_workspace_bytes(N, K, M, dX is given)."""
-    N, K = _mx_matrix(codes, scales)
-    _need(X, "X", _BF16, (2,))
-    M = X.shape[0]
-    if X.shape[1] != K:
-        raise ValueError(f"X has {X.shape[1]} columns, the matrix K = {K}")
-    _like(targets, "targets", (M,), (torch.int64,))
+    N, K, M = _loss_sizes(codes, scales, X, targets, dloss)
     _like(loss, "loss", (M,), _F32)
     _like(lse, "lse", (M,), _F32)
     if (dX is None) != (dloss is None):
         raise ValueError("dX and dloss are given together")
     if dX is not None:
         _like(dX, "dX", (M, K), _FLOATS)
-        _like(dloss, "dloss", (M,), _F32)
     if workspace is not None:
         _need(workspace, "workspace", _U8)
     if dev_status is not None:
         _need(dev_status, "dev_status", _I32)
-    _run("nf4_mx_cross_entropy", (X, codes, scales, targets, loss, lse, dloss, dX, workspace, dev_status),
-         (codes.data_ptr(), scales.data_ptr(), N, K, X.data_ptr(), targets.data_ptr(), M,
-          loss.data_ptr(), lse.data_ptr(), _addr(dloss), _addr(dX), 0 if dX is None else _DTYPE[dX.dtype],
-          _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(dev_status)), stream)
+    _loss(codes, scales, N, K, X, targets, M, loss, lse, dloss, dX, workspace, dev_status, stream)
 
 
 def mx_cross_entropy(codes, scales, X, targets, dloss=None, out_dtype=torch.bfloat16, stream=None,
@@ -942,16 +975,17 @@ def mx_cross_entropy(codes, scales, X, targets, dloss=None, out_dtype=torch.bflo
     """(loss, lse) of each row, or with the losses' gradients dloss (loss, lse, dX).  A target
     below 0 is ignored, and so is one of N or more; with check=True the latter raises (a host
     synchronisation, so not under capture)."""
-    N, K = _mx_matrix(codes, scales)
-    _need(X, "X", _BF16, (2,))
-    M, dev = X.shape[0], X.device
-    need = _load().nf4_mx_cross_entropy_workspace_bytes(N, K, M, int(dloss is not None))
+    N, K, M = _loss_sizes(codes, scales, X, targets, dloss)
+    if out_dtype not in _DTYPE:
+        raise TypeError(f"out_dtype is {out_dtype}, expected one of {_FLOATS}")
+    dev = X.device
+    need = _load().nf4_mx_cross_entropy_workspace_bytes(N, K, M, 0 if dloss is None else 1)
     loss = _empty((M,), torch.float32, dev, stream)
     lse = _empty((M,), torch.float32, dev, stream)
     dX = None if dloss is None else _empty((M, K), out_dtype, dev, stream)
-    ws = _empty(max(need, 0), torch.uint8, dev, stream)
+    ws = _empty((max(need, 0),), torch.uint8, dev, stream)
     status = _empty(1, torch.int32, dev, stream) if check else None
-    nf4_mx_cross_entropy(codes, scales, X, targets, loss, lse, dloss, dX, ws, status, stream)
+    _loss(codes, scales, N, K, X, targets, M, loss, lse, dloss, dX, ws, status, stream)
     if check:
         st = _read(status, stream)
         if st:
@@ -959,15 +993,29 @@ def mx_cross_entropy(codes, scales, X, targets, dloss=None, out_dtype=torch.bflo
     return (loss, lse) if dX is None else (loss, lse, dX)
 
 
-def _mlp_shape(codes1, scales1, codes2, scales2, act):
-    """(E, H, I) of an expert layer's matrices."""
+def _mlp_sizes(codes1, scales1, codes2, scales2, act, X, experts, weights, residual, out_dtype):
+    """(E, H, I, number of the act, T, topk) of an expert layer."""
     E, N1, H = _mx_matrix(codes1, scales1, ndim=3)
     E2, H2, I = _mx_matrix(codes2, scales2, ndim=3)
-    cols = _act(act, N1)[1]
-    if (E2, H2, I) != (E, H, cols):
+    number, cols = _act(act, N1)
+    if E2 != E or H2 != H or I != cols:
         raise ValueError(f"codes1 {tuple(codes1.shape)} with act {act!r} needs codes2 of [E={E}][H={H}]"
                          f"[I/2={cols // 2}], got {tuple(codes2.shape)}")
-    return E, H, I
+    _need(X, "X", _BF16, (2,))
+    T, width = X.shape
+    if width != H:
+        raise ValueError(f"X has {width} columns, the matrices H = {H}")
+    if T > MOE_MLP_MAX_T:
+        raise ValueError(f"moe_mlp takes up to {MOE_MLP_MAX_T} tokens, got {T}; sort the tokens (moe_sort) "
+                         "and use the grouped products")
+    _need(experts, "experts", (torch.int64,), (2,))
+    rows, topk = experts.shape
+    if rows != T:
+        raise ValueError(f"experts must be [T={T}][topk], has {tuple(experts.shape)}")
+    _like(weights, "weights", (T, topk), _F32)
+    if residual is not None:
+        _like(residual, "residual", (T, H), (out_dtype,))
+    return E, H, I, number, T, topk
 
 
 def moe_mlp_workspace_bytes(E, H, I, T, topk, act="swiglu"):
@@ -978,44 +1026,38 @@ def moe_mlp_workspace_bytes(E, H, I, T, topk, act="swiglu"):
     return int(n)
 
 
+def _mlp(codes1, scales1, codes2, scales2, sizes, X, experts, weights, residual, out, workspace, stream):
+    E, H, I, number, T, topk = sizes
+    _run("nf4_moe_mlp", (X, codes1, scales1, codes2, scales2, experts, weights, residual, out, workspace),
+         (codes1.data_ptr(), scales1.data_ptr(), codes2.data_ptr(), scales2.data_ptr(), E, H, I,
+          X.data_ptr(), experts.data_ptr(), weights.data_ptr(), T, topk, number, _addr(residual),
+          out.data_ptr(), _DTYPE[out.dtype], _addr(workspace),
+          0 if workspace is None else workspace.numel()), stream)
+
+
 def nf4_moe_mlp(codes1, scales1, codes2, scales2, X, experts, weights, out, act="swiglu", residual=None,
                 workspace=None, stream=None):
     """out [T][H] (fp32 or bf16) = sum_j weights[t][j] W2[e] act(W1[e] X[t]) + residual[t] with e =
     experts[t][j] (int64; none outside [0, E)), X bf16 [T][H], at most MOE_MLP_MAX_T tokens; W1
     packed [E][2 I][H] ([E][I][H] for an act that does not gate), W2 packed [E][H][I].
     workspace: uint8, moe_mlp_workspace_bytes(E, H, I, T, topk, act)."""
-    E, H, I = _mlp_shape(codes1, scales1, codes2, scales2, act)
-    _need(X, "X", _BF16, (2,))
-    T = X.shape[0]
-    if X.shape[1] != H:
-        raise ValueError(f"X has {X.shape[1]} columns, the matrices H = {H}")
-    _need(experts, "experts", (torch.int64,), (2,))
-    if experts.shape[0] != T:
-        raise ValueError(f"experts must be [T={T}][topk], has {tuple(experts.shape)}")
-    _like(weights, "weights", experts.shape, _F32)
-    _like(out, "out", (T, H), _FLOATS)
-    if residual is not None:
-        _like(residual, "residual", (T, H), (out.dtype,))
+    _need(out, "out", _FLOATS)
+    sizes = _mlp_sizes(codes1, scales1, codes2, scales2, act, X, experts, weights, residual, out.dtype)
+    _like(out, "out", X.shape, _FLOATS)
     if workspace is not None:
         _need(workspace, "workspace", _U8)
-    _run("nf4_moe_mlp", (X, codes1, scales1, codes2, scales2, experts, weights, residual, out, workspace),
-         (codes1.data_ptr(), scales1.data_ptr(), codes2.data_ptr(), scales2.data_ptr(), E, H, I,
-          X.data_ptr(), experts.data_ptr(), weights.data_ptr(), T, experts.shape[1], ACTS[act],
-          _addr(residual), out.data_ptr(), _DTYPE[out.dtype], _addr(workspace),
-          0 if workspace is None else workspace.numel()), stream)
+    _mlp(codes1, scales1, codes2, scales2, sizes, X, experts, weights, residual, out, workspace, stream)
 
 
 def moe_mlp(codes1, scales1, codes2, scales2, X, experts, weights, act="swiglu", residual=None,
             out_dtype=torch.bfloat16, stream=None):
     """A whole layer of experts for up to MOE_MLP_MAX_T tokens; see nf4_moe_mlp."""
-    E, H, I = _mlp_shape(codes1, scales1, codes2, scales2, act)
-    _need(X, "X", _BF16, (2,))
-    _need(experts, "experts", (torch.int64,), (2,))
-    if X.shape[0] > MOE_MLP_MAX_T:
-        raise ValueError(f"moe_mlp takes up to {MOE_MLP_MAX_T} tokens, got {X.shape[0]}; sort the tokens "
-                         "(moe_sort) and use the grouped products")
-    out = _empty((X.shape[0], H), out_dtype, X.device, stream)
-    need = _load().nf4_moe_mlp_workspace_bytes(E, H, I, ACTS[act], X.shape[0], experts.shape[1])
-    ws = _empty(max(need, 0), torch.uint8, X.device, stream)
-    nf4_moe_mlp(codes1, scales1, codes2, scales2, X, experts, weights, out, act, residual, ws, stream)
+    sizes = _mlp_sizes(codes1, scales1, codes2, scales2, act, X, experts, weights, residual, out_dtype)
+    if out_dtype not in _DTYPE:
+        raise TypeError(f"out_dtype is {out_dtype}, expected one of {_FLOATS}")
+    E, H, I, number, T, topk = sizes
+    out = _empty((T, H), out_dtype, X.device, stream)
+    need = _load().nf4_moe_mlp_workspace_bytes(E, H, I, number, T, topk)
+    ws = _empty((max(need, 0),), torch.uint8, X.device, stream)
+    _mlp(codes1, scales1, codes2, scales2, sizes, X, experts, weights, residual, out, ws, stream)
     return out

@@ -348,26 +348,30 @@ static int launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
 }
 
 // ------------------------------------------------- sums shared out over workgroups ----
-// A dense gradient has few tiles where rows are few, so the n are shared out: parts of the
-// sum in fp32, added in order by whoever takes them.
+// A dense gradient has few tiles where rows are few, so the n are shared out over the
+// workgroups of a tile: parts of the sum in fp32, added in order by whoever takes them.
+// Measured, us with the sum of the parts, M x N x K (splits):
+//   taken                    case                              others
+//   64 x 512                 2048 x 28672 x 4096 (2)     443   not shared out: 475
+//                            300 x 4096 x 14336 (2)       76   two K-groups: 80, 32 x 512: 88
+//   64 x 512, two K-groups   1000 x 13824 x 5120 (1)     173   one, shared out by two: 188
+//   32 x 256, two K-groups   512 x 4096 x 4096 (1)        30   64 x 512 (4): 42
+//                            77 x 13824 x 5120 (4)        33   64 x 512 (25): 54, (12): 34
+//                            32 x 28672 x 4096 (16)       26   32 x 512 (16): 33
+//   16 x 256, two            16 x 28672 x 4096 (16)       23   four (16): 26, two (8): 31
 struct DensePlan {
   int mf, wv, kg, splits;
 };
 static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
   const auto tiles = [&](int bm, int bk) { return (M + bm - 1) / bm * ((K + bk - 1) / bk); };
-  DensePlan d;
-  if (M > 32)
-    d = {4, 4, tiles(64, 512) >= 256 ? 1 : 2, 0};
-  else if (M > 16)
-    d = {2, 4, 2, 0};
-  else
-    d = {1, 2, 4, 0};
-  const int64_t n = tiles(16 * d.mf, 128 * d.wv);
-  // at least four stages of 64 n a group, and no more workgroups than two a CU
-  const int64_t most = (N + 256 * d.kg - 1) / (256 * d.kg), want = 512 / (n < 512 ? n : 512);
-  d.splits = (int)(want < most ? want : most);
-  if (d.splits < 1) d.splits = 1;
-  return d;
+  const int64_t large = tiles(64, 512);
+  if (large >= 256) return {4, 4, 1, large < 512 && N >= 1024 ? 2 : 1};
+  if (large >= 160) return {4, 4, 2, 1};
+  if (large >= 112) return {4, 4, 1, N >= 1024 ? 2 : 1};
+  const int mf = M > 16 ? 2 : 1;
+  // one workgroup a CU, and at least four stages of 64 n for each K-group
+  const int64_t want = 256 / tiles(16 * mf, 256), most = N / 512, n = want < most ? want : most;
+  return {mf, 2, 2, (int)(n > 1 ? n : 1)};
 }
 
 int grad_splits(int64_t M, int64_t N, int64_t K) { return plan_dense(M, N, K).splits; }
@@ -375,10 +379,9 @@ int grad_splits(int64_t M, int64_t N, int64_t K) { return plan_dense(M, N, K).sp
 int launch_grad_parts(const GradParts &g, hipStream_t s) {
   const DensePlan d = plan_dense(g.plan_M, g.plan_N, g.K);
   GradArgs a{g.codes, g.scales, g.dY, nullptr, g.parts, g.M, 1, (int)g.N, (int)g.K, {}, g.ld, d.splits, g.rescale};
-  if (d.mf == 4 && d.kg == 1) return launch_grad<4, 4, 1>(a, NF4_F32, s);
-  if (d.mf == 4) return launch_grad<4, 4, 2>(a, NF4_F32, s);
-  if (d.mf == 2) return launch_grad<2, 4, 2>(a, NF4_F32, s);
-  return launch_grad<1, 2, 4>(a, NF4_F32, s);
+  if (d.mf == 1) return launch_grad<1, 2, 2>(a, NF4_F32, s);
+  if (d.mf == 2) return launch_grad<2, 2, 2>(a, NF4_F32, s);
+  return d.kg == 1 ? launch_grad<4, 4, 1>(a, NF4_F32, s) : launch_grad<4, 4, 2>(a, NF4_F32, s);
 }
 
 // out = the parts' sum, in order
@@ -387,8 +390,9 @@ __global__ void __launch_bounds__(256)
     mx_parts_kernel(const float *__restrict__ parts, int splits, int64_t size, OUT *__restrict__ out) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= size) return;
-  f32x4_t v = *reinterpret_cast<const f32x4_t *>(parts + i);
-  for (int k = 1; k < splits; ++k) v += *reinterpret_cast<const f32x4_t *>(parts + k * size + i);
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int k = 0; k < splits; ++k) v += *reinterpret_cast<const f32x4_t *>(parts + k * size + i);
   store4<OUT>(out + i, 0, 4, v, true);
 }
 

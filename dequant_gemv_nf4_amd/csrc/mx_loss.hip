@@ -119,10 +119,10 @@ struct RowState {  // of a row of X, between pieces
   float *c, *sum, *rescale, *target_logit;
 };
 
-// A row's strips of a piece: 16 rows a workgroup, a thread for every 64th strip.  Writes
+// A row's strips of a piece: four rows a workgroup, a thread for every 256th strip.  Writes
 // the row's c and sum, the factor for what is summed so far, and for each strip how far
 // its exponents have to go down.  `loss` (after the last piece): the outputs.
-constexpr int kJoinThreads = 1024, kJoinRows = 16;
+constexpr int kJoinThreads = 1024, kJoinRows = 4;
 __global__ void __launch_bounds__(kJoinThreads)
     mx_loss_join_kernel(const Strip *__restrict__ strips, int n, int M, int first_piece, RowState rows,
                         uint8_t *__restrict__ down, const int64_t *__restrict__ targets, int64_t N,
@@ -133,7 +133,16 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int m = blockIdx.x * kJoinRows + r;
   Strip v{kNoMax, 0.f};
   if (m < M)
-    for (int i = share; i < n; i += kShares) v = join(v, strips[(int64_t)i * M + m]);
+    for (int i0 = share; i0 < n; i0 += 8 * kShares) {
+      Strip s[8];  // loads that do not wait for one another
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * kShares;
+        s[k] = i < n ? strips[(int64_t)i * M + m] : Strip{kNoMax, 0.f};
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v = join(v, s[k]);
+    }
   part[share][r] = v;
   __syncthreads();
 #pragma unroll
@@ -199,6 +208,7 @@ __global__ void __launch_bounds__(256)
     const f32x4_t *at = reinterpret_cast<const f32x4_t *>(parts + m * K + k);
     lo = at[0];
     hi = at[1];
+#pragma unroll 4
     for (int s = 1; s < splits; ++s) {
       at += M * K / 4;
       lo += at[0];
