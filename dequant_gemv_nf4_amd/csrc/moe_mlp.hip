@@ -258,8 +258,9 @@ __device__ __forceinline__ f32x4_t multiply(const RangeLoads<SVEC, PAIRS> &w, co
 // order, dealt out in runs of equal length: as many workgroups as the CUs hold, each with
 // one run, so that nothing depends on how the tokens chose.  In a tile the workgroup's
 // waves have a range of K each (several in turn, if K is longer than the waves' ranges),
-// whose rows of X stay in registers while the weights pass by; the next block is always
-// under way; the waves' sums meet in LDS once a block, in the two halves of `part` in turn.
+// whose rows of X stay in registers while the weights pass by; the next two blocks are
+// always under way; the waves' sums meet in LDS once a block, in the two halves of `part`
+// in turn.
 struct UpArgs {
   Args p;
   Routing r;
@@ -279,7 +280,9 @@ __device__ __forceinline__ int count_tiles(const Routing &r, const Masks &masks)
   return n;
 }
 
-template <int G, bool SVEC, bool PAIRS>
+// LONG: more than one pass.  (Compiled in: with loads of X behind a branch, the products
+// would wait for everything in flight.)
+template <int G, bool SVEC, bool PAIRS, bool LONG>
 __global__ void __launch_bounds__(512)
     moe_up_kernel(UpArgs a) {
   extern __shared__ float part[];  // [2][wave][row][16 G]
@@ -293,14 +296,16 @@ __global__ void __launch_bounds__(512)
   make_masks(r, masks);
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.ncounters; i += gridDim.x * blockDim.x)
     a.counters[i] = 0u;
-  const int64_t items = (int64_t)count_tiles(r, masks) * a.blocks;
-  const int64_t lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
-  const int passes = (p.K + waves * kRange - 1) / (waves * kRange);
+  // fp64 (fewer than 2^37 items, so exact but for the rounding of lo and hi, which is one for
+  // both sides of a border): a 64-bit division takes a microsecond
+  const double items = (double)count_tiles(r, masks) * a.blocks;
+  const int64_t lo = (int64_t)(items * blockIdx.x / gridDim.x), hi = (int64_t)(items * (blockIdx.x + 1) / gridDim.x);
+  const int passes = LONG ? (p.K + waves * kRange - 1) / (waves * kRange) : 1;
   const ActRows<PAIRS> out{r, a.act};
   float *half = part;
   int first = threadIdx.x;  // of a block's outputs: another wave has them each time
   for (int64_t at = lo; at < hi;) {
-    const int tile = (int)(at / a.blocks), b0 = (int)(at - (int64_t)tile * a.blocks);
+    const int tile = (int)((double)at / a.blocks), b0 = (int)(at - (int64_t)tile * a.blocks);
     const int b1 = (int)(hi - at < a.blocks - b0 ? b0 + (hi - at) : a.blocks);
     at += b1 - b0;
     __syncthreads();  // the last tile's state has been read
@@ -309,39 +314,51 @@ __global__ void __launch_bounds__(512)
     const __amdgpu_buffer_rsrc_t xrs = buffer(p.X, (int64_t)r.T * p.K * 2);
     const int xrow = (l16 < t.rows ? st.tokens[l16] : 0) * p.K * 2;
     const int kfirst = wave * kRange;
-    RangeLoads<SVEC, PAIRS> w[G];
-    const auto load = [&](RangeLoads<SVEC, PAIRS> &to, int b, int g, int k0) __attribute__((always_inline)) {
+    RangeLoads<SVEC, PAIRS> w[2][G];
+    const auto load = [&](RangeLoads<SVEC, PAIRS> &to, int b, int g, int pass) __attribute__((always_inline)) {
       const int n0 = b * 16 * G, cols = b < b1 ? min(16 * G, p.N - n0) : 0;  // past the run the buffers are empty
       const int col = PAIRS ? n0 >> 1 : n0, wrows = PAIRS && cols > 0 ? (p.N + cols) >> 1 : cols;
-      to.load(ce + (int64_t)col * kc, se + (int64_t)col * kb, wrows, g * 16, p.N, p.K, k0);
+      to.load(ce + (int64_t)col * kc, se + (int64_t)col * kb, wrows, g * 16, p.N, p.K, kfirst + pass * waves * kRange);
     };
+    const auto advance = [&](int &b, int &pass) __attribute__((always_inline)) {
+      if (++pass == passes) {
+        pass = 0;
+        ++b;
+      }
+    };
+    int b = b0, pass = 0, fb = b0, fpass = 0;  // this step, and the one whose weights are asked for
 #pragma unroll
-    for (int g = 0; g < G; ++g) load(w[g], b0, g, kfirst);
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) load(w[i][g], fb, g, fpass);
+      advance(fb, fpass);
+    }
     u32x4_t x[4][4];
     load_range(x, xrs, l16 < t.rows, xrow, p.K, kfirst);
     if ((int)threadIdx.x < t.rows) st.weight[threadIdx.x] = row_weight(r, st.tokens[threadIdx.x], t.e);
-    for (int b = b0; b < b1; ++b) {
-      const int n0 = b * 16 * G;
-      f32x4_t acc[G];
+    f32x4_t acc[G];
 #pragma unroll
-      for (int g = 0; g < G; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      for (int pass = 0; pass < passes; ++pass) {
-        const int k0 = kfirst + pass * waves * kRange;
-        const bool last = pass + 1 == passes;
-        const int k1 = last ? kfirst : k0 + waves * kRange;
+    for (int g = 0; g < G; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const auto step = [&](RangeLoads<SVEC, PAIRS> (&now)[G]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          acc[g] = multiply(w[g], x, acc[g], p.K, k0);
-          load(w[g], last ? b + 1 : b, g, k1);
-          __builtin_amdgcn_sched_barrier(0);  // else the loads are moved to where they are needed
-        }
-        if (passes > 1) load_range(x, xrs, l16 < t.rows, xrow, p.K, k1);
+      for (int g = 0; g < G; ++g) {
+        acc[g] = multiply(now[g], x, acc[g], p.K, kfirst + pass * waves * kRange);
+        load(now[g], fb, g, fpass);
+        __builtin_amdgcn_sched_barrier(0);  // else the loads are moved to where they are needed
       }
+      advance(fb, fpass);
+      const int n0 = b * 16 * G;
+      const bool last = pass + 1 == passes;
+      advance(b, pass);
+      if constexpr (LONG) load_range(x, xrs, l16 < t.rows, xrow, p.K, kfirst + pass * waves * kRange);
+      if (!last) return;
       if (l16 < t.rows) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
           *reinterpret_cast<f32x4_t *>(half + (wave * 16 + l16) * (16 * G) + g * 16 + q * 4) = acc[g];
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       __syncthreads();
       constexpr int W = PAIRS ? 8 : 4, quads = 16 * G / W;
       for (int i = first; i < t.rows * quads; i += blockDim.x) {
@@ -360,6 +377,12 @@ __global__ void __launch_bounds__(512)
       }
       half = half == part ? part + waves * 16 * 16 * G : part;
       first = first < 64 ? first + blockDim.x - 64 : first - 64;
+    };
+    while (true) {
+      step(w[0]);
+      if (b >= b1) break;
+      step(w[1]);
+      if (b >= b1) break;
     }
   }
 }
@@ -597,27 +620,32 @@ static bool few_rows(int64_t T, int64_t topk, int64_t E) { return T * topk <= 8 
 // the tiles that there can be
 static int64_t tiles_of(int64_t pairs, int64_t E) { return slots_for(pairs, E, true, 16); }
 
+template <int G, bool PAIRS>
+static int launch_up_as(const UpArgs &u, bool svec, bool longer, dim3 grid, dim3 threads, size_t lds, hipStream_t s) {
+  if (svec && !longer)
+    hipLaunchKernelGGL((moe_up_kernel<G, true, PAIRS, false>), grid, threads, lds, s, u);
+  else if (svec)
+    hipLaunchKernelGGL((moe_up_kernel<G, true, PAIRS, true>), grid, threads, lds, s, u);
+  else if (!longer)
+    hipLaunchKernelGGL((moe_up_kernel<G, false, PAIRS, false>), grid, threads, lds, s, u);
+  else
+    hipLaunchKernelGGL((moe_up_kernel<G, false, PAIRS, true>), grid, threads, lds, s, u);
+  return launch_status(hipGetLastError());
+}
 template <bool PAIRS>
 static int launch_up_few(const MlpArgs &a, int ncounters, hipStream_t s) {
   const int ranges = (a.H + kRange - 1) / kRange, waves = ranges < 8 ? ranges : 8;
   const int hold = 256 * (8 / waves);
   const int64_t tiles = tiles_of(a.pairs, a.E);
-  // blocks of one group where four to a block would leave CUs without one
-  const int g = tiles * ((a.N1 + 63) / 64) >= hold ? 4 : 1, blocks = (a.N1 + 16 * g - 1) / (16 * g);
+  // blocks of one group where two to a block would leave CUs without one
+  const int g = tiles * ((a.N1 + 31) / 32) >= hold ? 2 : 1, blocks = (a.N1 + 16 * g - 1) / (16 * g);
   const dim3 grid((unsigned)(tiles * blocks < hold ? tiles * blocks : hold)), threads(64 * waves);
   const size_t lds = (size_t)waves * 16 * 16 * g * 4 * 2;
   const UpArgs u{{a.codes1, a.scales1, a.X, nullptr, a.rows, a.pairs, a.E, a.N1, a.H, {}}, a.r, blocks, a.act,
                  a.counters, ncounters};
   const bool svec = a.H % 128 == 0 && aligned_to(a.scales1, 4);
-  if (g == 4 && svec)
-    hipLaunchKernelGGL((moe_up_kernel<4, true, PAIRS>), grid, threads, lds, s, u);
-  else if (g == 4)
-    hipLaunchKernelGGL((moe_up_kernel<4, false, PAIRS>), grid, threads, lds, s, u);
-  else if (svec)
-    hipLaunchKernelGGL((moe_up_kernel<1, true, PAIRS>), grid, threads, lds, s, u);
-  else
-    hipLaunchKernelGGL((moe_up_kernel<1, false, PAIRS>), grid, threads, lds, s, u);
-  return launch_status(hipGetLastError());
+  return g == 2 ? launch_up_as<2, PAIRS>(u, svec, ranges > waves, grid, threads, lds, s)
+                : launch_up_as<1, PAIRS>(u, svec, ranges > waves, grid, threads, lds, s);
 }
 
 // How the second product is dealt out: groups of 16 columns a workgroup, and workgroups that
@@ -672,11 +700,13 @@ static int launch_few(const MlpArgs &a, hipStream_t s) {
 template <class ROWS, class EPI, bool F32, bool B16>
 static int launch_tiles(Product<ROWS, EPI, F32, B16> p) {
   const Args &a = p.a;
-  const int64_t rows = (a.R + a.E - 1) / a.E;
   const auto tiles = [&](int bm, int bn) { return slots_for(a.R, a.E, true, bm) * ((a.N + bn - 1) / bn); };
-  if (rows > 16 && tiles(32, 128) >= 384) return p.template tile<2, 2, 4, 2, 2, 1>();
-  if (rows > 8) return p.template tile<2, 1, 4, 4, 4, 1>();
-  return p.template tile<1, 1, 4, 4, 4, 1>();
+  // 32 x 128, us, first and second product of 64 tokens, 8 experts of 4096 x 14336: 64 k a
+  // stage 118 and 66, 128 k (one workgroup a CU) 129 and 55; 32 x 64 137 and 67, 64 x 128 128
+  // and 76
+  if (tiles(32, 128) >= 768) return p.template tile<2, 2, 4, 2, 2, 1>();
+  if (tiles(32, 128) >= 256) return p.template tile<2, 2, 4, 4, 4, 1>();
+  return p.template tile<2, 1, 4, 4, 4, 1>();
 }
 
 static int launch_mlp(const MlpArgs &a, hipStream_t s) {
