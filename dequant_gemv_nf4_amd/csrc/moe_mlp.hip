@@ -463,44 +463,36 @@ __global__ void __launch_bounds__(512)
   const auto add = [&](const Unit &v, int m0, int tok, int g, f32x4_t s) __attribute__((always_inline)) {
     if (m0 + l16 < v.rows) *reinterpret_cast<f32x4_t *>(own + tok * kCols + g * 16 + q * 4) += s;
   };
-  RangeLoads<SVEC, false> w[G > 1 ? 2 : 1];
-  u32x4_t x[2][4][4];
-  const auto turn = [&](u32x4_t (&now)[4][4], u32x4_t (&next)[4][4], const Unit &v, const Unit &after)
-                        __attribute__((always_inline)) {
+  // The weights of the next unit are under way while this one's are multiplied, each group's
+  // asked for when its registers are free; the rows' values follow at the unit's end.
+  RangeLoads<SVEC, false> w[G];
+  u32x4_t x[4][4];
+  const int u0 = split * waves + wave;
+  Unit v = unit(u0);
+#pragma unroll
+  for (int g = 0; g < G; ++g) load_w(w[g], v, g);
+  load_x(x, v, 0);
+  for (int u = u0; u < units; u += step) {
+    const Unit after = unit(u + step);
     const int tok = token(v, 0);
-    load_x(next, after, 0);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      RangeLoads<SVEC, false> one;
-      RangeLoads<SVEC, false> &use = G > 1 ? w[g & 1] : one;
-      if constexpr (G == 1) one = w[0];
-      if (g + 1 < G)
-        load_w(w[(g + 1) & 1], v, g + 1);
-      else
-        load_w(w[0], after, 0);
+      add(v, 0, tok, g, multiply(w[g], x, f32x4_t{0.f, 0.f, 0.f, 0.f}, p.K, v.k0));
+      load_w(w[g], after, g);
       __builtin_amdgcn_sched_barrier(0);  // else the loads are moved to where they are needed
-      add(v, 0, tok, g, multiply(use, now, f32x4_t{0.f, 0.f, 0.f, 0.f}, p.K, v.k0));
     }
     for (int m0 = 16; m0 < v.rows; m0 += 16) {  // more rows than a tile: the weights once more
       const int more = token(v, m0);
-      load_x(now, v, m0);
+      load_x(x, v, m0);
 #pragma unroll 1
       for (int g = 0; g < G; ++g) {
         RangeLoads<SVEC, false> again;
         load_w(again, v, g);
-        add(v, m0, more, g, multiply(again, now, f32x4_t{0.f, 0.f, 0.f, 0.f}, p.K, v.k0));
+        add(v, m0, more, g, multiply(again, x, f32x4_t{0.f, 0.f, 0.f, 0.f}, p.K, v.k0));
       }
     }
-  };
-  const int u0 = split * waves + wave;
-  Unit a = unit(u0);
-  load_w(w[0], a, 0);
-  load_x(x[0], a, 0);
-  for (int u = u0; u < units; u += 2 * step) {
-    const Unit b = unit(u + step);
-    turn(x[0], x[1], a, b);
-    a = unit(u + 2 * step);
-    turn(x[1], x[0], b, a);
+    v = after;
+    load_x(x, v, 0);
   }
   __syncthreads();
   const auto put = [&](int t, int c, f32x4_t v) __attribute__((always_inline)) {
