@@ -2,12 +2,18 @@
 // vocabulary, and its gradient in X, without the logits in memory (gfx950):
 //   l[m][n] = sum_k X[m][k] v(n,k);  lse = log sum_n exp l;  loss = lse - l[target]
 //   dX[m][k] = dloss[m] (sum_n exp(l - lse) v(n,k) - v(target,k))
+//            = dloss[m] (sum_(n != target) exp(l - lse) v(n,k) - (1 - p) v(target,k)),
+// p the target's probability.  The second form is the one computed, with 1 - p as the others'
+// sum over the whole: for a token that the model predicts well both terms of the first are
+// nearly one, and the gradient would be what their rounding leaves.  The loss is, for such a
+// token, log(1 + the others' sum / the target's).
 //
 // The vocabulary goes in pieces.  Of each piece
 //  1. the product's tiles (mx_product.h) take exp2(l log2(e) - c) of their logits, c a whole
 //     number, at least the strip's largest exponent and the row's so far; the strip's c and
 //     sum stay, and for the gradient the values, at most 1, in bf16 (so each has its full
-//     relative precision however far below the row's maximum its strip lies);
+//     relative precision however far below the row's maximum its strip lies); the target's
+//     is left out of both, its logit is kept;
 //  2. a row's strips meet in the row's new c and sum; strips with a smaller c are moved to
 //     it by a subtraction in the exponents of their values;
 //  3. the values' product with the piece's matrix (mx_grad.hip) is added to the row's sum
@@ -74,7 +80,10 @@ struct LossOut {
         for (int k = 0; k < NF; ++k)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (k * 16 + q * 4 + i == at) target_logit[row] = l[k][i];
+            if (k * 16 + q * 4 + i == at) {
+              target_logit[row] = l[k][i];
+              l[k][i] = -__builtin_inff();
+            }
       }
       float sum = 0.f;
 #pragma unroll
@@ -115,8 +124,8 @@ __device__ __forceinline__ Strip join(Strip a, Strip b) {
   return {c, a.sum * __builtin_amdgcn_exp2f(a.c - c) + b.sum * __builtin_amdgcn_exp2f(b.c - c)};
 }
 
-struct RowState {  // of a row of X, between pieces
-  float *c, *sum, *rescale, *target_logit;
+struct RowState {  // of a row of X, between pieces; sum: without the target
+  float *c, *sum, *rescale, *target_logit, *total;
 };
 
 // A row's strips of a piece: four rows a workgroup, a thread for every 256th strip.  Writes
@@ -164,9 +173,14 @@ __global__ void __launch_bounds__(kJoinThreads)
     rows.rescale[m] = __builtin_amdgcn_exp2f(before - all.c);
     if (loss) {
       const int64_t t = targets[m];
-      const float total = __builtin_fmaf(__builtin_amdgcn_logf(all.sum), kLn2, all.c * kLn2);
-      lse[m] = total;
-      loss[m] = t >= 0 && t < N ? total - rows.target_logit[m] : 0.f;
+      const bool counts = t >= 0 && t < N;
+      const float l = counts ? rows.target_logit[m] : 0.f;
+      const float own = counts ? __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2e, -all.c)) : 0.f;
+      const float total = all.sum + own;
+      const float log = __builtin_fmaf(__builtin_amdgcn_logf(total), kLn2, all.c * kLn2);
+      rows.total[m] = total;
+      lse[m] = log;
+      loss[m] = !counts ? 0.f : all.sum < own ? log1pf(all.sum / own) : log - l;
       if (t >= N && status) atomicOr(status, NF4_LOSS_BAD_TARGET);
     }
   }
@@ -190,11 +204,11 @@ __global__ void __launch_bounds__(256)
   *at = __builtin_elementwise_sub_sat(v, s);
 }
 
-// dX = (sum of the parts / the row's sum - the target's row) * dloss
+// dX = (sum of the parts - the others' sum * the target's row) / the row's whole sum * dloss
 template <typename OUT>
 __global__ void __launch_bounds__(256)
     mx_loss_grad_kernel(const float *__restrict__ parts, int splits, int64_t M, int K, const float *__restrict__ sum,
-                        const int64_t *__restrict__ targets, int64_t N, const float *__restrict__ dloss,
+                        const float *__restrict__ total, const int64_t *__restrict__ targets, int64_t N, const float *__restrict__ dloss,
                         const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                         OUT *__restrict__ dX) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // 8 columns
@@ -216,9 +230,9 @@ __global__ void __launch_bounds__(256)
     }
     const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + t * (K >> 1) + (k >> 1));
     const u32x4_t v = decode8(w, scale_of(scales[t * (K >> 5) + (k >> 5)]));
-    const float inv = 1.f / sum[m], d = dloss[m];
-    lo = (lo * inv - f32x4_t{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])}) * d;
-    hi = (hi * inv - f32x4_t{bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3])}) * d;
+    const float inv = 1.f / total[m], rest = sum[m], d = dloss[m];
+    lo = (lo - rest * f32x4_t{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])}) * inv * d;
+    hi = (hi - rest * f32x4_t{bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3])}) * inv * d;
   }
   store4<OUT>(dX + m * K, k, K, lo, true);
   store4<OUT>(dX + m * K, k + 4, K, hi, true);
@@ -229,7 +243,7 @@ __global__ void mx_loss_clear_kernel(int32_t *status) { *status = 0; }
 // Rows and columns of a piece, and what of the workspace is whose.
 struct LossPlan {
   int64_t rows, cols, ld, splits;
-  int64_t p, parts, strips, down, state, bytes;  // offsets; state: 4 floats a row
+  int64_t p, parts, strips, down, state, bytes;  // offsets; state: 5 floats a row
 };
 // Up to kLossRows rows at a time, and as many columns as keep the values under kLossBytes,
 // which with the piece of the matrix fits the 256 MB of the last cache; without the values,
@@ -255,7 +269,7 @@ static LossPlan loss_plan(int64_t N, int64_t K, int64_t M, bool grad) {
   d.parts = take(d.splits * d.rows * K * 4);
   d.strips = take(n * d.rows * (int64_t)sizeof(Strip));
   d.down = take(grad ? n * d.rows : 0);
-  d.state = take(4 * d.rows * 4);
+  d.state = take(5 * d.rows * 4);
   d.bytes = at;
   return d;
 }
@@ -264,7 +278,7 @@ static int loss_rows(const LossPlan &d, const uint8_t *codes, const uint8_t *sca
                      const uint16_t *X, const int64_t *targets, int64_t M, float *loss, float *lse,
                      const float *dloss, void *dX, int out_dtype, uint8_t *ws, int32_t *status, hipStream_t s) {
   float *const state = reinterpret_cast<float *>(ws + d.state);
-  const RowState rows{state, state + M, state + 2 * M, state + 3 * M};
+  const RowState rows{state, state + M, state + 2 * M, state + 3 * M, state + 4 * M};
   Strip *const strips = reinterpret_cast<Strip *>(ws + d.strips);
   uint16_t *const P = dX ? reinterpret_cast<uint16_t *>(ws + d.p) : nullptr;
   uint8_t *const down = dX ? ws + d.down : nullptr;
@@ -298,10 +312,10 @@ static int loss_rows(const LossPlan &d, const uint8_t *codes, const uint8_t *sca
   const int splits = (int)d.splits;
   if (out_dtype == NF4_F32)
     hipLaunchKernelGGL((mx_loss_grad_kernel<float>), dim3(blocks), dim3(256), 0, s, parts, splits, M, (int)K,
-                       rows.sum, targets, N, dloss, codes, scales, static_cast<float *>(dX));
+                       rows.sum, rows.total, targets, N, dloss, codes, scales, static_cast<float *>(dX));
   else
     hipLaunchKernelGGL((mx_loss_grad_kernel<uint16_t>), dim3(blocks), dim3(256), 0, s, parts, splits, M, (int)K,
-                       rows.sum, targets, N, dloss, codes, scales, static_cast<uint16_t *>(dX));
+                       rows.sum, rows.total, targets, N, dloss, codes, scales, static_cast<uint16_t *>(dX));
   return launch_status(hipGetLastError());
 }
 

@@ -498,7 +498,8 @@ int nf4_mx_linear_grad(const uint8_t *codes, const uint8_t *scales, int64_t N, i
  *    same time.  The function returns -1 for sizes that the call refuses.
  * The sums over k are the products'; exp is within 2^-20 of its value (|l| at most 64, in
  * proportion beyond), sums of it are fp32, and the gradient takes exp(l - lse) in bf16, each
- * rounded once.
+ * rounded once, but for the target, whose factor 1 - exp(l - lse) is the others' sum in fp32:
+ * the gradient of a well predicted token keeps its relative precision, and so does its loss.
  * Alignment: codes, X and dX 16 bytes, targets 8.  Errors: NF4_ERANGE for M < 1, M >= 2^26,
  * N > 2^23 or a missing or short workspace, otherwise as nf4_mx_gemm.
  */

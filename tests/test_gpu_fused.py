@@ -388,6 +388,36 @@ def test_loss_rising_maximum():
         inside(dx, want[4], want[5] + 1e-36, "dX")
 
 
+def test_loss_of_well_predicted_tokens():
+    """Targets of probabilities from next to nothing up to 1 - 3e-5: the loss and the gradient
+    are as precise as they are small (the target's own value is not rounded)."""
+    m, n, k = 24, 5000, 64
+    codes, scales = matrix(n, k, 1)
+    v = values(codes, scales)
+    targets = torch.arange(m, device=DEV) * 200 + 7
+    row = v[targets]
+    x = (row * (torch.linspace(8, 30, m, device=DEV) / (row * row).sum(1)).unsqueeze(1)).to(BF)
+    dloss = torch.ones(m, device=DEV)
+    loss, lse, dx = nf4.mx_cross_entropy(codes, scales, x, targets, dloss, out_dtype=F32)
+    l = x.double() @ v.t().contiguous()
+    dl = ((k + 8) * 2.0 ** -24 * (x.double().abs() @ v.abs().t().contiguous())).amax(1)
+    others = l.clone()
+    others[torch.arange(m), targets] = float("-inf")
+    rest = torch.logsumexp(others, 1) - l.gather(1, targets.unsqueeze(1)).squeeze(1)   # log of the ratio
+    want = torch.nn.functional.softplus(rest)
+    assert float(want.min()) < 1e-4 and int((want < 0.1).sum()) > 5
+    # the ratio of two sums of exp, each off by e relative to itself
+    e = 2 * dl + 2 * (2.0 ** -20 * (1 + l.abs().amax(1) / 64) + 2.0 ** -17)
+    # where the ratio is below 1 it is taken as such, else as a difference of logs
+    tol = torch.where(rest < -0.01, e * want + 2.0 ** -22 * want, e + 2.0 ** -21 * lse.double().abs())
+    inside(loss, want, tol, "loss")
+    p = torch.softmax(others, 1)
+    share = torch.sigmoid(rest).unsqueeze(1)                  # 1 - p of the target
+    want = share * (p @ v - row)
+    size = share * (p @ v.abs() + row.abs())
+    inside(dx, want, size * (2.0 ** -8 + (n + 40) * 2.0 ** -24 + 2 * e.unsqueeze(1)), "dX")
+
+
 def test_loss_not_finite():
     codes, scales = matrix(5000, 64, 1)
     x = rand((8, 64), 2)
