@@ -280,6 +280,11 @@ __device__ __forceinline__ int count_tiles(const Routing &r, const Masks &masks)
   return n;
 }
 
+// Bound by memory, and by the 8 us that it takes to route, to fill and to end: experts of 28672
+// x 4096, 16 rows of 8 experts each 91 us (5.5 TB/s), two experts of one token 31 (4.0), 19 x 8
+// slots of 128 experts of 1536 x 2048 37.  With static shares of the tiles that there could
+// be, empty ones among them, the first took 126; weights asked for one block ahead where
+// the compiler moved the loads down to their use, 29 of the two experts' became 33.
 // LONG: more than one pass.  (Compiled in: with loads of X behind a branch, the products
 // would wait for everything in flight.)
 template <int G, bool SVEC, bool PAIRS, bool LONG>
@@ -391,6 +396,11 @@ __global__ void __launch_bounds__(512)
 // output for all tokens (G groups of 16, for which a range of the rows is loaded once).  A unit is a range of an expert's I; the units go in turn to the
 // waves of the `splits` workgroups that share the columns, and a wave adds its units, in
 // order, into sums of its own in LDS.
+// Bound by memory (rows' pieces of 256 bytes a wave: 4.9 TB/s) and 7 us of start, fill and end:
+// experts of 4096 x 14336, 16 rows of 8 59 us, two experts of one token 22-23; about 90 of 128 of
+// 2048 x 768 28.  (Built and slower: the items of the first product with a last workgroup
+// that adds up, 70, 24 and 33, since few workgroups are last for all columns; the sums
+// written back by a fence of the whole cache, 76, 23 and 62.)
 struct ActiveExperts {
   Masks masks;
   uint16_t expert[NF4_MOE_MAX_E];
@@ -654,8 +664,8 @@ static DownPlan down_plan(int64_t H, int64_t I, int64_t tiles) {
     return n < most ? n : most;
   };
   // G = 4 from where every wave of the chip has a unit and a half, us against G = 1: 2 experts
-  // of 4096 x 14336 (56 units) 21.3, 24.0; of 4096 x 4096 (16) 14.9, 9.1; 8 of 128 of 2048 x
-  // 768 (16) 14.8, 9.8, about 90 of them 29, 32
+  // of 4096 x 14336 (56 units) 22.7, 24.1; of 4096 x 8192 (32) 15.1, 15.3; of 4096 x 4096 (16)
+  // 13.4, 9.0; 8 of 128 of 2048 x 768 (16) 12.7, 7.9, about 90 of them 28, 34
   const int64_t b4 = (H + 63) / 64;
   d.g = 2 * units * (b4 < 256 ? b4 : 256) >= 3 * 8 * 256 ? 4 : 1;
   d.blocks = (int)((H + 16 * d.g - 1) / (16 * d.g));

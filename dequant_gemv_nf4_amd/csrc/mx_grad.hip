@@ -384,7 +384,8 @@ int launch_grad_parts(const GradParts &g, hipStream_t s) {
   return d.kg == 1 ? launch_grad<4, 4, 1>(a, NF4_F32, s) : launch_grad<4, 4, 2>(a, NF4_F32, s);
 }
 
-// out = the parts' sum, in order
+// out = the parts' sum, in order.  Bound by memory: two parts of 2048 x 4096 12.5 us (6.7 TB/s,
+// from the caches); four of 77 x 5120 4.
 template <typename OUT>
 __global__ void __launch_bounds__(256)
     mx_parts_kernel(const float *__restrict__ parts, int splits, int64_t size, OUT *__restrict__ out) {
@@ -401,6 +402,8 @@ __global__ void __launch_bounds__(256)
 // unrounded values.  A thread has four columns (of both halves, gated) and every
 // `blockDim.y`-th row of its workgroup's, so that with `bias` a workgroup has whole columns
 // and the sums are added in one order.
+// Bound by memory: 2048 rows of 28672, gated, 61 us (4.8 TB/s); 77 rows of 13824 with the column
+// sums 5-6, mostly start and the sums' way through LDS.
 template <int LANES, bool GATED>
 __global__ void __launch_bounds__(1024)
     mx_act_grad_kernel(const uint16_t *__restrict__ dY, const uint16_t *__restrict__ Z, int64_t M, int N,

@@ -21,6 +21,11 @@
 // So the logits are computed once, 4 M N K operations with the gradient where a second pass
 // over them takes 6.  Last, the sums are divided by the row's, the target's row is taken
 // off, and dloss applied.
+// Bound by the products (the exponentials run beside another workgroup's matrix
+// instructions).  Of 128256 x 4096: 1000 rows 750-780 us (1.35-1.4 PFLOP/s); 2047 rows with the
+// gradient, four pieces, 3.4-3.5 ms (1.23-1.26): 390-410 us a piece the logits, 390-450 their
+// product back, 9 the join, 13-17 moving strips (most of it in the first piece, where the
+// maximum is found).  32000 x 4096, 5 rows: 14.5 (4.8 TB/s) and 3.9.
 #include "mx_grad.h"
 #include "mx_product.h"
 
