@@ -393,9 +393,10 @@ __global__ void __launch_bounds__(512)
 }
 
 // Second product and the sum over a token's experts: a workgroup owns 16 G columns of the
-// output for all tokens (G groups of 16, for which a range of the rows is loaded once).  A unit is a range of an expert's I; the units go in turn to the
-// waves of the `splits` workgroups that share the columns, and a wave adds its units, in
-// order, into sums of its own in LDS.
+// output for all tokens (G groups of 16, for which a range of the rows is loaded once).  A
+// unit is a range of an expert's I; the units go in turn to the waves of the `splits`
+// workgroups that share the columns, and a wave adds its units, in order, into sums of its
+// own in LDS.
 // Bound by memory (rows' pieces of 256 bytes a wave: 4.9 TB/s) and 7 us of start, fill and end:
 // experts of 4096 x 14336, 16 rows of 8 59 us, two experts of one token 22-23; about 90 of 128 of
 // 2048 x 768 28.  (Built and slower: the items of the first product with a last workgroup

@@ -7,8 +7,7 @@
 // Bound as the plain products are, the epilogue hides behind another workgroup's products:
 // 28672 x 4096, gated, M = 1: 14.2 us (4.4 TB/s, without: 13.3); M = 1021 with z kept: 190-200
 // (1.2-1.26 PFLOP/s); 4096 x 4096 with residual, M = 1: 5.4; 333 x 13824 x 5120 with bias and
-// gelu in fp32: 76 (0.62 PFLOP/s: 648 tiles of 64 x 128, of which the chip holds 512, and
-// LDS reads, one for every two matrix instructions there).
+// gelu in fp32: 62 (0.76 PFLOP/s: 432 tiles of 96 x 128, of which the chip holds 512).
 #include "mx_act.h"
 #include "mx_product.h"
 

@@ -199,12 +199,12 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // Values of strips that are to go down: their exponents less `down`, at least 0.
 __global__ void __launch_bounds__(256)
-    mx_loss_down_kernel(const uint8_t *__restrict__ down, int n, int shift, uint16_t *__restrict__ P, int64_t ld) {
+    mx_loss_down_kernel(const uint8_t *__restrict__ down, int n, int width, uint16_t *__restrict__ P, int64_t ld) {
   typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
   const int64_t m = blockIdx.y;
   const int i = blockIdx.x * 256 + threadIdx.x;  // 8 columns
-  const int strip = i * 8 >> shift;
-  if (strip >= n) return;
+  const int strip = i * 8 / width;  // (a multiple of 16 columns)
+  if (strip >= n || i * 8 >= ld) return;
   const uint32_t d = down[m * n + strip];
   if (d == 0) return;
   u16x8 *at = reinterpret_cast<u16x8 *>(P + m * ld) + i;
@@ -311,9 +311,8 @@ static int loss_rows(const LossPlan &d, const uint8_t *codes, const uint8_t *sca
                          n, (int)M, first, rows, down, targets, N, last ? loss : nullptr, lse, status);
     if (int r = launch_status(hipGetLastError())) return r;
     if (!dX) continue;
-    const int shift = p.strip == 16 ? 4 : p.strip == 32 ? 5 : 6;
     hipLaunchKernelGGL(mx_loss_down_kernel, dim3((unsigned)((d.ld / 8 + 255) / 256), (unsigned)M), dim3(256), 0, s,
-                       down, n, shift, P, d.ld);
+                       down, n, p.strip, P, d.ld);
     if (int r = launch_status(hipGetLastError())) return r;
     if (int r = launch_grad_parts(
             {pc, ps, cols, K, d.rows, d.cols, P, d.ld, M, parts, first ? nullptr : rows.rescale}, s))

@@ -518,6 +518,7 @@ struct Product {
   ROWS rows;
   EPI epi;
   hipStream_t s;
+  static constexpr bool kPlain = EPI::kPlain;
 
   template <int TR, typename OUT>
   int gemv_as(unsigned n, int threads, size_t lds, int chunks, int wrows) {
@@ -624,6 +625,23 @@ static int launch_product(P &p) {
   if (mean <= 2) return p.template gemv<2>();
   if (mean <= 4 && tiles(16, 64) < 256) return p.template gemv<4>();
   constexpr int kBig = 208, kFill = 384, kSplit = 192;
+  if constexpr (!P::kPlain) {
+    // Three more tiles, between 64 x 128 and 128 x 256: the largest of which there are nearly as
+    // many as the chip holds at once, two a CU, where neither of those two is that.
+    // M x N x K, us, against what the rules below take:
+    //   128 x 192   900 x 10240 x 1024 (432)   32.4   128 x 256: 36.3
+    //   128 x 128   200 x 28672 x 4096 (448)   61               67
+    //              2000 x 4096 x 4096 (512)    63               67
+    //   96 x 128    333 x 13824 x 5120 (432)   61     64 x 128: 67
+    //               100 x 28672 x 4096 (448)   51      (448)    38: the condition on these
+    // (The plain products keep the tiles they had, and their bits.)
+    const auto once = [&](int bm, int bn) { return tiles(bm, bn) >= kFill && tiles(bm, bn) <= 512; };
+    if (rows > 64 && tiles(128, 256) < kFill && tiles(64, 128) > 512) {
+      if (once(128, 192)) return p.template tile<8, 3, 4, 1, 2, 1>();
+      if (once(128, 128)) return p.template tile<8, 2, 4, 1, 2, 1>();
+      if (once(96, 128)) return p.template tile<6, 2, 4, 1, 2, 1>();
+    }
+  }
   // grouped, each expert leaves one that is partly empty
   if (rows > (grouped ? 150 : 64) && tiles(128, 256) >= (grouped ? kFill : kBig))
     return p.template tile<8, 4, 4, 1, 2, 1>();

@@ -446,8 +446,8 @@ enum nf4_act {
  *  - bias fp32 or bf16 [N], residual of Y's shape and type, Z bf16 [M][N]: each may be
  *    NULL.  Z receives z, rounded once, which nf4_mx_linear_grad takes.  residual may be Y
  *    itself (each element is read before it is written, by the same thread).
- * z is within the products' bound (plus 2^-23 |z| for the bias); f is within 2^-20 of its
- * value, the normal numbers' range given.
+ * z is within the products' bound (plus 2^-23 |z| for the bias), f within 2^-20 |z| of its
+ * value.
  * Alignment: codes, X, Y, residual and Z 16 bytes, bias that of its type.  Errors as
  * nf4_mx_gemm; NF4_EINVAL for an unknown act or dtype and for a gated act with odd N.
  */

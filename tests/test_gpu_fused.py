@@ -133,7 +133,8 @@ def test_linear_odd_columns(m, n):
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (2, 4096, 2080), (4, 2048, 4096), (8, 4096, 4096),
                                    (16, 10240, 512), (16, 28672, 256), (33, 24576, 256),
                                    (100, 6144, 512), (40, 26624, 288), (300, 13824, 256),
-                                   (300, 13824, 96), (520, 14336, 256), (520, 14336, 160)])
+                                   (300, 13824, 96), (520, 14336, 256), (520, 14336, 160),
+                                   (700, 13824, 128), (700, 13810, 96), (200, 28672, 128), (200, 28610, 160)])
 @pytest.mark.parametrize("act", ["swiglu", "gelu_tanh"])
 def test_linear_kernels(m, n, k, act):
     run_linear(m, n, k, act, bias=F32, residual=True, keep=m % 2 == 0, seed=k + m)
@@ -356,7 +357,8 @@ def test_loss_small(m, n, grad):
 
 @pytest.mark.parametrize("m,n,k", [(1, 32000, 4096), (5, 32000, 512), (16, 128256, 128), (33, 50257, 160),
                                    (70, 50257, 96), (300, 32001, 256), (2100, 40003, 64), (4200, 301, 32),
-                                   (4100, 17000, 32), (130, 700, 8192)])
+                                   (4100, 17000, 32), (130, 700, 8192), (700, 13810, 64), (200, 28609, 96),
+                                   (300, 13801, 96), (400, 48000, 64)])
 @pytest.mark.parametrize("grad", [False, True])
 def test_loss_shapes(m, n, k, grad):
     run_loss(m, n, k, grad, seed=k, dtype=BF if m % 2 else F32)
