@@ -390,6 +390,32 @@ def test_loss_rising_maximum():
         inside(dx, want[4], want[5] + 1e-36, "dX")
 
 
+def test_loss_of_huge_logits():
+    """Logits up to 2^29: finite, and right to what fp32 holds of them; a row that has one
+    far above the others is its one-hot gradient."""
+    m, n, k = 40, 5000, 32
+    codes = torch.zeros((n, 16), dtype=torch.uint8, device=DEV)
+    codes[:, 0] = 2                                     # value 1 at k = 0
+    codes[:, 8] = 4                                     # value 2 at k = 16
+    scales = (127 + torch.arange(n, device=DEV) % 24).to(torch.uint8).reshape(n, 1)
+    scales[n - 1] = 127 + 26
+    x = torch.zeros((m, k), dtype=BF, device=DEV)
+    x[:, 0] = torch.linspace(-8, 8, m, device=DEV).to(BF)
+    targets = torch.arange(m, device=DEV) * 131 % n
+    targets[m - 1] = n - 1
+    loss, lse, dx = nf4.mx_cross_entropy(codes, scales, x, targets, torch.ones(m, device=DEV), out_dtype=F32)
+    l = x.double() @ values(codes, scales).t().contiguous()
+    assert float(l.max()) == 2.0 ** 29 and float(l.min()) == -2.0 ** 29
+    want = loss_reference(codes, scales, x, targets, torch.ones(m, device=DEV))
+    inside(lse, want[2], want[3], "lse")
+    inside(loss, want[0], want[1], "loss")
+    v = values(codes, scales)
+    top = x[:, 0] > 0.1                                 # the last column is the largest by far
+    one = v[n - 1] - v[targets]
+    inside(dx[top], one[top], 2.0 ** -8 * (v[n - 1].abs() + v[targets].abs())[top], "dX")
+    assert (dx[m - 1] == 0).all() and loss[m - 1] == 0
+
+
 def test_loss_of_well_predicted_tokens():
     """Targets of probabilities from next to nothing up to 1 - 3e-5: the loss and the gradient
     are as precise as they are small (the target's own value is not rounded)."""
