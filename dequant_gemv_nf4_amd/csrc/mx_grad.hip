@@ -348,30 +348,68 @@ static int launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
 }
 
 // ------------------------------------------------- sums shared out over workgroups ----
-// A dense gradient has few tiles where rows are few, so the n are shared out over the
+// A dense gradient has few tiles where rows are few, so the n may be shared out over the
 // workgroups of a tile: parts of the sum in fp32, added in order by whoever takes them.
-// Measured, us with the sum of the parts, M x N x K (splits):
-//   taken                    case                              others
-//   64 x 512                 2048 x 28672 x 4096 (2)     443   not shared out: 475
-//                            300 x 4096 x 14336 (2)       76   two K-groups: 80, 32 x 512: 88
-//   64 x 512, two K-groups   1000 x 13824 x 5120 (1)     173   one, shared out by two: 188
-//   32 x 256, two K-groups   512 x 4096 x 4096 (1)        30   64 x 512 (4): 42
-//                            77 x 13824 x 5120 (4)        33   64 x 512 (25): 54, (12): 34
-//                            32 x 28672 x 4096 (16)       26   32 x 512 (16): 33
-//   16 x 256, two            16 x 28672 x 4096 (16)       23   four (16): 26, two (8): 31
 struct DensePlan {
   int mf, wv, kg, splits;
 };
+// Tile and splits by an estimate of the time.  Workgroups go to the XCDs in whole groups of
+// row tiles (make_grid), 32 CUs each, two workgroups of 256 threads or one of 512 at once a
+// CU; a workgroup takes a time for every stage of 64 n of its K-groups, and two together
+// less than twice that.  `one`, `two`, kFill (stages' worth of start and end) and the cost of
+// the parts (us, and us a MB) are fitted to 1090 measurements, 43 sizes of 1 to 4096 rows
+// each with all tiles and up to 32 splits, and the plan so found is the fastest measured or
+// within 1 % at all but four of the small ones (4-6 %).  Measured, us with the sum of the
+// parts, M x N x K, taken (splits), and others:
+//    16 x 28672 x 4096    16 x 256, two K-groups (16)   21   32 x 256 (16): 24
+//    77 x 13824 x 5120    32 x 256, two K-groups (8)    31   64 x 512 (12): 35
+//   200 x 19360 x 4992    64 x 512, two K-groups (6)    64   32 x 256 (2): 100, (1): 197
+//   512 x 4096 x 4096     32 x 256, two K-groups (1)    29   64 x 512, two K-groups (4): 42
+//  1000 x 13824 x 5120    64 x 512 (3)                 150   two K-groups (1): 173
+//  2048 x 4096 x 4096     64 x 512, two K-groups (1)    65   64 x 512 (2): 94
+//  2048 x 28672 x 4096    64 x 512, two K-groups (1)   392   64 x 512 (2): 428
 static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
-  const auto tiles = [&](int bm, int bk) { return (M + bm - 1) / bm * ((K + bk - 1) / bk); };
-  const int64_t large = tiles(64, 512);
-  if (large >= 256) return {4, 4, 1, large < 512 && N >= 1024 ? 2 : 1};
-  if (large >= 160) return {4, 4, 2, 1};
-  if (large >= 112) return {4, 4, 1, N >= 1024 ? 2 : 1};
-  const int mf = M > 16 ? 2 : 1;
-  // one workgroup a CU, and at least four stages of 64 n for each K-group
-  const int64_t want = 256 / tiles(16 * mf, 256), most = N / 512, n = want < most ? want : most;
-  return {mf, 2, 2, (int)(n > 1 ? n : 1)};
+  struct Tile {
+    DensePlan plan;
+    int row_shift, col_shift;  // log2 of the tile
+    float one, two;            // us a stage of one workgroup on a CU, of two
+  };
+  static constexpr Tile kTiles[] = {{{1, 2, 2, 1}, 4, 8, 0.64f, 1.11f},
+                                    {{2, 2, 2, 1}, 5, 8, 0.72f, 1.13f},
+                                    {{4, 4, 1, 1}, 6, 9, 0.89f, 1.43f},
+                                    {{4, 4, 2, 1}, 6, 9, 1.52f, 3.04f}};
+  static constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32};
+  constexpr float kFill = 2.3f, kParts = 4.4f, kPartsMb = 0.42f;
+  constexpr int64_t kPartsBytes = int64_t(256) << 20;
+  const int stages = (int)((N + 63) >> 6);
+  DensePlan best{};
+  float least = 0.f;
+  for (const Tile &t : kTiles) {
+    if (t.plan.mf == 1 ? M > 64 : t.plan.mf == 4 && M <= 16) continue;
+    const int64_t rows = (M + (1 << t.row_shift) - 1) >> t.row_shift;
+    const int64_t cols = (K + (1 << t.col_shift) - 1) >> t.col_shift;
+    const int64_t group = rows < 8 ? rows : 8, units = (rows < 8 ? 1 : (rows + 7) >> 3) * cols;
+    for (const int splits : kSplits) {
+      const int shares = t.plan.kg * splits;
+      // at least four stages for each share
+      if (splits > 1 && (stages < 4 * shares || splits * M * K * 4 > kPartsBytes)) break;
+      const int64_t a_cu = (((units * splits + 7) >> 3) * group + 31) >> 5;
+      float cost = ((float)(a_cu >> 1) * t.two + (float)(a_cu & 1) * t.one) *
+                   ((float)((stages + shares - 1) / shares) + kFill);
+      if (splits > 1) cost += kParts + kPartsMb * 4e-6f * (float)(splits * M * K);
+      if (best.mf != 0 && cost >= least) continue;
+      best = t.plan;
+      best.splits = splits;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+static int launch_plan(const DensePlan &d, GradArgs &a, int out_dtype, hipStream_t s) {
+  if (d.mf == 1) return launch_grad<1, 2, 2>(a, out_dtype, s);
+  if (d.mf == 2) return launch_grad<2, 2, 2>(a, out_dtype, s);
+  return d.kg == 1 ? launch_grad<4, 4, 1>(a, out_dtype, s) : launch_grad<4, 4, 2>(a, out_dtype, s);
 }
 
 int grad_splits(int64_t M, int64_t N, int64_t K) { return plan_dense(M, N, K).splits; }
@@ -379,29 +417,26 @@ int grad_splits(int64_t M, int64_t N, int64_t K) { return plan_dense(M, N, K).sp
 int launch_grad_parts(const GradParts &g, hipStream_t s) {
   const DensePlan d = plan_dense(g.plan_M, g.plan_N, g.K);
   GradArgs a{g.codes, g.scales, g.dY, nullptr, g.parts, g.M, 1, (int)g.N, (int)g.K, {}, g.ld, d.splits, g.rescale};
-  if (d.mf == 1) return launch_grad<1, 2, 2>(a, NF4_F32, s);
-  if (d.mf == 2) return launch_grad<2, 2, 2>(a, NF4_F32, s);
-  return d.kg == 1 ? launch_grad<4, 4, 1>(a, NF4_F32, s) : launch_grad<4, 4, 2>(a, NF4_F32, s);
+  return launch_plan(d, a, NF4_F32, s);
 }
 
 // out = the parts' sum, in order.  Bound by memory: two parts of 2048 x 4096 12.5 us (6.7 TB/s,
 // from the caches); four of 77 x 5120 4.
 template <typename OUT>
 __global__ void __launch_bounds__(256)
-    mx_parts_kernel(const float *__restrict__ parts, int splits, int64_t size, OUT *__restrict__ out) {
+    mx_parts_kernel(const float *__restrict__ parts, int splits, int64_t size, OUT *__restrict__ out, bool vec) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= size) return;
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
   for (int k = 0; k < splits; ++k) v += *reinterpret_cast<const f32x4_t *>(parts + k * size + i);
-  store4<OUT>(out + i, 0, 4, v, true);
+  store4<OUT>(out + i, 0, 4, v, vec);
 }
 
 // ------------------------------------------------------- in front of the sums ----
 // dZ = dY f'(Z) (gated: dY z_u f'(z_g) and dY f(z_g)) in bf16, and its column sums from the
-// unrounded values.  A thread has four columns (of both halves, gated) and every
-// `blockDim.y`-th row of its workgroup's, so that with `bias` a workgroup has whole columns
-// and the sums are added in one order.
+// unrounded values.  A thread has four columns (of both halves, gated) and every 64th row of
+// its workgroup's; the sums are added in one order.
 // Bound by memory: 2048 rows of 28672, gated, 61 us (4.8 TB/s); 77 rows of 13824 with the column
 // sums 5-6, mostly start and the sums' way through LDS.
 template <int LANES, bool GATED>
@@ -445,31 +480,57 @@ __global__ void __launch_bounds__(1024)
     }
   }
   if (!dbias) return;
+  dbias += (int64_t)blockIdx.y * N;
 #pragma unroll
   for (int i = 0; i < W; ++i) part[(y * LANES + c) * W + i] = sum[i];
   __syncthreads();
   for (int k = threadIdx.x; k < LANES * W; k += 1024) {
     float v = 0.f;
     for (int r = 0; r < ny; ++r) v += part[r * LANES * W + k];
-    const int at = (blockIdx.x * LANES + k / W) * 4 + k % 4;
+    const int at = ((int)blockIdx.x * LANES + k / W) * 4 + k % 4;
     if (at < cols) dbias[k % W >= 4 ? cols + at : at] = v;
   }
 }
 
+// Workgroups that share the rows of a column: without column sums 64 rows each; with them one
+// has all, but where columns are few and rows many, whose sums then meet in the workspace.
+// Us, one and shared out, the sums' kernel included: 2000 x 8192 gated 50 and 26, 1695 x 15792
+// gated 55 and 41, 1000 x 4096 17 and 13; 1024 x 14336 (224 workgroups of columns) is as fast
+// as without sums, 38.
+static int64_t bias_groups(int64_t M, int64_t N, bool gated) {
+  const int64_t blocks = ((gated ? N >> 1 : N) + 63) >> 6;
+  if (M < 512 || blocks > 128) return 1;
+  const int64_t want = 512 / blocks, most = M >> 6;
+  return want < most ? want : most;
+}
+static int64_t bias_bytes(int64_t groups, int64_t N) { return groups > 1 ? (groups * N * 4 + 255) / 256 * 256 : 0; }
+
+static int launch_parts(const float *parts, int splits, int64_t size, void *out, int out_dtype, hipStream_t s) {
+  const dim3 grid((unsigned)((size / 4 + 255) / 256));
+  if (out_dtype == NF4_F32)
+    hipLaunchKernelGGL((mx_parts_kernel<float>), grid, dim3(256), 0, s, parts, splits, size,
+                       static_cast<float *>(out), aligned_to(out, 16));
+  else
+    hipLaunchKernelGGL((mx_parts_kernel<uint16_t>), grid, dim3(256), 0, s, parts, splits, size,
+                       static_cast<uint16_t *>(out), true);
+  return launch_status(hipGetLastError());
+}
+
+// sums: for bias_groups x N parts of dbias
 static int launch_act_grad(const uint16_t *dY, const uint16_t *Z, int64_t M, int64_t N, int act, uint16_t *dZ,
-                           float *dbias, hipStream_t s) {
+                           float *dbias, float *sums, hipStream_t s) {
   const bool gated = is_gated(act);
   const int64_t cols = gated ? N / 2 : N;
-  // without a bias the rows are shared out as well
-  const int64_t rows = dbias ? M : 64;
-  const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)((M + rows - 1) / rows));
+  const int64_t groups = dbias ? bias_groups(M, N, gated) : (M + 63) >> 6;
+  const int64_t rows = (M + groups - 1) / groups, used = (M + rows - 1) / rows;
+  const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)used);
+  float *const to = dbias && used > 1 ? sums : dbias;
   if (gated)
-    hipLaunchKernelGGL((mx_act_grad_kernel<16, true>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ,
-                       dbias);
+    hipLaunchKernelGGL((mx_act_grad_kernel<16, true>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ, to);
   else
-    hipLaunchKernelGGL((mx_act_grad_kernel<16, false>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ,
-                       dbias);
-  return launch_status(hipGetLastError());
+    hipLaunchKernelGGL((mx_act_grad_kernel<16, false>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ, to);
+  if (int r = launch_status(hipGetLastError())) return r;
+  return dbias && used > 1 ? launch_parts(sums, (int)used, N, dbias, NF4_F32, s) : NF4_OK;
 }
 
 }  // namespace mx
@@ -499,7 +560,7 @@ int64_t nf4_mx_linear_grad_workspace_bytes(int64_t N, int64_t K, int64_t M) {
   if (nf4::check_mx_shape(N, K) || N % 8 != 0 || N > (int64_t(1) << 23) || M < 1 || M > (int64_t(1) << 21))
     return -1;
   const int64_t n = nf4::mx::grad_splits(M, N, K);
-  return n > 1 ? n * M * K * 4 : 0;
+  return (n > 1 ? n * M * K * 4 : 0) + nf4::mx::bias_bytes(nf4::mx::bias_groups(M, N, true), N);
 }
 
 int nf4_mx_linear_grad(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, const uint16_t *dY,
@@ -518,29 +579,25 @@ int nf4_mx_linear_grad(const uint8_t *codes, const uint8_t *scales, int64_t N, i
       !nf4::aligned_to(dZ, 16) || !nf4::aligned_to(dX, 16) || !nf4::aligned_to(dbias, 4) ||
       !nf4::aligned_to(workspace, 256))
     return NF4_EALIGN;
-  const int64_t need = nf4_mx_linear_grad_workspace_bytes(N, K, M);
+  const DensePlan plan = plan_dense(M, N, K);
+  const int splits = plan.splits;
+  const int64_t sums = dbias ? bias_bytes(bias_groups(M, N, is_gated(act)), N) : 0;
+  const int64_t need = sums + (splits > 1 ? splits * M * K * 4 : 0);
   if (need > 0 && (!workspace || workspace_bytes < need)) return NF4_ERANGE;
   if (int r = nf4::device_status()) return r;
   hipStream_t s = (hipStream_t)stream;
   if (!plain || dZ || dbias)
-    if (int r = launch_act_grad(dY, plain ? nullptr : Z, M, N, act, dZ, dbias, s)) return r;
+    if (int r = launch_act_grad(dY, plain ? nullptr : Z, M, N, act, dZ, dbias, static_cast<float *>(workspace), s))
+      return r;
   const uint16_t *d = plain ? dY : dZ;
-  if (need == 0) {
+  if (splits == 1) {
     GradArgs a{codes, scales, d, nullptr, dX, M, 1, (int)N, (int)K, {}, 0, 1, nullptr};
-    return launch_rows_grad(a, out_dtype, s);
+    return launch_plan(plan, a, out_dtype, s);
   }
-  float *parts = static_cast<float *>(workspace);
-  if (int r = launch_grad_parts({codes, scales, N, K, M, N, d, N, M, parts, nullptr}, s)) return r;
-  const int splits = grad_splits(M, N, K);
-  const int64_t size = M * K;
-  const unsigned blocks = (unsigned)((size / 4 + 255) / 256);
-  if (out_dtype == NF4_F32)
-    hipLaunchKernelGGL((mx_parts_kernel<float>), dim3(blocks), dim3(256), 0, s, parts, splits, size,
-                       static_cast<float *>(dX));
-  else
-    hipLaunchKernelGGL((mx_parts_kernel<uint16_t>), dim3(blocks), dim3(256), 0, s, parts, splits, size,
-                       static_cast<uint16_t *>(dX));
-  return nf4::launch_status(hipGetLastError());
+  float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + sums);
+  GradArgs a{codes, scales, d, nullptr, parts, M, 1, (int)N, (int)K, {}, N, splits, nullptr};
+  if (int r = launch_plan(plan, a, out_dtype, s)) return r;
+  return launch_parts(parts, splits, M * K, dX, out_dtype, s);
 }
 
 }  // extern "C"

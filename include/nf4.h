@@ -466,7 +466,8 @@ int nf4_mx_linear(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_
  * relu'(0) = 0.  N is a multiple of 8 (NF4_EINVAL) and at most 2^23, M at most 2^21.
  *  - workspace: device memory, 256-byte aligned, of at least
  *    nf4_mx_linear_grad_workspace_bytes(N, K, M) bytes (0: may be NULL), with anything in
- *    it; the sums over n of calls of few rows are shared out over workgroups and meet there.
+ *    it, at most 2^28 + 2^18; where the tiles of dX are few, the sums over n are shared out
+ *    over workgroups and meet there, and so are dbias's of many rows.
  *    Calls that share one must not run at the same time.
  * Alignment: codes, dY, Z, dZ and dX 16 bytes.  Errors: NF4_ERANGE for a missing or short
  * workspace, otherwise as nf4_mx_linear.
@@ -494,9 +495,9 @@ int nf4_mx_linear_grad(const uint8_t *codes, const uint8_t *scales, int64_t N, i
  * fp32 numbers are 2^7 apart.
  *  - workspace: device memory, 256-byte aligned, of at least
  *    nf4_mx_cross_entropy_workspace_bytes(N, K, M, dX != NULL) bytes, with anything in it:
- *    up to 2^28 bytes, and with dX 4 K bytes a row of up to 4096 rows (more for few rows,
- *    whose sums are shared out over workgroups).  Calls that share one must not run at the
- *    same time.  The function returns -1 for sizes that the call refuses.
+ *    up to 2^28 bytes, and with dX 4 K bytes a row of up to 4096 rows (or more, up to 2^28
+ *    bytes, where their sums are shared out over workgroups).  Calls that share one must not
+ *    run at the same time.  The function returns -1 for sizes that the call refuses.
  * The sums over k are the products'; exp is within 2^-20 of its value (|l| at most 64, in
  * proportion beyond), sums of it are fp32, and the gradient takes exp(l - lse) in bf16, each
  * rounded once, but for the target, whose factor 1 - exp(l - lse) is the others' sum in fp32:

@@ -224,7 +224,8 @@ def test_grad_acts(m, act):
 
 @pytest.mark.parametrize("m,n,k", [(1, 8, 32), (2, 16, 64), (1, 4096, 4096), (20, 8192, 96), (77, 13824, 640),
                                    (64, 1000, 4096), (700, 504, 1056), (2100, 64, 4096), (50, 1032, 32),
-                                   (33, 4104, 8192)])
+                                   (33, 4104, 8192), (300, 8192, 1056), (300, 8192, 1152), (1100, 8200, 2464),
+                                   (1100, 8200, 2560), (1000, 8200, 1504), (1200, 2056, 4128), (130, 28672, 256)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_grad_shapes(m, n, k, dtype):
     run_grad(m, n, k, "swiglu" if n % 16 == 0 else "silu", m % 2 == 0, dtype, seed=n)
@@ -266,6 +267,23 @@ def test_grad_by_differences(act):
         e[j] = h
         want = (total(x64, b64 + e) - total(x64, b64 - e)) / (2 * h)
         assert abs(float(db[j]) - want) <= 2.0 ** -7 * size * m, (act, j)
+
+
+@pytest.mark.parametrize("act", [None, "silu", "swiglu"])
+@pytest.mark.parametrize("m", [511, 512, 577, 3000])
+def test_bias_gradient_of_many_rows(m, act):
+    """Rows shared out over workgroups; dbias anywhere that fp32 may lie."""
+    n, k = 136, 64
+    codes, scales = matrix(n, k, 1)
+    dy, z = rand((m, n // 2 if act == "swiglu" else n), 2), rand((m, n), 3)
+    buf, ws = alloc((nf4.mx_linear_grad_workspace_bytes(n, k, m),), torch.uint8, DEV)
+    db = torch.full((n + 5,), 7.0, device=DEV)
+    dx, dz = torch.empty((m, k), device=DEV), torch.empty_like(z)
+    nf4.nf4_mx_linear_grad(codes, scales, dy, None if act is None else z, act, dx, dz, db[3:3 + n], ws)
+    check(buf, "workspace")
+    assert (db[:3] == 7).all() and (db[3 + n:] == 7).all()
+    want, tol = grad_reference(codes, scales, dy, z, act)[2:]
+    inside(db[3:3 + n], want, tol, f"dbias {m} {act}")
 
 
 def test_grad_without_activation():
