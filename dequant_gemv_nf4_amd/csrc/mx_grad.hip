@@ -374,12 +374,12 @@ static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
     int row_shift, col_shift;  // log2 of the tile
     float one, two;            // us a stage of one workgroup on a CU, of two
   };
-  static constexpr Tile kTiles[] = {{{1, 2, 2, 1}, 4, 8, 0.64f, 1.11f},
+  static constexpr Tile kTiles[] = {{{1, 2, 2, 1}, 4, 8, 0.65f, 1.12f},
                                     {{2, 2, 2, 1}, 5, 8, 0.72f, 1.13f},
-                                    {{4, 4, 1, 1}, 6, 9, 0.89f, 1.43f},
-                                    {{4, 4, 2, 1}, 6, 9, 1.52f, 3.04f}};
+                                    {{4, 4, 1, 1}, 6, 9, 0.88f, 1.43f},
+                                    {{4, 4, 2, 1}, 6, 9, 1.5f, 3.f}};
   static constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32};
-  constexpr float kFill = 2.3f, kParts = 4.4f, kPartsMb = 0.42f;
+  constexpr float kFill = 2.35f, kParts = 4.5f, kPartsMb = 0.43f;
   constexpr int64_t kPartsBytes = int64_t(256) << 20;
   const int stages = (int)((N + 63) >> 6);
   DensePlan best{};
@@ -388,12 +388,13 @@ static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
     if (t.plan.mf == 1 ? M > 64 : t.plan.mf == 4 && M <= 16) continue;
     const int64_t rows = (M + (1 << t.row_shift) - 1) >> t.row_shift;
     const int64_t cols = (K + (1 << t.col_shift) - 1) >> t.col_shift;
-    const int64_t group = rows < 8 ? rows : 8, units = (rows < 8 ? 1 : (rows + 7) >> 3) * cols;
+    const int64_t group = rows < 8 ? rows : 8, whole = rows < 8 ? 1 : rows >> 3, rest = rows < 8 ? 0 : rows & 7;
     for (const int splits : kSplits) {
       const int shares = t.plan.kg * splits;
       // at least four stages for each share
       if (splits > 1 && (stages < 4 * shares || splits * M * K * 4 > kPartsBytes)) break;
-      const int64_t a_cu = (((units * splits + 7) >> 3) * group + 31) >> 5;
+      const int64_t blocks = cols * splits;
+      const int64_t a_cu = (((whole * blocks + 7) >> 3) * group + ((blocks + 7) >> 3) * rest + 31) >> 5;
       float cost = ((float)(a_cu >> 1) * t.two + (float)(a_cu & 1) * t.one) *
                    ((float)((stages + shares - 1) / shares) + kFill);
       if (splits > 1) cost += kParts + kPartsMb * 4e-6f * (float)(splits * M * K);

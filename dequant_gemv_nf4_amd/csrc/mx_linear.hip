@@ -26,12 +26,27 @@ struct LinearOut {
     return bias_bf16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(bias)[n] << 16)
                      : reinterpret_cast<const float *>(bias)[n];
   }
-  // z[0 .. 3] at columns n .. n + 3 of row m of the matrix's N columns; adds the bias and keeps z
-  __device__ __forceinline__ f32x4_t take(const Args &p, int64_t m, int n, int end, f32x4_t z, bool vec) const {
+  // The bias of four outputs from column n of Y on, and of what a gated one multiplies them with.
+  struct Bias {
+    f32x4_t z, zu;
+  };
+  __device__ __forceinline__ Bias bias_of(const Args &p, int n) const {
+    Bias b{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     if (bias) {
+      const int cols = PAIRS ? p.N >> 1 : p.N;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] += n + i < end ? bias_at(n + i) : 0.f;
+      for (int i = 0; i < 4; ++i)
+        if (n + i < cols) {
+          b.z[i] = bias_at(n + i);
+          if (PAIRS) b.zu[i] = bias_at(cols + n + i);
+        }
     }
+    return b;
+  }
+  // z[0 .. 3] at columns n .. n + 3 of row m of the matrix's N columns; adds the bias and keeps z
+  __device__ __forceinline__ f32x4_t take(const Args &p, int64_t m, int n, int end, f32x4_t z, f32x4_t b,
+                                          bool vec) const {
+    if (bias) z += b;
     if (Z) {
       uint16_t *row = Z + m * p.N;
       store4<uint16_t>(row, n, end, z, vec);
@@ -66,12 +81,13 @@ struct LinearOut {
   }
   // Four outputs from column n of Y on; zu: what a gated product multiplies them with.
   template <typename OUT>
-  __device__ __forceinline__ void finish(const Args &p, int64_t m, int n, f32x4_t z, f32x4_t zu) const {
+  __device__ __forceinline__ void finish(const Args &p, int64_t m, int n, f32x4_t z, f32x4_t zu,
+                                         const Bias &b) const {
     const int cols = PAIRS ? p.N >> 1 : p.N;
     const bool vec = (cols & 3) == 0;
-    z = take(p, m, n, cols, z, vec);
+    z = take(p, m, n, cols, z, b.z, vec);
     f32x4_t y = act_values(act, z);
-    if constexpr (PAIRS) y *= take(p, m, cols + n, p.N, zu, vec);
+    if constexpr (PAIRS) y *= take(p, m, cols + n, p.N, zu, b.zu, vec);
     put<OUT>(p, m, n, cols, y, vec);
   }
 
@@ -89,7 +105,8 @@ struct LinearOut {
         if (c < cols) z[j] = sum(m, c);
         if (PAIRS && c < cols) zu[j] = sum(m, c + 1);
       }
-      finish<OUT>(p, t.row0 + m, (PAIRS ? n0 >> 1 : n0) + r / (W / 4), z, zu);
+      const int n = (PAIRS ? n0 >> 1 : n0) + r / (W / 4);
+      finish<OUT>(p, t.row0 + m, n, z, zu, bias_of(p, n));
     }
   }
   template <int MF, int NF, int WV, int KG, typename OUT, int BYTES, class ROWS>
@@ -97,20 +114,26 @@ struct LinearOut {
                                            int kg, const f32x4_t (&acc)[NF][MF], uint8_t *lds) const {
     typedef TileRows<MF, NF, WV, KG, BYTES> T;
     T::each(wave, kg, acc, lds, [&](const float *z, int m0, int rows) __attribute__((always_inline)) {
-      constexpr int W = PAIRS ? 8 : 4, quads = T::kCols / W;
+      constexpr int W = PAIRS ? 8 : 4, quads = T::kCols / W, kThreads = 64 * WV * KG;
       const int n = min(rows, t.rows - m0) * quads;
+      const auto first = [&](int r) __attribute__((always_inline)) { return PAIRS ? (n0 + r) >> 1 : n0 + r; };
+      // a thread's columns are the same in all rows, but in tiles of 192: the bias is read once
+      // (1021 x 28672 x 4096, gated, with bias 227 us read for each row, 212 so, as without one)
+      constexpr bool kFixed = kThreads % quads == 0;
+      Bias b = bias_of(p, first((int)threadIdx.x % quads * W));
 #pragma unroll 1
-      for (int i = threadIdx.x; i < n; i += 64 * WV * KG) {
+      for (int i = threadIdx.x; i < n; i += kThreads) {
         const int m = i / quads, r = i % quads * W;
         if (n0 + r >= p.N) continue;
+        if (!kFixed) b = bias_of(p, first(r));
         const float *s = z + m * T::kPitch + r;
         const f32x4_t a = *reinterpret_cast<const f32x4_t *>(s);
         if constexpr (PAIRS) {
-          const f32x4_t b = *reinterpret_cast<const f32x4_t *>(s + 4);
-          finish<OUT>(p, t.row0 + m0 + m, (n0 + r) >> 1, f32x4_t{a[0], a[2], b[0], b[2]},
-                      f32x4_t{a[1], a[3], b[1], b[3]});
+          const f32x4_t c = *reinterpret_cast<const f32x4_t *>(s + 4);
+          finish<OUT>(p, t.row0 + m0 + m, first(r), f32x4_t{a[0], a[2], c[0], c[2]},
+                      f32x4_t{a[1], a[3], c[1], c[3]}, b);
         } else {
-          finish<OUT>(p, t.row0 + m0 + m, n0 + r, a, a);
+          finish<OUT>(p, t.row0 + m0 + m, first(r), a, a, b);
         }
       }
     });
@@ -142,6 +165,9 @@ int nf4_mx_linear(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_
       !nf4::aligned_to(residual, 16) || !nf4::aligned_to(Z, 16) ||
       !nf4::aligned_to(bias, bias_dtype == NF4_BF16 ? 2 : 4))
     return NF4_EALIGN;
+  // with nothing after it the product itself: its kernels, and its bits
+  if (act == NF4_ACT_NONE && !bias && !residual && !Z)
+    return nf4_mx_gemm(codes, scales, N, K, X, M, Y, out_dtype, stream);
   if (int r = nf4::device_status()) return r;
   const nf4::mx::Args a{codes, scales, X, nullptr, Y, M, 1, (int)N, (int)K, {}};
   hipStream_t s = (hipStream_t)stream;
