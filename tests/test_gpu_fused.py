@@ -149,6 +149,20 @@ def test_linear_vector_and_in_place():
     assert torch.equal(r, want)
 
 
+# One size of each tile of the products with epilogues, with whole words of scales and
+# (second of each) without, the last columns of a tile left out
+TILES = [(600, 20010, 128), (600, 20010, 160), (200, 40006, 128), (200, 40006, 160), (200, 20010, 128),
+         (200, 20010, 160), (100, 9000, 128), (100, 9000, 160), (20, 40006, 128), (20, 40006, 160),
+         (100, 2050, 128), (100, 2050, 160), (100, 2050, 4096), (100, 2050, 4128), (40, 130, 128),
+         (40, 130, 160), (40, 4100, 1024), (40, 4100, 1056), (40, 130, 1024), (40, 130, 1056)]
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+@pytest.mark.parametrize("act,bias", [("geglu", BF), ("silu", F32)])
+def test_linear_tiles(m, n, k, act, bias):
+    run_linear(m, n, k, act, bias=bias, residual=act == "silu", keep=act == "geglu", seed=k + m)
+
+
 def test_linear_is_the_product():
     """Without bias, activation and residual the sums are nf4_mx_gemm's, bit for bit."""
     for m in (1, 3, 20, 300):
@@ -380,6 +394,11 @@ def test_loss_small(m, n, grad):
 @pytest.mark.parametrize("grad", [False, True])
 def test_loss_shapes(m, n, k, grad):
     run_loss(m, n, k, grad, seed=k, dtype=BF if m % 2 else F32)
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_loss_tiles(m, n, k):
+    run_loss(m, n, k, True, seed=k, dtype=BF)
 
 
 @pytest.mark.parametrize("scale", [0.0, 1e-3, 30.0, 1000.0])
