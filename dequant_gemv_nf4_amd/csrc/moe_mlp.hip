@@ -666,9 +666,11 @@ static DownPlan down_plan(int64_t H, int64_t I, int64_t tiles) {
   };
   // G = 4 from where every wave of the chip has a unit and a half, us against G = 1: 2 experts
   // of 4096 x 14336 (56 units) 22.7, 24.1; of 4096 x 8192 (32) 15.1, 15.3; of 4096 x 4096 (16)
-  // 13.4, 9.0; 8 of 128 of 2048 x 768 (16) 12.7, 7.9, about 90 of them 28, 34
+  // 13.4, 9.0; 8 of 128 of 2048 x 768 (16) 12.7, 7.9, about 90 of them 28, 34.  And where G = 1
+  // makes more than 256 column blocks: 8 experts of 5120 x 2048 (32 units) 20.8, 25.4; 2 of
+  // 8192 x 4096 (16) 13.8, 17.0; 1 of 8192 x 512 (1) 5.4, 6.4; 4 of 4608 x 1024 (8) 11.4, 10.3
   const int64_t b4 = (H + 63) / 64;
-  d.g = 2 * units * (b4 < 256 ? b4 : 256) >= 3 * 8 * 256 ? 4 : 1;
+  d.g = H > 4096 || 2 * units * (b4 < 256 ? b4 : 256) >= 3 * 8 * 256 ? 4 : 1;
   d.blocks = (int)((H + 16 * d.g - 1) / (16 * d.g));
   d.splits = (int)splits(d.g);
   return d;
