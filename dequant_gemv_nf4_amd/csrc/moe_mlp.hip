@@ -615,10 +615,12 @@ struct MlpArgs {
 };
 
 // Whether the rows of an expert are few (16 a tile) or the tiles of the longer products are
-// used; at most 2^13 pairs either way (16 x 512, or eight an expert).
-// Both, us, 4096 x 14336 of 8 experts, two a token: 24 tokens 167 and 175, 32 172 and 182, 64
-// 289 and 229; 2048 x 768 of 64, eight a token: 64 tokens 59 and 59.
-static bool few_rows(int64_t T, int64_t topk, int64_t E) { return T * topk <= 8 * E || T <= 16; }
+// used; at most 2^13 pairs with few (16 x 512).
+// Both, us, rows an expert in brackets: 4096 x 14336 of 8 experts 170 and 182 (4.2), 187 both
+// (6), 191 and 189 (8), 242 and 195 (12); 2048 x 768 of 128 91 and 84 (3.8), of 96 77 and 68 (5),
+// of 64 60 and 49 (7.5); 2048 x 4096 of 10 62 and 46 (6.4); 4096 x 1536 of 121 259 and 276 (4.2),
+// of 32 84 and 86 (6).
+static bool few_rows(int64_t T, int64_t topk, int64_t E) { return T * topk <= 5 * E || T <= 16; }
 
 // the tiles that there can be
 static int64_t tiles_of(int64_t pairs, int64_t E) { return slots_for(pairs, E, true, 16); }
