@@ -614,13 +614,22 @@ struct MlpArgs {
   int64_t pairs;
 };
 
+constexpr int kFewWaves = 8;  // of a workgroup of the first product of few rows
+
 // Whether the rows of an expert are few (16 a tile) or the tiles of the longer products are
 // used; at most 2^13 pairs with few (16 x 512).
 // Both, us, rows an expert in brackets: 4096 x 14336 of 8 experts 170 and 182 (4.2), 187 both
 // (6), 191 and 189 (8), 242 and 195 (12); 2048 x 768 of 128 91 and 84 (3.8), of 96 77 and 68 (5),
 // of 64 60 and 49 (7.5); 2048 x 4096 of 10 62 and 46 (6.4); 4096 x 1536 of 121 259 and 276 (4.2),
 // of 32 84 and 86 (6).
-static bool few_rows(int64_t T, int64_t topk, int64_t E) { return T * topk <= 5 * E || T <= 16; }
+// Where H takes the first product more than one pass, that waits for X in each: few and tiles,
+// 8 of 64 experts of 7168 x 2048 59 and 47 (one token), of 128 of 6144 x 1024 327 and 253 (32), 4
+// of 32 of 5120 x 1536 96 and 77 (8); 1 of 16 of 5120 x 8192 129 and 137 (8); but one of 5120 x
+// 2048, one token, 18 and 26.
+static bool few_rows(int64_t T, int64_t topk, int64_t E, int64_t H) {
+  if (H > kFewWaves * kRange && T * (topk < E ? topk : E) >= 8) return false;
+  return T * topk <= 5 * E || T <= 16;
+}
 
 // the tiles that there can be
 static int64_t tiles_of(int64_t pairs, int64_t E) { return slots_for(pairs, E, true, 16); }
@@ -639,7 +648,7 @@ static int launch_up_as(const UpArgs &u, bool svec, bool longer, dim3 grid, dim3
 }
 template <bool PAIRS>
 static int launch_up_few(const MlpArgs &a, int ncounters, hipStream_t s) {
-  const int ranges = (a.H + kRange - 1) / kRange, waves = ranges < 8 ? ranges : 8;
+  const int ranges = (a.H + kRange - 1) / kRange, waves = ranges < kFewWaves ? ranges : kFewWaves;
   const int hold = 256 * (8 / waves);
   const int64_t tiles = tiles_of(a.pairs, a.E);
   // blocks of one group where two to a block would leave CUs without one
@@ -717,7 +726,7 @@ static int launch_tiles(Product<ROWS, EPI, F32, B16> p) {
 }
 
 static int launch_mlp(const MlpArgs &a, hipStream_t s) {
-  if (few_rows(a.r.T, a.r.topk, a.E)) return launch_few(a, s);
+  if (few_rows(a.r.T, a.r.topk, a.E, a.H)) return launch_few(a, s);
   const Args up{a.codes1, a.scales1, a.X, nullptr, a.rows, a.pairs, a.E, a.N1, a.H, {}};
   int r;
   if (is_gated(a.act))
@@ -748,7 +757,7 @@ static MlpPlan mlp_plan(int64_t E, int64_t H, int64_t I, int64_t T, int64_t topk
   MlpPlan d;
   d.pairs = pair_count(T, topk, E);
   d.sums = whole(d.pairs * I * 2);
-  if (!few_rows(T, topk, E)) {
+  if (!few_rows(T, topk, E, H)) {
     d.counters = d.bytes = d.sums + whole(d.pairs * H * 4);
     return d;
   }

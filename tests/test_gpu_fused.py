@@ -611,7 +611,7 @@ def test_moe_acts(t, k, e, act):
 @pytest.mark.parametrize("t,k,e,h,i", [(1, 8, 128, 2048, 768), (19, 8, 128, 256, 96), (64, 2, 128, 512, 160),
                                        (64, 1, 512, 32, 32), (64, 8, 8, 1024, 32), (64, 2, 8, 512, 4096),
                                        (2, 2, 4, 32, 14336), (3, 4, 6, 8192, 32), (33, 2, 16, 544, 1056),
-                                       (64, 512, 512, 32, 32), (5, 2, 8, 4640, 544), (1, 1, 4, 8192, 512), (16, 16, 16, 160, 224), (1, 1, 2, 4096, 8224),
+                                       (64, 512, 512, 32, 32), (5, 2, 8, 4640, 544), (1, 1, 4, 8192, 512), (3, 2, 8, 4640, 544), (1, 8, 16, 7168, 96), (16, 16, 16, 160, 224), (1, 1, 2, 4096, 8224),
                                        (48, 40, 64, 64, 32)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_moe_shapes(t, k, e, h, i, dtype):
