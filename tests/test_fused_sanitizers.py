@@ -16,7 +16,7 @@ def test_fused_validation_under_asan_ubsan(tmp_path):
     exe = str(tmp_path / "fused_abi_asan")
     srcs = [os.path.join(CSRC, f) for f in (
         "api.hip", "pack.hip", "gemv.hip", "gemm_mfma.hip", "gemm_prefill.hip", "embed.hip",
-        "mx_grad.hip", "mx_linear.hip", "mx_loss.hip", "moe_mlp.hip")]
+        "mx_gemm.hip", "mx_grad.hip", "mx_linear.hip", "mx_loss.hip", "moe_mlp.hip")]
     srcs.append(os.path.join(HERE, "fused_abi_driver.cpp"))
     flags = ["--offload-arch=gfx950", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
