@@ -7,6 +7,7 @@
 // sum over the token's slots with that expert; rows are numbered by expert, then token.
 // The first kernel writes act(W1 x) times the row's weight, in bf16 (one rounding, as
 // between two layers); the second one's sums over all its rows are then the output.
+#include "moe_units.h"
 #include "mx_act.h"
 #include "mx_product.h"
 
@@ -22,10 +23,6 @@ struct Routing {
   int T, topk, E;
 };
 
-// What every workgroup makes of the routing.
-struct Masks {
-  uint32_t of[2 * NF4_MOE_MAX_E];  // tokens of each expert
-};
 __device__ __forceinline__ uint64_t mask_of(const Masks &m, int e) {
   return (uint64_t)m.of[2 * e + 1] << 32 | m.of[2 * e];
 }
@@ -402,12 +399,6 @@ __global__ void __launch_bounds__(512)
 // 2048 x 768 28.  (Built and slower: the items of the first product with a last workgroup
 // that adds up, 70, 24 and 33, since few workgroups are last for all columns; the sums
 // written back by a fence of the whole cache, 76, 23 and 62.)
-struct ActiveExperts {
-  Masks masks;
-  uint16_t expert[NF4_MOE_MAX_E];
-  uint16_t row0[NF4_MOE_MAX_E];
-  int count;
-};
 template <int G, bool SVEC, typename OUT>
 __global__ void __launch_bounds__(512)
     moe_down_kernel(Args p, int splits, Routing r, const void *residual, float *parts, uint32_t *counters) {
@@ -443,18 +434,8 @@ __global__ void __launch_bounds__(512)
   const auto uniform = [](int v) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(v); };
   const int ranges = (p.K + kRange - 1) / kRange, units = uniform(act.count) * ranges, step = waves * splits;
   float *const own = sums + wave * r.T * kCols;
-  struct Unit {  // past the last one `rows` and `cols` are 0, and its buffers empty
-    int e, row0, rows, cols, k0;
-    uint64_t mask;
-  };
   const auto unit = [&](int u) __attribute__((always_inline)) {
-    const bool ok = u < units;
-    const int i = ok ? u / ranges : 0;
-    Unit v{uniform(act.expert[i]), uniform(act.row0[i]), 0, ok ? cols : 0, ok ? (u - i * ranges) * kRange : 0, 0};
-    const uint64_t m = (uint64_t)(uint32_t)uniform(act.masks.of[2 * v.e + 1]) << 32 | (uint32_t)uniform(act.masks.of[2 * v.e]);
-    v.mask = ok ? m : 0;
-    v.rows = __popcll(v.mask);
-    return v;
+    return unit_of(act, u, units, ranges, kRange, cols, uniform);
   };
   const auto load_x = [&](u32x4_t (&x)[4][4], const Unit &v, int m0) __attribute__((always_inline)) {
     const int rows = max(min(16, v.rows - m0), 0);
