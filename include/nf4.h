@@ -490,9 +490,11 @@ int nf4_mx_linear_grad(const uint8_t *codes, const uint8_t *scales, int64_t N, i
  * is frozen); both are given or both NULL.  A row whose target is negative is ignored: loss 0,
  * a zero row of dX, its lse as for the others.  So is one whose target is N or more, which is
  * flagged in *dev_status (device int32, may be NULL; if given, the call first clears it).
- * A row with a NaN or infinite logit has a lse that is not finite, and (if not ignored) a loss
- * and a row of dX that are not.  The same may happen beyond |l| = 2^30, where neighbouring
- * fp32 numbers are 2^7 apart.
+ * A row with a logit of NaN or +infinity has a lse that is not finite, and (if not ignored) a
+ * loss and a row of dX that are not.  The same may happen beyond |l| = 2^30, where neighbouring
+ * fp32 numbers are 2^7 apart.  A logit of -infinity has probability 0: beside finite ones lse
+ * and dX are theirs, and the loss is infinite if it is the target's; a row of nothing else has
+ * lse -infinity, and a loss and a row of dX that are not finite.
  *  - workspace: device memory, 256-byte aligned, of at least
  *    nf4_mx_cross_entropy_workspace_bytes(N, K, M, dX != NULL) bytes, with anything in it:
  *    up to 2^28 bytes, and with dX 4 K bytes a row of up to 4096 rows (or more, up to 2^28
