@@ -1,11 +1,12 @@
 """Calls of the fused MXFP4 operators that their documentation allows and that lie at an edge:
-layers of experts that no token goes to, infinite logits."""
+layers of experts that no token goes to, infinite logits; and gradients by differences."""
 import pytest
 import torch
 
 import dequant_gemv_nf4_amd as nf4
+import grad_differences
 from mx_reference import values
-from test_gpu_fused import BF, DEV, F32, inside, loss_reference, matrix, rand, run_moe
+from test_gpu_fused import ACTS, BF, DEV, F32, inside, loss_reference, matrix, rand, run_moe
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,21 @@ def test_loss_of_nothing_but_infinities():
     assert not torch.isfinite(loss[:2]).any() and not torch.isfinite(dx[:2]).any()
     assert torch.isfinite(lse[2]) and torch.isfinite(loss[2]) and torch.isfinite(dx[2]).all()
     assert loss[3] == 0 and (dx[3] == 0).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n,k", [(3, 64, 64), (40, 128, 96), (600, 64, 32)])
+def test_gradient_against_differences(act, m, n, k):
+    """dZ, dbias and dX against differences of the activation itself; the bounds are shown to
+    refuse wrong gradients in test_grad_differences.py."""
+    codes, scales = matrix(n, k, m + n)
+    v = values(codes, scales)
+    x, bias = rand((m, k), m + 1), rand((n,), m + 2, F32, 0.1)
+    exact = x.double() @ v.t().contiguous() + bias.double()
+    y, z = nf4.mx_linear(codes, scales, x, bias=bias, act=act, out_dtype=F32, keep_z=True)
+    dy = rand(y.shape, m + 3)
+    dx, dz, db = nf4.mx_linear_grad(codes, scales, dy, z, act, out_dtype=F32, bias_grad=True)
+    assert grad_differences.check_dz(act, z, dy, dz) == 0
+    assert grad_differences.check_dbias(act, z, dy, db) == 0
+    assert grad_differences.check_dx(dz, v, dx) == 0
+    assert grad_differences.check_whole(act, exact, dy, v, dx) == 0
