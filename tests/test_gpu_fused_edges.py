@@ -1,12 +1,14 @@
 """Calls of the fused MXFP4 operators that their documentation allows and that lie at an edge:
-layers of experts that no token goes to, infinite logits; and gradients by differences."""
+layers of experts that no token goes to, as many tokens as there may be, infinite logits, values
+that have no part, scales at any address; and gradients by differences."""
 import pytest
 import torch
 
 import dequant_gemv_nf4_amd as nf4
 import grad_differences
 from mx_reference import values
-from test_gpu_fused import ACTS, BF, DEV, F32, inside, loss_reference, matrix, rand, run_moe
+from test_gpu_fused import (ACTS, BF, DEV, F32, inside, linear_reference, loss_reference, matrix, moe_reference,
+                            rand, run_moe)
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +96,110 @@ def test_gradient_against_differences(act, m, n, k):
     assert grad_differences.check_dbias(act, z, dy, db) == 0
     assert grad_differences.check_dx(dz, v, dx) == 0
     assert grad_differences.check_whole(act, exact, dy, v, dx) == 0
+
+
+@pytest.mark.parametrize("m,n,k", [(65, 32000, 256), (2, 5001, 96), (2100, 40003, 64)])
+def test_losses_with_and_without_gradient(m, n, k):
+    """One call with the gradient and one without, which takes the vocabulary in fewer pieces
+    (the last size: two and one): both within the reference's bounds."""
+    codes, scales = matrix(n, k, 1)
+    x = rand((m, k), 2)
+    targets = torch.arange(m, device=DEV) * 97 % n
+    targets[::9] = -1
+    loss, lse, _ = nf4.mx_cross_entropy(codes, scales, x, targets, torch.ones(m, device=DEV))
+    alone, lse_alone = nf4.mx_cross_entropy(codes, scales, x, targets)
+    want = loss_reference(codes, scales, x, targets, None)
+    for a, b in ((loss, lse), (alone, lse_alone)):
+        inside(a, want[0], want[1], "loss")
+        inside(b, want[2], want[3], "lse")
+
+
+# few rows an expert with 16 and with 64 columns a workgroup of the second product, with and
+# without parts that meet; the most tokens of that form, whose sums take 128 KB of LDS; tiles
+FORMS = [(3, 2, 8, 256, 320), (4, 2, 8, 4096, 7168), (5, 1, 4, 4160, 544), (64, 1, 16, 4096, 1536),
+         (61, 2, 32, 2080, 2080), (64, 2, 4, 512, 160)]
+
+
+@pytest.mark.parametrize("t,k,e,h,i", FORMS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_moe_forms_in_place(t, k, e, h, i, dtype):
+    """Every form with a residual, which may be the output itself."""
+    m1, m2, x, experts, weights, out = run_moe(t, k, e, h, i, residual=True, dtype=dtype, seed=h)
+    r = rand((t, h), h + 6, dtype)
+    ws = torch.empty(nf4.moe_mlp_workspace_bytes(e, h, i, t, k), dtype=torch.uint8, device=DEV)
+    nf4.nf4_moe_mlp(*m1, *m2, x, experts, weights, r, residual=r, workspace=ws)
+    assert torch.equal(r, out)
+
+
+@pytest.mark.parametrize("t,k,e,h,i", FORMS)
+def test_moe_values_that_have_no_part(t, k, e, h, i):
+    """NaN in the weights of slots without an expert, and in tokens without any slot."""
+    m1, m2 = matrix(2 * i, h, 1, lead=(e,)), matrix(h, i, 2, lead=(e,))
+    x, weights = rand((t, h), 3), rand((t, k + 1), 4, F32)
+    experts = torch.arange(t * (k + 1), device=DEV).reshape(t, k + 1) * 5 % e
+    experts[:, k] = -1
+    experts[0] = e
+    weights[:, k] = float("nan")
+    weights[0] = float("inf")
+    x[0] = float("nan")
+    out = nf4.moe_mlp(*m1, *m2, x, experts, weights)
+    want = nf4.moe_mlp(*m1, *m2, torch.where(torch.isnan(x), 0, x).to(BF), experts,
+                       torch.where(torch.isfinite(weights), weights, 0))
+    assert torch.equal(out, want) and bool(torch.isfinite(out).all()) and bool((out[0] == 0).all())
+
+
+def test_loss_gradients_of_ignored_rows_have_no_part():
+    codes, scales = matrix(3001, 96, 1)
+    x = rand((20, 96), 2)
+    targets = torch.arange(20, device=DEV) * 31
+    targets[::3], targets[1] = -100, 5000
+    dloss = rand((20,), 3, F32)
+    want = nf4.mx_cross_entropy(codes, scales, x, targets, dloss)
+    out = (targets < 0) | (targets >= 3001)
+    dloss[out], x[out] = float("nan"), float("inf")
+    got = nf4.mx_cross_entropy(codes, scales, x, targets, dloss)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    assert bool((got[0][out] == 0).all()) and bool((got[2][out] == 0).all())
+
+
+def shifted(scales, by):
+    """The same scale bytes `by` bytes off a multiple of 16."""
+    buf = torch.zeros(scales.numel() + 16, dtype=torch.uint8, device=DEV)
+    buf[by:by + scales.numel()] = scales.reshape(-1)
+    return buf[by:by + scales.numel()].view(scales.shape)
+
+
+@pytest.mark.parametrize("by", [1, 2, 7])
+@pytest.mark.parametrize("m", [1, 4, 20, 100])
+def test_scales_and_biases_anywhere(m, by):
+    """Scales have no alignment, a bias that of its type: within the bounds at any address."""
+    n, k = 1040, 256
+    codes, scales = matrix(n, k, 1)
+    s = shifted(scales, by)
+    x = rand((m, k), 2)
+    for dtype in (BF, F32):
+        bias = rand((n + 3,), 3, dtype)[3:]
+        for act in ("silu", "swiglu"):
+            y, z = nf4.mx_linear(codes, s, x, bias=bias, act=act, keep_z=True)
+            want = linear_reference(codes, scales, x, bias, act, None, BF)
+            inside(y, want[0], want[1], "Y")
+            inside(z, want[2], want[3], "Z")
+    dy = rand((m, n), 4)
+    dx = nf4.mx_linear_grad(codes, s, dy, out_dtype=F32)[0]
+    v = values(codes, scales)
+    inside(dx, dy.double() @ v, (n + 40) * 2.0 ** -24 * (dy.double().abs() @ v.abs()) + 1e-30, "dX")
+    targets = torch.arange(m, device=DEV) * 7
+    loss, lse, dx = nf4.mx_cross_entropy(codes, s, x, targets, torch.ones(m, device=DEV), out_dtype=F32)
+    want = loss_reference(codes, scales, x, targets, torch.ones(m, device=DEV))
+    inside(lse, want[2], want[3], "lse")
+    inside(loss, want[0], want[1], "loss")
+    inside(dx, want[4], want[5] + 1e-36, "dX")
+
+
+@pytest.mark.parametrize("by", [1, 2, 7])
+@pytest.mark.parametrize("t,k,e,h,i", FORMS)
+def test_expert_scales_anywhere(t, k, e, h, i, by):
+    m1, m2, x, experts, weights, _ = run_moe(t, k, e, h, i, dtype=F32, seed=by)
+    out = nf4.moe_mlp(m1[0], shifted(m1[1], by), m2[0], shifted(m2[1], by), x, experts, weights, out_dtype=F32)
+    want, tol = moe_reference(m1, m2, x, experts, weights, "swiglu", None, F32)
+    inside(out, want, tol, "experts")
