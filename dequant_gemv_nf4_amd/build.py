@@ -29,7 +29,7 @@ HASHED = ["include/nf4.h"] + ["dequant_gemv_nf4_amd/csrc/" + f for f in
                                "pack.hip", "gemv.hip", "gemm_mfma.hip", "gemm_prefill.hip",
                                "embed.hip", "ring.hip", "nf4_check.h", "mx_device.h",
                                "mx_pack.hip", "mx_gemm.hip", "mx_packed.hip", "mx_grad.hip",
-                               "moe.hip", "mx_product.h", "mx_act.h", "mx_grad.h",
+                               "moe.hip", "mx_product.h", "mx_act.h", "mx_plan.h", "mx_grad.h",
                                "mx_linear.hip", "mx_loss.hip", "moe_units.h", "moe_mlp.hip")]
 BUILD_INFO = os.path.join(HERE, "build_info.json")
 

@@ -10,6 +10,7 @@
 // tiles of a lane are 8 consecutive outputs.
 #include "mx_act.h"
 #include "mx_grad.h"
+#include "mx_plan.h"
 
 namespace nf4 {
 namespace mx {
@@ -348,65 +349,7 @@ static int launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
 }
 
 // ------------------------------------------------- sums shared out over workgroups ----
-// A dense gradient has few tiles where rows are few, so the n may be shared out over the
-// workgroups of a tile: parts of the sum in fp32, added in order by whoever takes them.
-struct DensePlan {
-  int mf, wv, kg, splits;
-};
-// Tile and splits by an estimate of the time.  Workgroups go to the XCDs in whole groups of
-// row tiles (make_grid), 32 CUs each, two workgroups of 256 threads or one of 512 at once a
-// CU; a workgroup takes a time for every stage of 64 n of its K-groups, and two together
-// less than twice that.  `one`, `two`, kFill (stages' worth of start and end) and the cost of
-// the parts (us, and us a MB) are fitted to 1090 measurements, 43 sizes of 1 to 4096 rows
-// each with all tiles and up to 32 splits, and the plan so found is the fastest measured or
-// within 1 % at all but four of the small ones (4-6 %).  Measured, us with the sum of the
-// parts, M x N x K, taken (splits), and others:
-//    16 x 28672 x 4096    16 x 256, two K-groups (16)   21   32 x 256 (16): 24
-//    77 x 13824 x 5120    32 x 256, two K-groups (8)    31   64 x 512 (12): 35
-//   200 x 19360 x 4992    64 x 512, two K-groups (6)    64   32 x 256 (2): 100, (1): 197
-//   512 x 4096 x 4096     32 x 256, two K-groups (1)    29   64 x 512, two K-groups (4): 42
-//  1000 x 13824 x 5120    64 x 512 (3)                 150   two K-groups (1): 173
-//  2048 x 4096 x 4096     64 x 512, two K-groups (1)    65   64 x 512 (2): 94
-//  2048 x 28672 x 4096    64 x 512, two K-groups (1)   392   64 x 512 (2): 428
-static DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
-  struct Tile {
-    DensePlan plan;
-    int row_shift, col_shift;  // log2 of the tile
-    float one, two;            // us a stage of one workgroup on a CU, of two
-  };
-  static constexpr Tile kTiles[] = {{{1, 2, 2, 1}, 4, 8, 0.65f, 1.12f},
-                                    {{2, 2, 2, 1}, 5, 8, 0.72f, 1.13f},
-                                    {{4, 4, 1, 1}, 6, 9, 0.88f, 1.43f},
-                                    {{4, 4, 2, 1}, 6, 9, 1.5f, 3.f}};
-  static constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32};
-  constexpr float kFill = 2.35f, kParts = 4.5f, kPartsMb = 0.43f;
-  constexpr int64_t kPartsBytes = int64_t(256) << 20;
-  const int stages = (int)((N + 63) >> 6);
-  DensePlan best{};
-  float least = 0.f;
-  for (const Tile &t : kTiles) {
-    if (t.plan.mf == 1 ? M > 64 : t.plan.mf == 4 && M <= 16) continue;
-    const int64_t rows = (M + (1 << t.row_shift) - 1) >> t.row_shift;
-    const int64_t cols = (K + (1 << t.col_shift) - 1) >> t.col_shift;
-    const int64_t group = rows < 8 ? rows : 8, whole = rows < 8 ? 1 : rows >> 3, rest = rows < 8 ? 0 : rows & 7;
-    for (const int splits : kSplits) {
-      const int shares = t.plan.kg * splits;
-      // at least four stages for each share
-      if (splits > 1 && (stages < 4 * shares || splits * M * K * 4 > kPartsBytes)) break;
-      const int64_t blocks = cols * splits;
-      const int64_t a_cu = (((whole * blocks + 7) >> 3) * group + ((blocks + 7) >> 3) * rest + 31) >> 5;
-      float cost = ((float)(a_cu >> 1) * t.two + (float)(a_cu & 1) * t.one) *
-                   ((float)((stages + shares - 1) / shares) + kFill);
-      if (splits > 1) cost += kParts + kPartsMb * 4e-6f * (float)(splits * M * K);
-      if (best.mf != 0 && cost >= least) continue;
-      best = t.plan;
-      best.splits = splits;
-      least = cost;
-    }
-  }
-  return best;
-}
-
+// The tile and shares of plan_dense().
 static int launch_plan(const DensePlan &d, GradArgs &a, int out_dtype, hipStream_t s) {
   if (d.mf == 1) return launch_grad<1, 2, 2>(a, out_dtype, s);
   if (d.mf == 2) return launch_grad<2, 2, 2>(a, out_dtype, s);

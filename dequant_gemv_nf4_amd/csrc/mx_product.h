@@ -13,6 +13,7 @@
 #pragma once
 
 #include "mx_device.h"
+#include "mx_plan.h"
 #include "nf4_check.h"
 
 namespace nf4 {
@@ -577,47 +578,10 @@ struct Product {
   }
 };
 
-// The tile of a dense product with an epilogue, of more than 16 rows, by an estimate of the
-// time: the workgroups of the fullest XCD (make_grid deals out groups of row tiles) go to its
-// 32 CUs, up to `places` at once on each, where they take `full` us for 64 k of a K-group,
-// and one alone `one`; kFill is what start and epilogue cost, in such stages.  Fitted to 1200
-// measurements, 117 sizes of 17 to 4096 rows with all tiles.  The estimate's choice is 1.5 % off the
-// fastest on average (24 % at most); the rules by counts of tiles that the plain products
-// keep (so that their bits stay) 7 % (54 %).  Us, M x N x K, taken, and by the rules:
-//   96 x 128    700 x 11008 x 4096   65   128 x 256: 89 (258 tiles on 256 CUs)
-//   96 x 128    333 x 13824 x 5120   54   64 x 128: 67
-//   32 x 64     411 x 1703 x 3744    17   64 x 128: 24
-//   32 x 128    31 x 17241 x 5216    27   32 x 64, two K-groups: 31
+// The tiles of dense_tile().
 template <class P>
 static int launch_dense_tile(P &p) {
-  struct Tile {
-    int rows, col_shift, groups, places;
-    float one, full;
-  };
-  static constexpr Tile kTiles[] = {
-      {128, 8, 1, 2, 0.775f, 1.266f}, {128, 0, 1, 2, 0.67f, 0.953f},  {128, 7, 1, 2, 0.507f, 0.683f},
-      {96, 7, 1, 3, 0.489f, 0.702f},  {64, 7, 1, 2, 0.255f, 0.414f},  {32, 7, 1, 3, 0.23f, 0.415f},
-      {32, 6, 1, 2, 0.143f, 0.229f},  {32, 6, 2, 1, 0.227f, 0.227f},  {16, 6, 1, 3, 0.126f, 0.23f},
-      {16, 6, 2, 1, 0.177f, 0.177f},  {16, 5, 4, 1, 0.196f, 0.196f}};
-  constexpr float kFill = 11.6f;
-  int best = 0;
-  float least = 0.f;
-  for (int i = 0; i < 11; ++i) {
-    const Tile &t = kTiles[i];
-    const int64_t tiles = (p.a.R + t.rows - 1) / t.rows;
-    const int64_t cols = t.col_shift ? (p.a.N + (1 << t.col_shift) - 1) >> t.col_shift : (p.a.N + 191) / 192;
-    const int64_t group = tiles < 8 ? tiles : 8, whole = tiles < 8 ? 1 : tiles >> 3, rest = tiles < 8 ? 0 : tiles & 7;
-    const int64_t a_cu = (((whole * cols + 7) >> 3) * group + ((cols + 7) >> 3) * rest + 31) >> 5;
-    const int64_t turns = a_cu / t.places;
-    const int left = (int)(a_cu - turns * t.places);
-    float cost = (float)turns * t.full;
-    if (left > 0) cost += t.one + (left > 1 ? (t.full - t.one) * (float)(left - 1) / (float)(t.places - 1) : 0.f);
-    cost *= (float)p.a.K / (float)(64 * t.groups) + kFill;
-    if (i > 0 && cost >= least) continue;
-    best = i;
-    least = cost;
-  }
-  switch (best) {
+  switch (dense_tile(p.a.R, p.a.N, p.a.K)) {
     case 0: return p.template tile<8, 4, 4, 1, 2, 1>();
     case 1: return p.template tile<8, 3, 4, 1, 2, 1>();
     case 2: return p.template tile<8, 2, 4, 1, 2, 1>();

@@ -8,7 +8,7 @@ import dequant_gemv_nf4_amd as nf4
 import grad_differences
 from mx_reference import values
 from test_gpu_fused import (ACTS, BF, DEV, F32, inside, linear_reference, loss_reference, matrix, moe_reference,
-                            rand, run_moe)
+                            rand, run_grad, run_linear, run_loss, run_moe)
 
 pytestmark = pytest.mark.gpu
 
@@ -203,3 +203,25 @@ def test_expert_scales_anywhere(t, k, e, h, i, by):
     out = nf4.moe_mlp(m1[0], shifted(m1[1], by), m2[0], shifted(m2[1], by), x, experts, weights, out_dtype=F32)
     want, tol = moe_reference(m1, m2, x, experts, weights, "swiglu", None, F32)
     inside(out, want, tol, "experts")
+
+
+# Sizes of the tiles and plans that the tests of kernels and shapes leave out
+MORE_TILES = [(193, 25094, 32), (200, 26006, 128)]
+MORE_GRADIENTS = [(70, 504, 1152), (1827, 3912, 32), (33, 29608, 2816), (330, 24, 4128), (1040, 744, 3712)]
+
+
+@pytest.mark.parametrize("m,n,k", MORE_TILES)
+@pytest.mark.parametrize("act,bias", [("geglu", BF), ("silu", F32)])
+def test_more_linear_tiles(m, n, k, act, bias):
+    run_linear(m, n, k, act, bias=bias, residual=act == "silu", keep=act == "geglu", seed=k + m)
+
+
+@pytest.mark.parametrize("m,n,k", MORE_TILES)
+def test_more_loss_tiles(m, n, k):
+    run_loss(m, n, k, True, seed=k, dtype=BF)
+
+
+@pytest.mark.parametrize("m,n,k", MORE_GRADIENTS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_more_gradients(m, n, k, dtype):
+    run_grad(m, n, k, "swiglu" if n % 16 == 0 else "silu", True, dtype, seed=n)
