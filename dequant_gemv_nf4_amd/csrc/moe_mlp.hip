@@ -751,7 +751,6 @@ static MlpPlan mlp_plan(int64_t E, int64_t H, int64_t I, int64_t T, int64_t topk
 static int check_mlp(int64_t E, int64_t H, int64_t I, int act, int64_t T, int64_t topk) {
   if (E < 1 || T < 0 || topk < 1 || !known_act(act)) return NF4_EINVAL;
   if (int r = check_mx_shape(H, I)) return r;
-  if (I > NF4_MAX_K) return NF4_ERANGE;
   if (int r = check_mx_shape(is_gated(act) ? 2 * I : I, H)) return r;
   if (E > NF4_MOE_MAX_E || topk > NF4_MOE_MAX_E || T > kTokens) return NF4_ERANGE;
   return NF4_OK;

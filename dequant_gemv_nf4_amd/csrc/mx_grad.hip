@@ -295,27 +295,31 @@ __global__ void __launch_bounds__(64 * WV *KG, 2) mx_grad_kernel(GradArgs p) {
   }
 }
 
-template <int MF, int WV, int KG, bool SVEC>
+template <int MF, int WV, int KG, bool SVEC, bool PARTS>
 static int launch_grad_as(GradArgs &a, int out_dtype, hipStream_t s) {
   const int64_t blocks = (a.K + 128 * WV - 1) / (128 * WV);
   a.grid = make_grid(slots_for(a.R, a.E, a.offsets != nullptr, 16 * MF), blocks * a.splits, 8);
   const int64_t n = grid_size(a.grid);
   if (n * 64 * WV * KG >= (int64_t(1) << 32)) return NF4_ERANGE;
   const dim3 grid((unsigned)n), threads(64 * WV * KG);
-  if (a.ld)
-    hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, float, true>), grid, threads, 0, s, a);
-  else if (out_dtype == NF4_F32)
+  if constexpr (PARTS)
+    if (a.ld) {
+      hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, float, true>), grid, threads, 0, s, a);
+      return launch_status(hipGetLastError());
+    }
+  if (out_dtype == NF4_F32)
     hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, float, false>), grid, threads, 0, s, a);
   else
     hipLaunchKernelGGL((mx_grad_kernel<MF, WV, KG, SVEC, uint16_t, false>), grid, threads, 0, s, a);
   return launch_status(hipGetLastError());
 }
 
-template <int MF, int WV, int KG>
+// PARTS: also the form whose sums are shared out (a.ld is given)
+template <int MF, int WV, int KG, bool PARTS = false>
 static int launch_grad(GradArgs &a, int out_dtype, hipStream_t s) {
   if (a.K % 128 == 0 && aligned_to(a.scales, 4))
-    return launch_grad_as<MF, WV, KG, true>(a, out_dtype, s);
-  return launch_grad_as<MF, WV, KG, false>(a, out_dtype, s);
+    return launch_grad_as<MF, WV, KG, true, PARTS>(a, out_dtype, s);
+  return launch_grad_as<MF, WV, KG, false, PARTS>(a, out_dtype, s);
 }
 
 // The largest tile that is not mostly empty and gives every CU work, with N shared out
@@ -351,9 +355,9 @@ static int launch_rows_grad(GradArgs &a, int out_dtype, hipStream_t s) {
 // ------------------------------------------------- sums shared out over workgroups ----
 // The tile and shares of plan_dense().
 static int launch_plan(const DensePlan &d, GradArgs &a, int out_dtype, hipStream_t s) {
-  if (d.mf == 1) return launch_grad<1, 2, 2>(a, out_dtype, s);
-  if (d.mf == 2) return launch_grad<2, 2, 2>(a, out_dtype, s);
-  return d.kg == 1 ? launch_grad<4, 4, 1>(a, out_dtype, s) : launch_grad<4, 4, 2>(a, out_dtype, s);
+  if (d.mf == 1) return launch_grad<1, 2, 2, true>(a, out_dtype, s);
+  if (d.mf == 2) return launch_grad<2, 2, 2, true>(a, out_dtype, s);
+  return d.kg == 1 ? launch_grad<4, 4, 1, true>(a, out_dtype, s) : launch_grad<4, 4, 2, true>(a, out_dtype, s);
 }
 
 int grad_splits(int64_t M, int64_t N, int64_t K) { return plan_dense(M, N, K).splits; }
@@ -383,11 +387,11 @@ __global__ void __launch_bounds__(256)
 // its workgroup's; the sums are added in one order.
 // Bound by memory: 2048 rows of 28672, gated, 61 us (4.8 TB/s); 77 rows of 13824 with the column
 // sums 5-6, mostly start and the sums' way through LDS.
-template <int LANES, bool GATED>
+template <bool GATED>
 __global__ void __launch_bounds__(1024)
     mx_act_grad_kernel(const uint16_t *__restrict__ dY, const uint16_t *__restrict__ Z, int64_t M, int N,
                        int act, int64_t rows_wg, uint16_t *__restrict__ dZ, float *__restrict__ dbias) {
-  constexpr int W = GATED ? 8 : 4;
+  constexpr int W = GATED ? 8 : 4, LANES = 16;
   __shared__ float part[1024 * W];
   const int cols = GATED ? N >> 1 : N;
   const int c = threadIdx.x % LANES, y = threadIdx.x / LANES, ny = 1024 / LANES;
@@ -470,9 +474,9 @@ static int launch_act_grad(const uint16_t *dY, const uint16_t *Z, int64_t M, int
   const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)used);
   float *const to = dbias && used > 1 ? sums : dbias;
   if (gated)
-    hipLaunchKernelGGL((mx_act_grad_kernel<16, true>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ, to);
+    hipLaunchKernelGGL((mx_act_grad_kernel<true>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ, to);
   else
-    hipLaunchKernelGGL((mx_act_grad_kernel<16, false>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ, to);
+    hipLaunchKernelGGL((mx_act_grad_kernel<false>), grid, dim3(1024), 0, s, dY, Z, M, (int)N, act, rows, dZ, to);
   if (int r = launch_status(hipGetLastError())) return r;
   return dbias && used > 1 ? launch_parts(sums, (int)used, N, dbias, NF4_F32, s) : NF4_OK;
 }

@@ -1,13 +1,16 @@
 """Which kernels the sizes of the fused operators' GPU tests reach, on the host: every tile of
 the dense products and of the gradients, whole and in parts, with whole words of scales and
-without, so that a change of a constant that makes the tests miss one fails here."""
+without, so that a change of a constant that makes the tests miss one fails here; and that no
+kernel is compiled that none of them reaches."""
 import itertools
 import os
 import random
+import re
 import shutil
 
 import pytest
 
+import dequant_gemv_nf4_amd as nf4
 import test_gpu_fused as fused
 import test_gpu_fused_edges as edges
 from test_sanitizers import CSRC, HERE, _run
@@ -70,3 +73,20 @@ def test_plans_hold_over_the_whole_range(plans):
         assert 0 <= tile < len(DENSE) and (mf, wv, kg) in GRAD and splits >= 1
         if splits > 1:
             assert splits * m * k * 4 <= 1 << 28 and (n + 63) // 64 >= 4 * kg * splits
+
+
+def kernels(name):
+    """The template arguments of every kernel `name` of the library."""
+    nm = shutil.which("nm")
+    if nm is None or not os.path.exists(nf4.lib_path()):
+        pytest.skip("no nm, or no library")
+    rc, out = _run([nm, "-C", nf4.lib_path()])
+    assert rc == 0, out
+    return [tuple(a.strip() for a in m.split(",")) for m in re.findall(rf"__device_stub__{name}<([^>]*)>", out)]
+
+
+def test_no_gradient_kernel_is_out_of_reach():
+    """Sums in parts are compiled for the tiles of plan_dense() and no others."""
+    found = {(tuple(map(int, k[:3])), k[3]) for k in kernels("mx_grad_kernel") if k[5] == "true"}
+    assert found == set(itertools.product(GRAD, ("true", "false")))
+    assert sorted(kernels("mx_act_grad_kernel")) == [("false",), ("true",)]
