@@ -5,8 +5,10 @@
 // The tokens are not sorted beforehand: every workgroup makes for each expert the mask of
 // its tokens (at most 64) in LDS.  A pair (token, expert) is one row, whose weight is the
 // sum over the token's slots with that expert; rows are numbered by expert, then token.
-// The first kernel writes act(W1 x) times the row's weight, in bf16 (one rounding, as
-// between two layers); the second one's sums over all its rows are then the output.
+// The first kernel writes act(W1 x) times the row's weight, in bf16, which is what the second
+// one's matrix instructions take (one rounding, as between two layers: out in bf16 is 2.4e-3 of
+// its norm off where one rounding at the end leaves 1.7e-3); the second one's sums over all its
+// rows are then the output.
 #include "moe_units.h"
 #include "mx_act.h"
 #include "mx_product.h"
@@ -278,8 +280,8 @@ __device__ __forceinline__ int count_tiles(const Routing &r, const Masks &masks)
 }
 
 // Bound by memory, and by the 8 us that it takes to route, to fill and to end: experts of 28672
-// x 4096, 16 rows of 8 experts each 91 us (5.5 TB/s), two experts of one token 31 (4.0), 19 x 8
-// slots of 128 experts of 1536 x 2048 37.  With static shares of the tiles that there could
+// x 4096, 17 tokens with 2 of 8 91-100 us (5.0-5.5 TB/s), 16 rows of each of 8 108-112, two
+// experts of one token 31 (4.0), 19 x 8 slots of 128 experts of 1536 x 2048 37.  With static shares of the tiles that there could
 // be, empty ones among them, the first took 126; weights asked for one block ahead where
 // the compiler moved the loads down to their use, 29 of the two experts' became 33.
 // LONG: more than one pass.  (Compiled in: with loads of X behind a branch, the products
@@ -394,9 +396,9 @@ __global__ void __launch_bounds__(512)
 // unit is a range of an expert's I; the units go in turn to the waves of the `splits`
 // workgroups that share the columns, and a wave adds its units, in order, into sums of its
 // own in LDS.
-// Bound by memory (rows' pieces of 256 bytes a wave: 4.9 TB/s) and 7 us of start, fill and end:
-// experts of 4096 x 14336, 16 rows of 8 59 us, two experts of one token 22-23; about 90 of 128 of
-// 2048 x 768 28.  (Built and slower: the items of the first product with a last workgroup
+// Bound by memory (rows' pieces of 256 bytes a wave: 4.2 TB/s) and 7 us of start, fill and end:
+// experts of 4096 x 14336, 17 tokens with 2 of 8 60-63 us, 16 rows of each of 8 78-81, two experts
+// of one token 22-26; about 90 of 128 of 2048 x 768 28.  (Built and slower: the items of the first product with a last workgroup
 // that adds up, 70, 24 and 33, since few workgroups are last for all columns; the sums
 // written back by a fence of the whole cache, 76, 23 and 62.)
 template <int G, bool SVEC, typename OUT>
@@ -607,6 +609,8 @@ constexpr int kFewWaves = 8;  // of a workgroup of the first product of few rows
 // 8 of 64 experts of 7168 x 2048 59 and 47 (one token), of 128 of 6144 x 1024 327 and 253 (32), 4
 // of 32 of 5120 x 1536 96 and 77 (8); 1 of 16 of 5120 x 8192 129 and 137 (8); but one of 5120 x
 // 2048, one token, 18 and 26.
+// The rule does not see I: where that is as small as 768 the tiles would be the faster ones from
+// 3.8 rows an expert on, by 8 to 13 %, and 5120 x 8192 is on its slower side by 6 %.
 static bool few_rows(int64_t T, int64_t topk, int64_t E, int64_t H) {
   if (H > kFewWaves * kRange && T * (topk < E ? topk : E) >= 8) return false;
   return T * topk <= 5 * E || T <= 16;

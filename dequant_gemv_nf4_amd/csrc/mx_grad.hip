@@ -25,7 +25,7 @@ struct GradArgs {
   int E, N, K;
   Grid grid;
   // partial sums (PART): rows of dY are ld values apart, zero from column N up to the next
-  // multiple of 64; split i of the n's goes to dX + i R K in fp32, added to what is there times
+  // multiple of 8; split i of the n's goes to dX + i R K in fp32, added to what is there times
   // rescale[row] if that is given.
   int64_t ld;
   int splits;
@@ -383,9 +383,11 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------- in front of the sums ----
 // dZ = dY f'(Z) (gated: dY z_u f'(z_g) and dY f(z_g)) in bf16, and its column sums from the
-// unrounded values.  A thread has four columns (of both halves, gated) and every 64th row of
+// unrounded values.  bf16 since that is what the matrix cores take: dZ in two halves of 8 bits
+// each would double their work, twice 380 us of 440 at 2048 x 28672 x 4096.  So dX (in bf16) is
+// 2.3e-3 of its norm off where one rounding at the end leaves 1.7e-3.  A thread has four columns (of both halves, gated) and every 64th row of
 // its workgroup's; the sums are added in one order.
-// Bound by memory: 2048 rows of 28672, gated, 61 us (4.8 TB/s); 77 rows of 13824 with the column
+// Bound by memory: 2048 rows of 28672, gated, 62-64 us (4.6-4.7 TB/s); 77 rows of 13824 with the column
 // sums 5-6, mostly start and the sums' way through LDS.
 template <bool GATED>
 __global__ void __launch_bounds__(1024)

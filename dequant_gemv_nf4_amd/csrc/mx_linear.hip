@@ -4,10 +4,12 @@
 // or, gated, Y[m][i] = act(z[m][i]) z[m][N/2 + i] + residual[m][i].
 // The sums are those of mx_product.h.  A gated product takes the rows of both halves in
 // turn, so that gate and gated value are neighbouring columns of one workgroup.
-// Bound as the plain products are, the epilogue hides behind another workgroup's products:
-// 28672 x 4096, gated, M = 1: 14.2 us (4.4 TB/s, without: 13.3); M = 1021 with z kept: 190-200
-// (1.2-1.26 PFLOP/s); 4096 x 4096 with residual, M = 1: 5.4; 333 x 13824 x 5120 with bias and
-// gelu in fp32: 62 (0.76 PFLOP/s: 432 tiles of 96 x 128, of which the chip holds 512).
+// Bound as the plain products are, the epilogue hides behind another workgroup's products.
+// Us on six cards, from the caches and (in brackets) with weights from memory: 28672 x 4096,
+// gated, M = 1: 14.3 (16.7, without the gate 13.9); M = 1021 with z kept: 197-210 (208-218;
+// 1.1-1.22 PFLOP/s); 4096 x 4096 with residual, M = 1: 5.7 (5.8, without 4.9); 333 x 13824 x
+// 5120 with bias and gelu in fp32: 60-65 (63-68; 0.7-0.78 PFLOP/s: 432 tiles of 96 x 128, of
+// which the chip holds 512).
 #include "mx_act.h"
 #include "mx_product.h"
 
@@ -118,7 +120,8 @@ struct LinearOut {
       const int n = min(rows, t.rows - m0) * quads;
       const auto first = [&](int r) __attribute__((always_inline)) { return PAIRS ? (n0 + r) >> 1 : n0 + r; };
       // a thread's columns are the same in all rows, but in tiles of 192: the bias is read once
-      // (1021 x 28672 x 4096, gated, with bias 227 us read for each row, 212 so, as without one)
+      // (1021 x 28672 x 4096, gated, with bias, on one card: 227 us read for each row, 212 so;
+      // 194-211 on four others, 193-209 without bias)
       constexpr bool kFixed = kThreads % quads == 0;
       Bias b = bias_of(p, first((int)threadIdx.x % quads * W));
 #pragma unroll 1

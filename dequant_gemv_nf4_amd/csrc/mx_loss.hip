@@ -11,9 +11,10 @@
 // The vocabulary goes in pieces.  Of each piece
 //  1. the product's tiles (mx_product.h) take exp2(l log2(e) - c) of their logits, c a whole
 //     number, at least the strip's largest exponent and the row's so far; the strip's c and
-//     sum stay, and for the gradient the values, at most 1, in bf16 (so each has its full
-//     relative precision however far below the row's maximum its strip lies); the target's
-//     is left out of both, its logit is kept;
+//     sum stay, and for the gradient the values, at most 1, in bf16, which is what the matrix
+//     cores take (so each has its full relative precision however far below the row's maximum
+//     its strip lies, and the gradient in bf16 is as near to 64 bits as one of fp32 values:
+//     1.6e-3 of its norm); the target's is left out of both, its logit is kept;
 //  2. a row's strips meet in the row's new c and sum; strips with a smaller c are moved to
 //     it by a subtraction in the exponents of their values;
 //  3. the values' product with the piece's matrix (mx_grad.hip) is added to the row's sum
@@ -22,10 +23,12 @@
 // over them takes 6.  Last, the sums are divided by the row's, the target's row is taken
 // off, and dloss applied.
 // Bound by the products (the exponentials run beside another workgroup's matrix
-// instructions).  Of 128256 x 4096: 1000 rows 750-780 us (1.35-1.4 PFLOP/s); 2047 rows with the
-// gradient, four pieces, 3.4-3.5 ms (1.23-1.26): 390-410 us a piece the logits, 390-450 their
-// product back, 9 the join, 13-17 moving strips (most of it in the first piece, where the
-// maximum is found).  32000 x 4096, 5 rows: 14.5 (4.8 TB/s) and 3.9.
+// instructions).  Us of 128256 x 4096, on six cards: 1000 rows 757-811 (1.3-1.39 PFLOP/s; up to
+// 832 in a trace); 2047 rows with the gradient, four pieces, 3380-3640 (1.18-1.27): 390-410 a
+// piece the logits, 413-450 their product back, 9 the join, 13-17 moving strips (most of it in
+// the first piece, where the maximum is found).  With the gradient, few rows, weights from
+// memory: 1 row 150, 8 157, 64 195-209 (without 99), 200 460-485 (without 214-230); of 32000 x
+// 4096 51, 50, 74 and 145.  32000 x 4096, 5 rows: 13.5-14.5 (4.8-5.1 TB/s) and 4-5.
 #include "mx_grad.h"
 #include "mx_product.h"
 
@@ -42,7 +45,7 @@ struct Strip {
 // Takes a tile's logits: strips of the 16 NF columns of a wave.
 struct LossOut {
   static constexpr bool kPairs = false, kPlain = false;
-  const int64_t *targets;  // of the rows, less the piece's first column
+  const int64_t *targets;  // of the rows
   int64_t first;           // the piece's first column
   const float *c;          // the rows' so far, or null
   float *target_logit;
@@ -118,6 +121,9 @@ struct LossProduct : Product<SortedRows, LossOut, false, true> {
     strip = 16 * NF;
     return this->Product::template tile<MF, NF, WV, KS, KW, KG>();
   }
+  // Up to two rows (four of a small head), where the plain product takes its row kernel.  Us,
+  // one row, weights from memory, against one K-group, which five rows take: 32000 x 4096 22-24
+  // and 21, 128256 x 4096 75 and 69, 50257 x 1600 28 and 21.
   template <int TR>
   int gemv() {
     return tile<1, 1, 4, 4, 4, 2>();

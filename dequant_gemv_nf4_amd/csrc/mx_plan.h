@@ -17,13 +17,16 @@ inline int64_t workgroups_a_cu(int64_t tiles, int64_t cols) {
 // The tile of a dense product with an epilogue, of more than 16 rows, by an estimate of the
 // time: a CU takes up to `places` workgroups at once, which take `full` us for 64 k of a
 // K-group, and one alone `one`; kFill is what start and epilogue cost, in such stages.  Fitted to 1200
-// measurements, 117 sizes of 17 to 4096 rows with all tiles.  The estimate's choice is 1.5 % off the
-// fastest on average (24 % at most); the rules by counts of tiles that the plain products
-// keep (so that their bits stay) 7 % (54 %).  Us, M x N x K, taken, and by the rules:
-//   96 x 128    700 x 11008 x 4096   65   128 x 256: 89 (258 tiles on 256 CUs)
-//   96 x 128    333 x 13824 x 5120   54   64 x 128: 67
-//   32 x 64     411 x 1703 x 3744    17   64 x 128: 24
-//   32 x 128    31 x 17241 x 5216    27   32 x 64, two K-groups: 31
+// measurements of mx_linear, 117 sizes of 17 to 4096 rows with all tiles.  The estimate's choice is
+// 1.5 % off the fastest on average (24 % at most); the rules by counts of tiles that the plain
+// products keep (so that their bits stay) 7 % (54 %).  The loss takes it, too: over 28 sizes of
+// 24 to 2047 rows of heads of 32000 x 4096, 50257 x 1600 and 128256 x 4096 it is 1.2 % off (12 %
+// at most, 1000 x 50257 x 1600: 96 x 128 174 us, 128 x 256 155).
+// Us on four cards, weights from memory, M x N x K with a bias, taken, and others:
+//   96 x 128    700 x 11008 x 4096   65-68   128 x 256: 95-99 (258 tiles on 256 CUs)
+//   96 x 128    333 x 13824 x 5120   57-62   64 x 128: 64-65
+//   32 x 64     411 x 1703 x 3744       17   64 x 128: 25
+//   32 x 64     31 x 17241 x 5216    30-31   32 x 128: 35; two K-groups: 36
 constexpr int kDenseTiles = 11;
 inline int dense_tile(int64_t M, int64_t N, int64_t K) {
   struct Tile {
@@ -65,14 +68,14 @@ struct DensePlan {
 // the parts (us, and us a MB) are fitted to 1090 measurements, 43 sizes of 1 to 4096 rows
 // each with all tiles and up to 32 splits, and the plan so found is the fastest measured or
 // within 1 % at all but four of the small ones (4-6 %).  Measured, us with the sum of the
-// parts, M x N x K, taken (splits), and others:
-//    16 x 28672 x 4096    16 x 256, two K-groups (16)   21   32 x 256 (16): 24
-//    77 x 13824 x 5120    32 x 256, two K-groups (8)    31   64 x 512 (12): 35
-//   200 x 19360 x 4992    64 x 512, two K-groups (6)    64   32 x 256 (2): 100, (1): 197
-//   512 x 4096 x 4096     32 x 256, two K-groups (1)    29   64 x 512, two K-groups (4): 42
-//  1000 x 13824 x 5120    64 x 512 (3)                 150   two K-groups (1): 173
-//  2048 x 4096 x 4096     64 x 512, two K-groups (1)    65   64 x 512 (2): 94
-//  2048 x 28672 x 4096    64 x 512, two K-groups (1)   392   64 x 512 (2): 428
+// parts, weights from memory, on four cards, M x N x K, taken (splits), and others:
+//    16 x 28672 x 4096    16 x 256, two K-groups (16)     22   32 x 256 (16): 22.4
+//    77 x 13824 x 5120    32 x 256, two K-groups (4)   30-31   (8): 31; 64 x 512, two (12): 34
+//   200 x 19360 x 4992    64 x 512, two K-groups (6)   64-67   32 x 256, two (2): 100, (1): 125
+//   512 x 4096 x 4096     32 x 256, two K-groups (1)   29-31   64 x 512, two (4): 42
+//  1000 x 13824 x 5120    64 x 512 (3)               148-164   two K-groups (1): 166-171
+//  2048 x 4096 x 4096     64 x 512, two K-groups (1)   62-72   64 x 512 (2): 90-93
+//  2048 x 28672 x 4096    64 x 512, two K-groups (1) 381-392   64 x 512 (2): 400-407
 inline DensePlan plan_dense(int64_t M, int64_t N, int64_t K) {
   struct Tile {
     DensePlan plan;

@@ -446,6 +446,7 @@ enum nf4_act {
  *  - bias fp32 or bf16 [N], residual of Y's shape and type, Z bf16 [M][N]: each may be
  *    NULL.  Z receives z, rounded once, which nf4_mx_linear_grad takes.  residual may be Y
  *    itself (each element is read before it is written, by the same thread).
+ * With none of act, bias, residual and Z it is nf4_mx_gemm: its kernels, bits and times.
  * z is within the products' bound (plus 2^-23 |z| for the bias), f within 2^-20 |z| of its
  * value.
  * Alignment: codes, X, Y, residual and Z 16 bytes, bias that of its type.  Errors as
